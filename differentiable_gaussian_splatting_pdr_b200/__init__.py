@@ -21,3 +21,18 @@ from .api import (  # noqa: F401
     step_host,
     workspace_bytes,
 )
+from .features import (  # noqa: F401
+    AdapterWeights,
+    adapter,
+    check_wait_error,
+    gated,
+    gated_bwd,
+    gated_fwd,
+    linear,
+    linear_bwd,
+    linear_fwd,
+    quantize_rows,
+    rms_norm,
+    rms_norm_bwd,
+    rms_norm_fwd,
+)

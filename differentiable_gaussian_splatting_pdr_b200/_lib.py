@@ -45,6 +45,19 @@ SIGNATURES = {
     "pdr_render_fwd_ex": (_i, [_vp] + [_i] * 6 + [_vp, _i, _vp, _sz, _i, _vp]),
     "pdr_render_bwd_ex": (_i, [_vp, _vp, _i] + [_i] * 6 + [_vp, _vp, _sz, _i, _vp]),
     "pdr_loss_l1_ssim": (_i, [_vp, _vp] + [_i] * 4 + [ctypes.c_float, ctypes.c_float] + [_vp] * 3 + [_sz, _vp]),
+    "pdr_linear_workspace_bytes": (_sz, [_i] * 4),
+    "pdr_linear_fwd": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _i, _vp] + [_i] * 4 + [_vp, _i, _vp, _sz, _vp]),
+    "pdr_linear_bwd_workspace_bytes": (_sz, [_i] * 6),
+    "pdr_linear_bwd": (_i, [_vp, _i, _vp, _vp, _i, _vp] + [_i] * 5 + [_vp] * 4 + [_sz, _vp]),
+    "pdr_gated_workspace_bytes": (_sz, [_i] * 4),
+    "pdr_gated_fwd": (_i, [_vp] * 3 + [_i] + [_vp] * 3 + [_i] * 4 + [_vp, _i, _vp, _sz, _vp]),
+    "pdr_gated_bwd_workspace_bytes": (_sz, [_i] * 4),
+    "pdr_gated_bwd": (_i, [_vp] * 4 + [_i] * 5 + [_vp] * 4 + [_sz, _vp]),
+    "pdr_rms_norm_fwd": (_i, [_vp, _vp, _i, _vp, _i, ctypes.c_float, _i, _i, _vp, _vp, _i, _vp, _vp]),
+    "pdr_quantize_rows": (_i, [_vp] + [_i] * 3 + [_vp] * 3),
+    "pdr_rms_norm_bwd_workspace_bytes": (_sz, [_i] * 2),
+    "pdr_rms_norm_bwd": (_i, [_vp, _vp, _i, _vp, _i, _vp, ctypes.c_float, _i, _i] + [_vp] * 3 + [_sz, _vp]),
+    "pdr_check_wait_error": (_i, [_vp]),
 }
 
 _lib = None

@@ -1,0 +1,234 @@
+// gated: h = act(x Wg^T) * (x Wu^T), and its gradients (include/pdr.h).
+//
+// Forward: one launch.  A tile's accumulator holds 128 gate columns and the
+// same 128 up columns side by side (rows of Wg and of Wu in the two halves of
+// the B tile), so that the epilogue has g and u of an element in one thread
+// and writes h alone: neither g nor u ever leaves the chip.
+//
+// Backward: g and u are formed again from x and the weights (nothing is saved
+// by the forward), and their product's epilogue turns them, with dh, into
+//   dg = dh u act'(g),   du = dh act(g),
+// rounded to x's type as operands of the three products that follow:
+//   dx = dg Wg + du Wu          one product, k running over both sources;
+//   dWg = dg^T x, dWu = du^T x  one launch, k split over the machine, fp32
+//                               partial results added in order.
+#include "gemm.cuh"
+
+namespace pdr {
+namespace {
+
+struct GatedLayout {
+    size_t x, wg, wu, dg, du, part, total;
+    long long ldk, ldf;
+    bool pack;
+    int splits;
+};
+
+bool sizes_ok(int M, int D, int F) { return M >= 0 && D >= 1 && F >= 1; }
+bool in_limits(int M, int D, int F) {
+    return M <= PDR_MAX_ROWS && D <= PDR_MAX_FEATURES && F <= PDR_MAX_FEATURES;
+}
+bool half_type(int t) { return t == PDR_F16 || t == PDR_BF16; }
+bool act_ok(int act) { return act >= PDR_ACT_NONE && act <= PDR_ACT_GELU_TANH; }
+long long round_up(long long a, long long b) { return (a + b - 1) / b * b; }
+
+GatedLayout fwd_layout(int M, int D, int F, int dtype) {
+    GatedLayout L = {};
+    const int e = dtype_bytes(dtype);
+    L.ldk = round_up(D, 16 / e);
+    L.pack = L.ldk != D;
+    if (L.pack) {
+        L.wg = align256((size_t)M * L.ldk * e);
+        L.wu = L.wg + align256((size_t)F * L.ldk * e);
+        L.total = L.wu + align256((size_t)F * L.ldk * e);
+    }
+    return L;
+}
+
+GatedLayout bwd_layout(int M, int D, int F, int dtype) {
+    GatedLayout L = fwd_layout(M, D, F, dtype);
+    L.ldf = round_up(F, 16);
+    L.dg = L.total;
+    L.du = L.dg + align256((size_t)M * L.ldf * 2);
+    L.part = L.du + align256((size_t)M * L.ldf * 2);
+    L.splits = gemm_splits(F, D, 2, M);
+    L.total = L.part;
+    if (L.splits > 1) L.total += align256((size_t)L.splits * 2 * F * D * 4);
+    return L;
+}
+
+// Rows that no TMA copy can address (not a multiple of 16 bytes long) in
+// padded copies.
+cudaError_t pack_rows(const GatedLayout &L, const void *&x, const void *&wg, const void *&wu, int M,
+                      int D, int F, int e, char *ws, cudaStream_t s) {
+    if (!L.pack) return cudaSuccess;
+    cudaError_t err = launch_pack(x, M, D, e, ws + L.x, L.ldk, s);
+    if (err == cudaSuccess) err = launch_pack(wg, F, D, e, ws + L.wg, L.ldk, s);
+    if (err == cudaSuccess) err = launch_pack(wu, F, D, e, ws + L.wu, L.ldk, s);
+    x = ws + L.x;
+    wg = ws + L.wg;
+    wu = ws + L.wu;
+    return err;
+}
+
+pdr_status done(cudaError_t e) { return e == cudaSuccess ? PDR_OK : PDR_ERR_CUDA; }
+
+}  // namespace
+}  // namespace pdr
+
+using namespace pdr;
+
+extern "C" {
+
+size_t pdr_gated_workspace_bytes(int M, int D, int F, int dtype) {
+    if (!sizes_ok(M, D, F) || !in_limits(M, D, F) || !(half_type(dtype) || dtype == PDR_E4M3)) return 0;
+    return fwd_layout(M, D, F, dtype).total;
+}
+
+pdr_status pdr_gated_fwd(const void *x, const void *w_gate, const void *w_up, int dtype,
+                         const float *x_scale, const float *gate_scale, const float *up_scale,
+                         int activation, int M, int D, int F, void *h, int h_dtype, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+    const bool fp8 = dtype == PDR_E4M3;
+    if (!sizes_ok(M, D, F) || !(half_type(dtype) || fp8) || !(half_type(h_dtype) || h_dtype == PDR_F32) ||
+        !act_ok(activation))
+        return PDR_ERR_INVALID_ARG;
+    if (!in_limits(M, D, F)) return PDR_ERR_TOO_LARGE;
+    if ((M > 0 && (!x || !h)) || !w_gate || !w_up || fp8 != (gate_scale != nullptr) ||
+        fp8 != (up_scale != nullptr) || (fp8 ? (M > 0 && !x_scale) : x_scale != nullptr))
+        return PDR_ERR_INVALID_ARG;
+    if (!aligned_to(x, 16) || !aligned_to(w_gate, 16) || !aligned_to(w_up, 16) ||
+        !aligned_to(x_scale, 4) || !aligned_to(gate_scale, 4) || !aligned_to(up_scale, 4) ||
+        !aligned_to(h, dtype_bytes(h_dtype)))
+        return PDR_ERR_INVALID_ARG;
+    const GatedLayout L = fwd_layout(M, D, F, dtype);
+    if (L.total && (!workspace || !aligned_to(workspace, 256))) return PDR_ERR_INVALID_ARG;
+    if (workspace_bytes < L.total) return PDR_ERR_WORKSPACE_TOO_SMALL;
+    if (M == 0) return PDR_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (pack_rows(L, x, w_gate, w_up, M, D, F, dtype_bytes(dtype), static_cast<char *>(workspace),
+                  s) != cudaSuccess)
+        return PDR_ERR_CUDA;
+    GemmArgs g;
+    g.mode = kDualB;
+    g.epi = kEpiGated;
+    g.dtype = dtype;
+    g.M = M;
+    g.N = F;
+    g.K[0] = D;
+    g.a[0] = {x, M, D, L.ldk};
+    g.b[0] = {w_gate, F, D, L.ldk};
+    g.b[1] = {w_up, F, D, L.ldk};
+    g.act = activation;
+    g.scale_m = x_scale;
+    g.scale_n = gate_scale;
+    g.scale_n2 = up_scale;
+    g.out = h;
+    g.out_dtype = h_dtype;
+    g.ldo = F;
+    return done(launch_gemm(g, s));
+}
+
+size_t pdr_gated_bwd_workspace_bytes(int M, int D, int F, int dtype) {
+    if (!sizes_ok(M, D, F) || !in_limits(M, D, F) || !half_type(dtype)) return 0;
+    return bwd_layout(M, D, F, dtype).total;
+}
+
+pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, const void *w_up,
+                         int dtype, int activation, int M, int D, int F, void *grad_x,
+                         void *grad_gate, void *grad_up, void *workspace, size_t workspace_bytes,
+                         void *stream) {
+    if (!sizes_ok(M, D, F) || !half_type(dtype) || !act_ok(activation)) return PDR_ERR_INVALID_ARG;
+    if (!in_limits(M, D, F)) return PDR_ERR_TOO_LARGE;
+    if ((M > 0 && (!grad || !x)) || !w_gate || !w_up || !grad_gate != !grad_up)
+        return PDR_ERR_INVALID_ARG;
+    if (!aligned_to(grad, 2) || !aligned_to(x, 16) || !aligned_to(w_gate, 16) ||
+        !aligned_to(w_up, 16) || !aligned_to(grad_x, 2) || !aligned_to(grad_gate, 2) ||
+        !aligned_to(grad_up, 2))
+        return PDR_ERR_INVALID_ARG;
+    const GatedLayout L = bwd_layout(M, D, F, dtype);
+    if (L.total && (!workspace || !aligned_to(workspace, 256))) return PDR_ERR_INVALID_ARG;
+    if (workspace_bytes < L.total) return PDR_ERR_WORKSPACE_TOO_SMALL;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (M == 0) {
+        if (grad_gate) e = cudaMemsetAsync(grad_gate, 0, (size_t)F * D * 2, s);
+        if (e == cudaSuccess && grad_up) e = cudaMemsetAsync(grad_up, 0, (size_t)F * D * 2, s);
+        return done(e);
+    }
+    if (!grad_x && !grad_gate) return PDR_OK;
+    char *ws = static_cast<char *>(workspace);
+    if (pack_rows(L, x, w_gate, w_up, M, D, F, 2, ws, s) != cudaSuccess) return PDR_ERR_CUDA;
+    const Operand ox = {x, M, D, L.ldk}, og = {w_gate, F, D, L.ldk}, ou = {w_up, F, D, L.ldk};
+    const Operand odg = {ws + L.dg, M, F, L.ldf}, odu = {ws + L.du, M, F, L.ldf};
+    {
+        GemmArgs g;
+        g.mode = kDualB;
+        g.epi = kEpiGatedBwd;
+        g.dtype = dtype;
+        g.M = M;
+        g.N = F;
+        g.K[0] = D;
+        g.a[0] = ox;
+        g.b[0] = og;
+        g.b[1] = ou;
+        g.act = activation;
+        g.in = grad;
+        g.in_dtype = dtype;
+        g.ldi = F;
+        g.out = ws + L.dg;
+        g.out2 = ws + L.du;
+        g.out_dtype = dtype;
+        g.ldo = L.ldf;
+        e = launch_gemm(g, s);
+    }
+    if (e == cudaSuccess && grad_x) {
+        GemmArgs g;
+        g.mode = kTwoSources;
+        g.dtype = dtype;
+        g.a[0] = odg;
+        g.a[1] = odu;
+        g.b[0] = og;
+        g.b[1] = ou;
+        g.b_mn = true;
+        g.M = M;
+        g.N = D;
+        g.K[0] = g.K[1] = F;
+        g.out = grad_x;
+        g.out_dtype = dtype;
+        g.ldo = D;
+        e = launch_gemm(g, s);
+    }
+    if (e == cudaSuccess && grad_gate) {
+        GemmArgs g;
+        g.mode = kBatchA;
+        g.dtype = dtype;
+        g.a[0] = odg;
+        g.a[1] = odu;
+        g.b[0] = ox;
+        g.a_mn = g.b_mn = true;
+        g.M = F;
+        g.N = D;
+        g.K[0] = M;
+        g.splits = L.splits;
+        g.ldo = D;
+        const long long n = (long long)F * D;
+        float *part = reinterpret_cast<float *>(ws + L.part);
+        if (L.splits > 1) {
+            g.out = part;
+            g.out_dtype = PDR_F32;
+            g.out_z = n;
+            g.out_split = 2 * n;
+        } else {
+            g.out = grad_gate;
+            g.out2 = grad_up;
+            g.out_dtype = dtype;
+        }
+        e = launch_gemm(g, s);
+        if (e == cudaSuccess && L.splits > 1)
+            e = launch_join(part, L.splits, 2 * n, n, grad_gate, grad_up, dtype, s);
+    }
+    return done(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,191 @@
+// Tiled matrix products on the fifth-generation tensor cores, with the
+// operators' arithmetic in their epilogues: host plan (GemmArgs), launch, and
+// the device helpers that linear.cu, gated.cu and norm.cu share.
+//
+// Every product here is  acc[m][n] = sum_k A(m, k) B(n, k)  with fp32
+// accumulators.  An operand lies in memory either "K-major" (its k are
+// contiguous: a row of x or of W) or "MN-major" (its m or n are contiguous: x
+// and dz read as the transposed factors of dW = dz^T x).
+#pragma once
+
+#include <cuda.h>
+
+#include "common.cuh"
+#include "pdr.h"
+
+namespace pdr {
+
+constexpr int kSMs = 148;
+
+// ---- activations -----------------------------------------------------------
+
+// 1 / (1 + e^-z).  e^-z overflows to infinity for very negative z: 0.
+__device__ __forceinline__ float logistic(float z) {
+    return __fdividef(1.0f, 1.0f + __expf(-z));
+}
+
+// Phi(z) = erfc(-z / sqrt 2) / 2, and e^{-z^2/2} as a by-product.  Abramowitz
+// and Stegun, Handbook of Mathematical Functions, 7.1.26: erfc(x) =
+// (a1 t + ... + a5 t^5) e^{-x^2}, t = 1 / (1 + p x), |error| <= 1.5e-7 for
+// x >= 0 -- below the rounding of every type that an activation is stored in
+// here, and small in the negative tail, where 1 + erf would cancel.
+__device__ __forceinline__ float normal_cdf(float z, float &gauss) {
+    const float x = fabsf(z) * 0.70710678118654752f;
+    gauss = __expf(-x * x);
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    float p = fmaf(1.061405429f, t, -1.453152027f);
+    p = fmaf(p, t, 1.421413741f);
+    p = fmaf(p, t, -0.284496736f);
+    p = fmaf(p, t, 0.254829592f);
+    const float half = 0.5f * p * t * gauss;  // erfc(|z| / sqrt 2) / 2
+    return z < 0.0f ? half : 1.0f - half;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+    if constexpr (ACT == PDR_ACT_RELU) return z < 0.0f ? 0.0f : z;  // NaN stays NaN
+    if constexpr (ACT == PDR_ACT_SILU) return z * logistic(z);
+    if constexpr (ACT == PDR_ACT_GELU) {
+        float e;
+        return z * normal_cdf(z, e);
+    }
+    if constexpr (ACT == PDR_ACT_GELU_TANH)  // (1 + tanh v) / 2 = logistic(2 v)
+        return z * logistic(1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.0f));
+    return z;
+}
+
+// The value (returned) and the derivative of an activation.
+template <int ACT>
+__device__ __forceinline__ float act_both(float z, float &slope) {
+    if constexpr (ACT == PDR_ACT_RELU) {
+        slope = z > 0.0f ? 1.0f : 0.0f;
+        return z < 0.0f ? 0.0f : z;
+    }
+    if constexpr (ACT == PDR_ACT_SILU) {
+        const float t = logistic(z);
+        slope = t * fmaf(z, 1.0f - t, 1.0f);
+        return z * t;
+    }
+    if constexpr (ACT == PDR_ACT_GELU) {
+        float e;
+        const float p = normal_cdf(z, e);
+        slope = fmaf(0.39894228040143268f * z, e, p);
+        return z * p;
+    }
+    if constexpr (ACT == PDR_ACT_GELU_TANH) {
+        const float t = logistic(1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.0f));
+        slope = fmaf(z * t * (1.0f - t), 1.5957691216057308f * fmaf(0.134145f * z, z, 1.0f), t);
+        return z * t;
+    }
+    slope = 1.0f;
+    return z;
+}
+
+// ---- element types ---------------------------------------------------------
+
+// Bytes of an element of a pdr_dtype.
+__host__ __device__ inline int dtype_bytes(int dtype) {
+    return dtype == PDR_F32 ? 4 : dtype == PDR_E4M3 ? 1 : 2;
+}
+
+// Two fp32 values rounded to nearest even to fp16 / bf16, as one 32-bit word.
+__device__ __forceinline__ unsigned pack2(float a, float b, int dtype) {
+    if (dtype == PDR_F16) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const unsigned *>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const unsigned *>(&h);
+}
+__device__ __forceinline__ float2 unpack2(unsigned w, int dtype) {
+    if (dtype == PDR_F16) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// 32-byte loads and stores (one full sector each; 32-byte aligned).
+__device__ __forceinline__ void load8(const void *p, unsigned (&w)[8]) {
+    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                   "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void store8(void *p, const unsigned (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// ---- host plan -------------------------------------------------------------
+
+// One operand of a product as it lies in memory: `rows` x `cols`, rows of `ld`
+// elements apart (ld and the address multiples of 16 bytes).
+struct Operand {
+    const void *p = nullptr;
+    long long rows = 0, cols = 0, ld = 0;
+};
+
+enum GemmMode {
+    kPlain = 0,      // A = a[0], B = b[0]
+    kDualB = 1,      // tile columns: first half from b[0], second half from b[1] (gated)
+    kTwoSources = 2, // k runs over a[0] b[0], then over a[1] b[1]
+    kBatchA = 3      // two products: A = a[z], B = b[0]
+};
+enum GemmEpi {
+    kEpiLinear = 0,   // out = act(acc * scales + bias) + residual
+    kEpiGated = 1,    // out = act(g) * u from the two halves of a tile's columns
+    kEpiSlope = 2,    // out = dy * act'(acc + bias), and its column sums
+    kEpiGatedBwd = 3  // out = dy * u * act'(g), out2 = dy * act(g)
+};
+
+struct GemmArgs {
+    int mode = kPlain, epi = kEpiLinear;
+    int dtype = PDR_BF16;           // of A and B (PDR_F16, PDR_BF16 or PDR_E4M3)
+    bool a_mn = false, b_mn = false;  // MN-major operands
+    Operand a[2], b[2];
+    int M = 0, N = 0;               // extent of the result (of h, in the gated modes)
+    long long K[2] = {0, 0};        // extent of k (of each source)
+    int splits = 1;                 // k split over this many tiles, fp32 results `out_split` apart
+    // epilogue
+    int act = PDR_ACT_NONE;
+    void *out = nullptr, *out2 = nullptr;  // out2: the second product's (kBatchA), or du
+    int out_dtype = PDR_F32;
+    long long ldo = 0, out_z = 0, out_split = 0;  // elements
+    const void *bias = nullptr;
+    int bias_dtype = PDR_F32;
+    const float *scale_m = nullptr, *scale_n = nullptr, *scale_n2 = nullptr;
+    const void *in = nullptr;       // residual, dy or dh: rows of ldi elements
+    int in_dtype = PDR_F32;
+    long long ldi = 0;
+    float *colsum = nullptr;        // kEpiSlope: [4 * ceil(M / 128)][N] partial column sums
+};
+
+// Columns of a tile that launch_gemm picks for a result of M x N (x nz products).
+int gemm_tile_columns(int epi, int M, int N, int nz);
+// Tiles along k that fill the machine for a weight gradient, at most `most`.
+int gemm_splits(int M, int N, int nz, long long K);
+cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s);
+// Reads (and clears) the word that a bounded wait sets when it gives up.
+cudaError_t read_wait_error(int *bits, cudaStream_t s);
+
+// ---- small kernels around the products ---------------------------------------
+
+// Rows of `cols` elements (16 bits or 8) copied to rows of `ld_to` elements.
+cudaError_t launch_pack(const void *from, long long rows, long long cols, int bytes, void *to,
+                        long long ld_to, cudaStream_t s);
+// to[i] = sum_s part[s * stride + i], i < n, rounded once to `dtype`; and
+// to2[i] the same of part + n where there is a second result.
+cudaError_t launch_join(const float *part, int splits, long long stride, long long n, void *to,
+                        void *to2, int dtype, cudaStream_t s);
+// Column sums of part[rows][cols] (rows in order within fixed groups) to `dtype`.
+cudaError_t launch_join_columns(const float *part, long long rows, long long cols, void *to,
+                                int dtype, cudaStream_t s);
+// dz = dy in `dz_dtype` (rows of ldz; null: not wanted) and partial column sums
+// of dy, one row of `colsum` for each of column_groups(M) groups of rows (null: not wanted).
+long long column_groups(long long M);
+cudaError_t launch_cast_columns(const void *dy, int dy_dtype, long long M, int N, void *dz,
+                                int dz_dtype, long long ldz, float *colsum, cudaStream_t s);
+
+inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+inline bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace pdr

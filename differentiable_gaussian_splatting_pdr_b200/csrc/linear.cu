@@ -1,0 +1,263 @@
+// linear: y = act(x W^T + b) + r, and its gradients (include/pdr.h).
+//
+// Forward: one tensor-core product over rows of x and rows of W, both
+// contiguous along k; scales, bias, activation and residual are applied to the
+// fp32 sums in the epilogue, and y is rounded once.
+//
+// Backward, with dz = dy act'(z):
+//   dz  without an activation dz is dy: read in place where its type and row
+//       length allow, else cast once; with one, z = x W^T + b is formed again
+//       and dz leaves that product's epilogue (nothing is saved by the
+//       forward: at widths up to about 1000 forming z again costs less time
+//       than writing and reading it, and no memory);
+//   db  sums of dy act'(z) in fp32 before any rounding: per 32-row group in
+//       the epilogue (or per 512 rows of dy), then over the groups in order;
+//   dx  = dz W     (W read with its k as rows: an MN-major operand);
+//   dW  = dz^T x   (both operands MN-major), k split over the machine, fp32
+//       partial results added in order: bitwise reproducible.
+// dz is rounded to x's type: it is an operand of 16-bit products, whose
+// results are rounded to that type too.
+#include "gemm.cuh"
+
+namespace pdr {
+namespace {
+
+struct LinearLayout {
+    size_t x, w, dz, colsum, part, total;
+    long long ldk, ldz, sum_rows;
+    bool pack, cast;
+    int splits;
+};
+
+bool linear_sizes(int M, int N, int K) { return M >= 0 && N >= 1 && K >= 1; }
+bool linear_in_limits(int M, int N, int K) {
+    return M <= PDR_MAX_ROWS && N <= PDR_MAX_FEATURES && K <= PDR_MAX_FEATURES;
+}
+
+long long round_up(long long a, long long b) { return (a + b - 1) / b * b; }
+
+LinearLayout fwd_layout(int M, int N, int K, int dtype) {
+    LinearLayout L = {};
+    const int e = dtype_bytes(dtype);
+    L.ldk = round_up(K, 16 / e);
+    L.pack = L.ldk != K;
+    if (L.pack) {
+        L.x = 0;
+        L.w = align256((size_t)M * L.ldk * e);
+        L.total = L.w + align256((size_t)N * L.ldk * e);
+    }
+    return L;
+}
+
+LinearLayout bwd_layout(int M, int N, int K, int dtype, int grad_dtype, int act) {
+    LinearLayout L = fwd_layout(M, N, K, dtype);
+    L.ldz = N;
+    L.cast = act != PDR_ACT_NONE || grad_dtype != dtype || N % 8 != 0;
+    L.dz = L.total;
+    if (L.cast) {
+        L.ldz = round_up(N, 16);
+        L.total += align256((size_t)M * L.ldz * 2);
+    }
+    L.sum_rows = act != PDR_ACT_NONE ? 4 * (((long long)M + 127) / 128) : column_groups(M);
+    L.colsum = L.total;
+    L.total += align256((size_t)L.sum_rows * N * 4);
+    L.splits = gemm_splits(N, K, 1, M);
+    L.part = L.total;
+    if (L.splits > 1) L.total += align256((size_t)L.splits * N * K * 4);
+    return L;
+}
+
+bool act_ok(int act) { return act >= PDR_ACT_NONE && act <= PDR_ACT_GELU_TANH; }
+bool half_type(int t) { return t == PDR_F16 || t == PDR_BF16; }
+bool float_type(int t) { return t == PDR_F32 || half_type(t); }
+
+pdr_status done(cudaError_t e) { return e == cudaSuccess ? PDR_OK : PDR_ERR_CUDA; }
+
+}  // namespace
+}  // namespace pdr
+
+using namespace pdr;
+
+extern "C" {
+
+size_t pdr_linear_workspace_bytes(int M, int N, int K, int dtype) {
+    if (!linear_sizes(M, N, K) || !linear_in_limits(M, N, K) || !(half_type(dtype) || dtype == PDR_E4M3))
+        return 0;
+    return fwd_layout(M, N, K, dtype).total;
+}
+
+pdr_status pdr_linear_fwd(const void *x, const void *weight, int dtype, const float *x_scale,
+                          const float *weight_scale, const void *bias, int bias_dtype,
+                          const void *residual, int activation, int M, int N, int K, void *y,
+                          int y_dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    const bool fp8 = dtype == PDR_E4M3;
+    if (!linear_sizes(M, N, K) || !(half_type(dtype) || fp8) || !float_type(y_dtype) ||
+        !act_ok(activation))
+        return PDR_ERR_INVALID_ARG;
+    if (!linear_in_limits(M, N, K)) return PDR_ERR_TOO_LARGE;
+    if ((M > 0 && (!x || !y)) || !weight || fp8 != (weight_scale != nullptr) ||
+        (fp8 ? (M > 0 && !x_scale) : x_scale != nullptr))
+        return PDR_ERR_INVALID_ARG;
+    if (bias && !float_type(bias_dtype)) return PDR_ERR_INVALID_ARG;
+    if (!aligned_to(x, 16) || !aligned_to(weight, 16) || !aligned_to(x_scale, 4) ||
+        !aligned_to(weight_scale, 4) || !aligned_to(y, dtype_bytes(y_dtype)) ||
+        !aligned_to(residual, dtype_bytes(y_dtype)) || !aligned_to(bias, bias ? dtype_bytes(bias_dtype) : 1))
+        return PDR_ERR_INVALID_ARG;
+    const LinearLayout L = fwd_layout(M, N, K, dtype);
+    if (L.total && (!workspace || !aligned_to(workspace, 256))) return PDR_ERR_INVALID_ARG;
+    if (workspace_bytes < L.total) return PDR_ERR_WORKSPACE_TOO_SMALL;
+    if (M == 0) return PDR_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    GemmArgs g;
+    g.dtype = dtype;
+    g.M = M;
+    g.N = N;
+    g.K[0] = K;
+    g.a[0] = {x, M, K, L.ldk};
+    g.b[0] = {weight, N, K, L.ldk};
+    if (L.pack) {
+        char *ws = static_cast<char *>(workspace);
+        const int e = dtype_bytes(dtype);
+        cudaError_t err = launch_pack(x, M, K, e, ws + L.x, L.ldk, s);
+        if (err == cudaSuccess) err = launch_pack(weight, N, K, e, ws + L.w, L.ldk, s);
+        if (err != cudaSuccess) return PDR_ERR_CUDA;
+        g.a[0].p = ws + L.x;
+        g.b[0].p = ws + L.w;
+    }
+    g.act = activation;
+    g.out = y;
+    g.out_dtype = y_dtype;
+    g.ldo = N;
+    g.bias = bias;
+    g.bias_dtype = bias_dtype;
+    g.scale_m = x_scale;
+    g.scale_n = weight_scale;
+    g.in = residual;
+    g.in_dtype = y_dtype;
+    g.ldi = N;
+    return done(launch_gemm(g, s));
+}
+
+size_t pdr_linear_bwd_workspace_bytes(int M, int N, int K, int dtype, int grad_dtype,
+                                      int activation) {
+    if (!linear_sizes(M, N, K) || !linear_in_limits(M, N, K) || !half_type(dtype) ||
+        !float_type(grad_dtype) || !act_ok(activation))
+        return 0;
+    return bwd_layout(M, N, K, dtype, grad_dtype, activation).total;
+}
+
+pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const void *weight,
+                          int dtype, const void *bias, int bias_dtype, int activation, int M, int N,
+                          int K, void *grad_x, void *grad_weight, void *grad_bias, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+    if (!linear_sizes(M, N, K) || !half_type(dtype) || !float_type(grad_dtype) || !act_ok(activation))
+        return PDR_ERR_INVALID_ARG;
+    if (!linear_in_limits(M, N, K)) return PDR_ERR_TOO_LARGE;
+    if ((M > 0 && (!grad || !x)) || !weight) return PDR_ERR_INVALID_ARG;
+    if ((bias || grad_bias) && !float_type(bias_dtype)) return PDR_ERR_INVALID_ARG;
+    const int be = bias || grad_bias ? dtype_bytes(bias_dtype) : 1;
+    if (!aligned_to(grad, 16) || !aligned_to(x, 16) || !aligned_to(weight, 16) ||
+        !aligned_to(bias, be) || !aligned_to(grad_bias, be) || !aligned_to(grad_x, 2) ||
+        !aligned_to(grad_weight, 2))
+        return PDR_ERR_INVALID_ARG;
+    const LinearLayout L = bwd_layout(M, N, K, dtype, grad_dtype, activation);
+    if (L.total && (!workspace || !aligned_to(workspace, 256))) return PDR_ERR_INVALID_ARG;
+    if (workspace_bytes < L.total) return PDR_ERR_WORKSPACE_TOO_SMALL;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (M == 0) {  // no rows: nothing to add up
+        if (grad_weight) e = cudaMemsetAsync(grad_weight, 0, (size_t)N * K * 2, s);
+        if (e == cudaSuccess && grad_bias) e = cudaMemsetAsync(grad_bias, 0, (size_t)N * be, s);
+        return done(e);
+    }
+    char *ws = static_cast<char *>(workspace);
+    const bool act = activation != PDR_ACT_NONE, products = grad_x || grad_weight;
+    if (!products && !grad_bias) return PDR_OK;
+    if (L.pack) {
+        if (act || grad_weight) {
+            e = launch_pack(x, M, K, 2, ws + L.x, L.ldk, s);
+            x = ws + L.x;
+        }
+        if (e == cudaSuccess && (act || grad_x)) {
+            e = launch_pack(weight, N, K, 2, ws + L.w, L.ldk, s);
+            weight = ws + L.w;
+        }
+        if (e != cudaSuccess) return PDR_ERR_CUDA;
+    }
+    float *colsum = grad_bias ? reinterpret_cast<float *>(ws + L.colsum) : nullptr;
+    const Operand ox = {x, M, K, L.ldk}, ow = {weight, N, K, L.ldk};
+    Operand oz = {L.cast ? ws + L.dz : grad, M, N, L.ldz};
+    if (act) {
+        GemmArgs g;
+        g.epi = kEpiSlope;
+        g.dtype = dtype;
+        g.a[0] = ox;
+        g.b[0] = ow;
+        g.M = M;
+        g.N = N;
+        g.K[0] = K;
+        g.act = activation;
+        g.bias = bias;
+        g.bias_dtype = bias_dtype;
+        g.in = grad;
+        g.in_dtype = grad_dtype;
+        g.ldi = N;
+        g.out = ws + L.dz;
+        g.out_dtype = dtype;
+        g.ldo = L.ldz;
+        g.colsum = colsum;
+        e = launch_gemm(g, s);
+    } else if ((L.cast && products) || colsum) {
+        e = launch_cast_columns(grad, grad_dtype, M, N, L.cast && products ? ws + L.dz : nullptr,
+                                dtype, L.ldz, colsum, s);
+    }
+    if (e == cudaSuccess && colsum)
+        e = launch_join_columns(colsum, L.sum_rows, N, grad_bias, bias_dtype, s);
+    if (e == cudaSuccess && grad_x) {
+        GemmArgs g;
+        g.dtype = dtype;
+        g.a[0] = oz;
+        g.b[0] = ow;
+        g.b_mn = true;
+        g.M = M;
+        g.N = K;
+        g.K[0] = N;
+        g.out = grad_x;
+        g.out_dtype = dtype;
+        g.ldo = K;
+        e = launch_gemm(g, s);
+    }
+    if (e == cudaSuccess && grad_weight) {
+        GemmArgs g;
+        g.dtype = dtype;
+        g.a[0] = oz;
+        g.b[0] = ox;
+        g.a_mn = g.b_mn = true;
+        g.M = N;
+        g.N = K;
+        g.K[0] = M;
+        g.splits = L.splits;
+        g.ldo = K;
+        if (L.splits > 1) {
+            g.out = ws + L.part;
+            g.out_dtype = PDR_F32;
+            g.out_split = (long long)N * K;
+        } else {
+            g.out = grad_weight;
+            g.out_dtype = dtype;
+        }
+        e = launch_gemm(g, s);
+        if (e == cudaSuccess && L.splits > 1)
+            e = launch_join(reinterpret_cast<float *>(ws + L.part), L.splits, (long long)N * K,
+                            (long long)N * K, grad_weight, nullptr, dtype, s);
+    }
+    return done(e);
+}
+
+pdr_status pdr_check_wait_error(void *stream) {
+    int bits = 0;
+    if (read_wait_error(&bits, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PDR_ERR_CUDA;
+    return bits ? PDR_ERR_DEVICE_TIMEOUT : PDR_OK;
+}
+
+}  // extern "C"

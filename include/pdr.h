@@ -66,7 +66,7 @@ typedef enum {
     PDR_ERR_INVALID_ARG = 1,          /* bad size, even k, null pointer, misaligned workspace */
     PDR_ERR_WORKSPACE_TOO_SMALL = 2,  /* workspace_bytes < pdr_workspace_bytes(...) */
     PDR_ERR_CUDA = 3,                 /* a CUDA runtime call or launch failed */
-    PDR_ERR_DEVICE_TIMEOUT = 4,       /* reserved: a bounded device-side wait gave up */
+    PDR_ERR_DEVICE_TIMEOUT = 4,       /* a bounded device-side wait gave up */
     PDR_ERR_INTERNAL = 5,             /* a device-side consistency check failed */
     PDR_ERR_TOO_LARGE = 6             /* sizes beyond the limits below */
 } pdr_status;
@@ -206,7 +206,12 @@ pdr_status pdr_check_device_error_noalloc(void *stream);
  * rendering"); params and grad_params stay fp32 (small, and mu feeds the
  * exact window centre).  The fp16/bf16 image of pdr_render_fwd_ex equals the
  * fp32 image of pdr_render_fwd rounded to that type. */
-typedef enum { PDR_F32 = 0, PDR_F16 = 1, PDR_BF16 = 2 } pdr_dtype;
+typedef enum {
+    PDR_F32 = 0,
+    PDR_F16 = 1,
+    PDR_BF16 = 2,
+    PDR_E4M3 = 3 /* 8 bits; operands and rows with scales only (below) */
+} pdr_dtype;
 
 /* pdr_render_fwd with the image stored as image_dtype (a pdr_dtype; the
  * image pointer aligned to its element size).  pdr_render_fwd(...) is
@@ -280,6 +285,115 @@ size_t pdr_loss_workspace_bytes(int B, int C, int H, int W);
 pdr_status pdr_loss_l1_ssim(const float *image, const float *target, int B, int C, int H,
                             int W, float lam, float data_range, float *loss, float *grad_image,
                             void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- From features to params: linear, gated feed-forward, RMS norm ------------
+ * The operators between a predictor's features and the Gaussians' parameters
+ * (reading notes, "Method": a lightweight adapter regresses them from the
+ * predictor's features), row by row over M rows (frames x Gaussians, or
+ * feature tokens), forward and backward:
+ *
+ *   linear    y = act(x W^T + b) + r
+ *   gated     h = act(x Wg^T) * (x Wu^T)
+ *   rms_norm  s = x + r,  y = s / sqrt(mean(s^2) + eps) * w
+ *
+ * The pages name the adapter and give none of its layers; these are the usual
+ * ones.  All tensors are dense and row-major, types as given by a pdr_dtype;
+ * products take 16-bit operands (PDR_F16 or PDR_BF16) or rows in 8 bits
+ * (PDR_E4M3) with one fp32 scale per row, and add up in fp32; every output is
+ * rounded once, to nearest even, from fp32.  fp32 operands are not taken: the
+ * tensor cores would round them.  Outputs are overwritten, may not overlap
+ * inputs, and are bitwise reproducible.  M = 0 is valid (gradients of weights
+ * are zero then; arrays sized by M may be NULL).
+ *
+ * Pointers: x, weights and grad 16-byte aligned in the products (TMA reads
+ * them), otherwise aligned to their element; workspaces 256-byte aligned, NULL
+ * where the needed size is 0.  Rows whose length is not a multiple of 16 bytes
+ * are first copied to the workspace in padded form.  Violations return
+ * PDR_ERR_INVALID_ARG, sizes beyond the limits PDR_ERR_TOO_LARGE, and nothing
+ * is launched then.  Streams as above.  A workspace holds nothing between
+ * calls; calls that can overlap on the GPU need workspaces of their own. */
+typedef enum {
+    PDR_ACT_NONE = 0,
+    PDR_ACT_RELU = 1,
+    PDR_ACT_SILU = 2,
+    PDR_ACT_GELU = 3,      /* z Phi(z) */
+    PDR_ACT_GELU_TANH = 4  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+} pdr_act;
+
+#define PDR_MAX_ROWS (1 << 30)
+#define PDR_MAX_FEATURES 65536       /* N, K, D and F of the products */
+#define PDR_MAX_NORM_FEATURES 16384  /* D of rms_norm and quantize_rows */
+
+/* x [M][K], weight [N][K] of `dtype`; bias [N] of bias_dtype (PDR_F32, PDR_F16
+ * or PDR_BF16) or NULL; residual [M][N] of y_dtype or NULL; y [M][N] of y_dtype
+ * (not PDR_E4M3).  x_scale [M] and weight_scale [N]: with PDR_E4M3 operands,
+ * which stand for value times scale; NULL otherwise.  Gaussian parameters
+ * straight for pdr_render_fwd: N = 5 + C, y_dtype = PDR_F32, the base
+ * parameters as residual. */
+size_t pdr_linear_workspace_bytes(int M, int N, int K, int dtype);
+pdr_status pdr_linear_fwd(const void *x, const void *weight, int dtype, const float *x_scale,
+                          const float *weight_scale, const void *bias, int bias_dtype,
+                          const void *residual, int activation, int M, int N, int K, void *y,
+                          int y_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* From grad = dL/dy [M][N] of grad_dtype: grad_x [M][K] and grad_weight [N][K]
+ * of `dtype` (16 bits), grad_bias [N] of bias_dtype; each may be NULL (not
+ * wanted).  dL/dresidual is grad itself.  The pre-activation is formed again
+ * from x, weight and bias where the activation needs it (nothing is saved by
+ * the forward); grad_bias sums unrounded fp32 values. */
+size_t pdr_linear_bwd_workspace_bytes(int M, int N, int K, int dtype, int grad_dtype,
+                                      int activation);
+pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const void *weight,
+                          int dtype, const void *bias, int bias_dtype, int activation, int M, int N,
+                          int K, void *grad_x, void *grad_weight, void *grad_bias, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* x [M][D], w_gate and w_up [F][D] of `dtype`; h [M][F] of h_dtype (not
+ * PDR_E4M3); scales as in pdr_linear_fwd, gate_scale and up_scale [F]. */
+size_t pdr_gated_workspace_bytes(int M, int D, int F, int dtype);
+pdr_status pdr_gated_fwd(const void *x, const void *w_gate, const void *w_up, int dtype,
+                         const float *x_scale, const float *gate_scale, const float *up_scale,
+                         int activation, int M, int D, int F, void *h, int h_dtype, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* From grad = dL/dh [M][F]: grad_x [M][D], grad_gate and grad_up [F][D], all of
+ * `dtype` (16 bits); grad_x, or both weight gradients, may be NULL. */
+size_t pdr_gated_bwd_workspace_bytes(int M, int D, int F, int dtype);
+pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, const void *w_up,
+                         int dtype, int activation, int M, int D, int F, void *grad_x,
+                         void *grad_gate, void *grad_up, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/* x [M][D] of `dtype` (PDR_F32, PDR_F16, PDR_BF16); residual like x or NULL;
+ * weight [D] of `dtype` or PDR_F32.  Writes sum = x + residual (NULL: not
+ * wanted; it must be NULL without a residual) and y, of `dtype` or PDR_E4M3.
+ * The norm is taken of the fp32 sum before it is rounded to `sum`.  PDR_E4M3:
+ * y stands for y * y_scale[m], y_scale[m] = max(max |row| / 448, 2^-126); a
+ * row with a NaN or an infinity has a NaN or infinite scale. */
+pdr_status pdr_rms_norm_fwd(const void *x, const void *residual, int dtype, const void *weight,
+                            int weight_dtype, float eps, int M, int D, void *sum, void *y,
+                            int y_dtype, float *y_scale, void *stream);
+
+/* The rows of x [M][D] in 8 bits as above, without a norm (weights, features). */
+pdr_status pdr_quantize_rows(const void *x, int dtype, int M, int D, void *y, float *y_scale,
+                             void *stream);
+
+/* From grad = dL/dy [M][D] and sum (the norm's input: x, or x + residual) of
+ * `dtype`, and grad_sum = dL/dsum from sum's other uses (or NULL): grad_x [M][D]
+ * of `dtype`, the gradient of x and of residual alike, and grad_weight [D] of
+ * weight_dtype; either may be NULL.  The workspace is needed for grad_weight
+ * only. */
+size_t pdr_rms_norm_bwd_workspace_bytes(int M, int D);
+pdr_status pdr_rms_norm_bwd(const void *grad, const void *sum, int dtype, const void *weight,
+                            int weight_dtype, const void *grad_sum, float eps, int M, int D,
+                            void *grad_x, void *grad_weight, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* The products' kernels bound every wait on the device; one that gives up ends
+ * the kernel with wrong results and sets a word of the current device.
+ * Synchronises `stream`, returns PDR_ERR_DEVICE_TIMEOUT if the word was set
+ * since the last call, and clears it. */
+pdr_status pdr_check_wait_error(void *stream);
 
 #ifdef __cplusplus
 }
