@@ -1,14 +1,19 @@
 // The tensor-core product kernel behind linear.cu and gated.cu.
 //
-// One persistent block per SM walks over 128 x BN tiles of the result.  A
-// block's warps have fixed parts:
-//   warp 0   copies A and B tiles to shared memory with TMA (128-byte
+// Pairs of blocks (a cluster of two SMs) walk over 256 x BN tiles of the
+// result, one persistent pair per two SMs.  Each block holds 128 rows of A, half
+// of the BN rows of B and its 128 rows of the accumulator; tcgen05.mma with
+// cta_group::2 multiplies over both blocks' shared memory.  (Single blocks with
+// 128 x 256 tiles were bound by the operands' way from L2: 7.7 TB/s at any
+// width; a pair reads a third less.)  A block's warps have fixed parts:
+//   warp 0   copies its A rows and B half to shared memory with TMA (128-byte
 //            swizzle, 64 16-bit or 128 8-bit k per stage, as many stages as
-//            fit);
-//   warp 1   issues tcgen05.mma (128 x BN x 32 bytes) into one of the
-//            accumulators in tensor memory (2 of 256 columns, 4 of fewer);
-//   warp 2   owns the tensor memory;
-//   warps 4..11 take finished accumulators to registers and run the
+//            fit).  Where all k of a tile's B half leave room for three
+//            stages of A, B stays in shared memory while the pair walks down a column
+//            of tiles, and the stages hold A alone;
+//   warp 1   owns the tensor memory, and in the first block issues the products
+//            into one of the accumulators there (2 of 256 columns, 4 of fewer);
+//   warps 4..19 take finished accumulators to registers and run the
 //            epilogue, while the next tile's products run.
 // What the four epilogues compute is in gemm.cuh (GemmEpi).
 #include <stdint.h>
@@ -24,31 +29,45 @@ constexpr int kBM = 128;              // tile rows
 constexpr int kRowBytes = 128;        // k of a stage, in bytes (the swizzle's width)
 constexpr int kABytes = kBM * kRowBytes;
 constexpr int kMaxStages = 12;
-constexpr int kThreads = 384;
-constexpr int kEpiWarp = 4;           // first epilogue warp
+constexpr int kGroups = 4, kEpiWarps = 4 * kGroups;  // epilogue warpgroups
+constexpr int kThreads = 32 * (kEpiWarps + 4);
+constexpr int kEpiRegs = 104, kOtherRegs = 64;  // per thread: 512 x 104 + 128 x 64 <= 640 x 96
+constexpr int kCopyWarp = 0, kProductWarp = 1, kEpiWarp = 4;
 constexpr int kMaxAcc = 4;            // accumulators in tensor memory
-constexpr int kChunk = 32;            // columns an epilogue warp handles at once
-constexpr int kStagePitch = 17;       // floats per row of the transposing buffer (16 columns)
-constexpr int kTransBytes = 32 * kStagePitch * 4;  // per epilogue warp
+constexpr int kChunk = 16;            // columns an epilogue warp computes at once
+constexpr int kStore = 2 * kChunk;    // columns that it stores at once
+constexpr int kMaxCols = 64;          // most columns of a tile that an epilogue warp has
+constexpr int kBufferBytes = 32 * kStore * 2;  // per epilogue warp: 32 rows of 16 floats or 32 halves
 // Tries of a bounded wait: each try sleeps in hardware for up to some
 // microseconds, so a wait gives up after seconds, far beyond any product.
 constexpr int kWaitTries = 1 << 22;
 
 __device__ int g_wait_error;  // set when a bounded wait gave up
 
+// Quotients by a divisor that is fixed for a launch, for dividends below 2^31:
+// with l = ceil(log2 d) and mul = floor(2^(31 + l) / d) + 1, n / d = (n mul) >> (31 + l).
+// (Integer divisions per tile held the products back: 5300 clocks for a tile of
+// 2048 clocks of them.)
+struct Divisor {
+    unsigned d, mul, shift;
+};
+
 struct __align__(64) GemmParams {
-    CUtensorMap a[2], b[2];
-    int mode, a_mn, b_mn, act;
-    int M, N, nm, nn, nz, splits, tiles;
+    CUtensorMap a[2], b[2], o[2];     // o: 16-bit results that TMA can store
+    int mode, a_mn, b_mn;
+    int M, N, nz, splits, tiles;
+    Divisor nm, nn;                   // tiles of 256 rows, of bcols columns
     int kb0, kb;                      // k blocks of the first source, of all
-    int bn, bcols, stages, nacc, split_cols;  // bcols: result columns of a tile
-    int b_bytes, kelems;              // B bytes of a stage, k of a stage
+    int bn, bcols, stages, nacc;      // bcols: result columns of a tile
+    int sharing;                      // epilogue groups that share a tile
+    int stationary;                   // B of a column of tiles stays in shared memory
+    int b_bytes, kelems;              // a block's B bytes, and k, of a k block
     unsigned idesc;
     unsigned long long adesc, bdesc;  // smem descriptors without the address
     int a_step, b_step;               // descriptor advance (16-byte units) of one mma
     int fp8;
     void *out, *out2;
-    int out_dtype, out_vec;
+    int out_dtype, out_vec, out_tma;
     long long ldo, out_z, out_split;
     const void *bias;
     int bias_dtype;
@@ -61,7 +80,7 @@ struct __align__(64) GemmParams {
 
 struct Barriers {
     unsigned long long full[kMaxStages], empty[kMaxStages], acc_full[kMaxAcc], acc_empty[kMaxAcc];
-    unsigned long long drain;
+    unsigned long long b_full, b_empty, drain;
     unsigned tmem;
     int abort;
 };
@@ -72,79 +91,105 @@ __device__ __forceinline__ unsigned smem_u32(const void *p) {
 __device__ __forceinline__ void bar_init(unsigned long long *b, int count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count) : "memory");
 }
-__device__ __forceinline__ void bar_arrive(unsigned long long *b) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+// The address of the same place in block `rank` of the cluster.
+__device__ __forceinline__ unsigned at_rank(unsigned addr, unsigned rank) {
+    unsigned r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
 }
-__device__ __forceinline__ void bar_expect(unsigned long long *b, unsigned bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)),
-                 "r"(bytes)
+// Arrives at a barrier of the pair (its cluster address).  Relaxed: what it
+// orders are reads of tensor memory, which tcgen05.wait::ld and the fence before
+// it have ended; a release at this scope would also wait for the warp's stores
+// to global memory (118 against 70 us for 65536 rows of 256 to 1024 gated).
+__device__ __forceinline__ void bar_arrive_at(unsigned addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// One thread of a converged warp.  The copies and products are issued under this
+// and not under a test of the lane: the compiler then knows that one thread is
+// active, and puts their operands into uniform registers without a loop over the
+// threads (which took some 100 clocks an instruction).
+__device__ __forceinline__ bool elect_one() {
+    unsigned p;
+    asm volatile(
+        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void bar_expect(unsigned bar, unsigned bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ bool bar_try(unsigned long long *b, unsigned parity) {
+__device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
     unsigned ok;
     asm volatile(
         "{\n .reg .pred p;\n"
         " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
-        : "r"(smem_u32(b)), "r"(parity)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
 }
 // Waits for a phase of a barrier, at most kWaitTries tries; false (and the
 // block's abort flag and the library's error word set) if it gave up.
-__device__ __forceinline__ bool bar_wait(unsigned long long *b, unsigned parity, int *abort) {
+__device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity, int *abort) {
     for (int i = 0; i < kWaitTries; ++i) {
-        if (bar_try(b, parity)) return true;
+        if (bar_try(bar, parity)) return true;
         if ((i & 63) == 63 && *(volatile int *)abort) return false;
     }
     *(volatile int *)abort = 1;
     atomicExch(&g_wait_error, 1);
     return false;
 }
-
-__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int x, int y,
-                                         unsigned long long *bar) {
+// The copy reports to a barrier of the first block (`bar`: its cluster address).
+__device__ __forceinline__ void tma_load(unsigned dst, const CUtensorMap *map, int x, int y,
+                                         unsigned bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
 
-__device__ __forceinline__ void mma(unsigned d, unsigned long long a, unsigned long long b,
+// One product of 32 bytes of k; the operands' descriptors in two words.
+__device__ __forceinline__ void mma(unsigned d, unsigned al, unsigned ah, unsigned bl, unsigned bh,
                                     unsigned idesc, bool acc, bool fp8) {
     if (fp8)
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"((unsigned)acc)
+            "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.u32 p, %6, 0;\n"
+            " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+            " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, p;\n}" ::"r"(d),
+            "r"(al), "r"(ah), "r"(bl), "r"(bh), "r"(idesc), "r"((unsigned)acc)
             : "memory");
     else
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"((unsigned)acc)
+            "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.u32 p, %6, 0;\n"
+            " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n}" ::"r"(d),
+            "r"(al), "r"(ah), "r"(bl), "r"(bh), "r"(idesc), "r"((unsigned)acc)
             : "memory");
 }
-__device__ __forceinline__ void mma_commit(unsigned long long *bar) {
+// Arrives at a barrier of both blocks when the products issued so far are done.
+__device__ __forceinline__ void mma_commit(unsigned bar) {
     asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-            smem_u32(bar))
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar), "h"((unsigned short)3)
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_load32(unsigned addr, float (&v)[kChunk]) {
+// 16 columns of the warp's 32 rows: lane l holds row l.
+__device__ __forceinline__ void tmem_load(unsigned addr, float *v) {
     unsigned *r = reinterpret_cast<unsigned *>(v);
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[14]), "=r"(r[15])
         : "r"(addr));
 }
 // Waits for the warp's tensor-memory loads; `settled` then keeps the compiler
@@ -153,119 +198,164 @@ __device__ __forceinline__ void tmem_load_wait() {
     __syncwarp();
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void settled(float (&v)[kChunk]) {
+template <int C>
+__device__ __forceinline__ void settled(float (&v)[C]) {
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) asm volatile("" : "+f"(v[i]));
+    for (int i = 0; i < C; ++i) asm volatile("" : "+f"(v[i]));
 }
 
-// ---- a row's 32 columns between registers and global memory ----------------
+// ---- a row's 16 columns between registers and global memory ----------------
 //
-// Lane l of a warp holds row l of a 32 x 32 block.  Aligned rows (vec) move as
-// full 32-byte sectors; other rows go through the warp's transposing buffer,
-// 16 columns at a time, so that a warp access covers runs of 16 neighbouring
-// elements.  `rows` x `cols`: what of the block is inside the result.
+// Lane l of a warp holds row l of a 32 x 16 block.  Aligned rows move as full
+// 32-byte sectors; other rows, and the last columns of a row, go through the
+// warp's transposing buffer, so that a warp access covers runs of 16
+// neighbouring elements.
 
-__device__ __forceinline__ void read_block(const void *p, long long ld, int dtype, bool vec,
-                                           long long row0, int rows, int col0, int cols,
-                                           float *trans, float (&v)[kChunk]) {
+struct Block {
+    int row0, rows;  // first row, rows inside the result (of 32)
+    int col0, cols;  // first column, columns inside the result from there
+};
+
+__device__ __forceinline__ void fetch_edge(const void *p, long long ld, int dtype, const Block &b,
+                                           unsigned (&raw)[kChunk]) {
+    const int lane = threadIdx.x & 31, c = lane & 15;
+    const long long at = (long long)(b.row0 + (lane >> 4)) * ld + b.col0 + c;
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+        float x = 0.0f;
+        if (2 * i + (lane >> 4) < b.rows && c < b.cols)
+            x = img_load(p, (size_t)(at + 2 * i * ld), dtype);
+        raw[i] = __float_as_uint(x);
+    }
+}
+// Place of a value in the transposing buffer (16 floats a row, without bank conflicts).
+__device__ __forceinline__ int buffer_at(int r, int c) { return r * kChunk + (c ^ (r & 15)); }
+__device__ __forceinline__ void unpack_edge(float *buffer, const unsigned (&raw)[kChunk],
+                                            float (&v)[kChunk]) {
     const int lane = threadIdx.x & 31;
-    if (vec && cols >= kChunk) {
-        if (lane < rows) {
-            const long long at = (row0 + lane) * ld + col0;
-            if (dtype == PDR_F32) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    unsigned w[8];
-                    load8(static_cast<const float *>(p) + at + 8 * i, w);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[8 * i + j] = __uint_as_float(w[j]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    unsigned w[8];
-                    load8(static_cast<const unsigned short *>(p) + at + 16 * i, w);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 f = unpack2(w[j], dtype);
-                        v[16 * i + 2 * j] = f.x;
-                        v[16 * i + 2 * j + 1] = f.y;
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i) v[i] = 0.0f;
-        }
-        return;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        __syncwarp();
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-            const int r = 2 * i + (lane >> 4), c = 16 * h + (lane & 15);
-            float x = 0.0f;
-            if (r < rows && c < cols) x = img_load(p, (size_t)((row0 + r) * ld + col0 + c), dtype);
-            trans[r * kStagePitch + (lane & 15)] = x;
-        }
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[16 * h + j] = trans[lane * kStagePitch + j];
-    }
     __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i)
+        buffer[buffer_at(2 * i + (lane >> 4), lane & 15)] = __uint_as_float(raw[i]);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) v[j] = buffer[buffer_at(lane, j)];
+}
+__device__ __forceinline__ void write_edge(void *p, long long ld, int dtype, const Block &b,
+                                           float *buffer, const float (&v)[kChunk]) {
+    const int lane = threadIdx.x & 31, c = lane & 15;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) buffer[buffer_at(lane, j)] = v[j];
+    __syncwarp();
+    const long long at = (long long)(b.row0 + (lane >> 4)) * ld + b.col0 + c;
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+        const int r = 2 * i + (lane >> 4);
+        if (r < b.rows && c < b.cols)
+            img_store(p, (size_t)(at + 2 * i * ld), dtype, buffer[buffer_at(r, c)]);
+    }
 }
 
-__device__ __forceinline__ void write_block(void *p, long long ld, int dtype, bool vec,
-                                            long long row0, int rows, int col0, int cols,
-                                            float *trans, const float (&v)[kChunk]) {
-    const int lane = threadIdx.x & 31;
-    if (vec && cols >= kChunk) {
-        if (lane < rows) {
-            const long long at = (row0 + lane) * ld + col0;
-            if (dtype == PDR_F32) {
+__device__ __forceinline__ void unpack_row(int dtype, const unsigned (&raw)[kChunk],
+                                           float (&v)[kChunk]) {
+    if (dtype == PDR_F32) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    unsigned w[8];
+        for (int i = 0; i < kChunk; ++i) v[i] = __uint_as_float(raw[i]);
+    } else if (dtype == PDR_F16) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * i + j]);
-                    store8(static_cast<float *>(p) + at + 8 * i, w);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    unsigned w[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        w[j] = pack2(v[16 * i + 2 * j], v[16 * i + 2 * j + 1], dtype);
-                    store8(static_cast<unsigned short *>(p) + at + 16 * i, w);
-                }
-            }
+        for (int i = 0; i < kChunk / 2; ++i) {
+            const float2 f = unpack2(raw[i], PDR_F16);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
         }
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) trans[lane * kStagePitch + j] = v[16 * h + j];
-        __syncwarp();
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-            const int r = 2 * i + (lane >> 4), c = 16 * h + (lane & 15);
-            if (r < rows && c < cols)
-                img_store(p, (size_t)((row0 + r) * ld + col0 + c), dtype,
-                          trans[r * kStagePitch + (lane & 15)]);
+        for (int i = 0; i < kChunk / 2; ++i) {
+            const float2 f = unpack2(raw[i], PDR_BF16);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
         }
     }
-    __syncwarp();
+}
+__device__ __forceinline__ void pack_row(int dtype, const float *v, unsigned (&w)[kChunk / 2]) {
+    if (dtype == PDR_F16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], PDR_F16);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], PDR_BF16);
+    }
+}
+__device__ __forceinline__ void write_row(bool on, char *q, int dtype, const float (&v)[kChunk]) {
+    if (dtype == PDR_F32) {
+        unsigned w[kChunk];
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) w[j] = __float_as_uint(v[j]);
+        store8(on, q, w);
+        store8(on, q + 32, w + 8);
+    } else {
+        unsigned w[kChunk / 2];
+        pack_row(dtype, v, w);
+        store8(on, q, w);
+    }
 }
 
-// Sums of the 32 columns over the warp's 32 rows: lane l returns column l's.
+// Results leave through the warp's buffer and TMA stores of 32 rows, which drop
+// what is behind the last row and column: direct stores of 32 bytes a lane take 32
+// turns of the load-store unit each, this way four.  A block in the buffer has
+// rows of 64 bytes (32 columns of 16 bits or 16 of 32) or of 32 bytes (16 of 16
+// bits), their 16-byte pieces swizzled as the map says.
+__device__ __forceinline__ void stage_half(char *buffer, int half, const unsigned (&w)[kChunk / 2]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<uint4 *>(buffer + lane * 64 + ((2 * half + j) ^ ((lane >> 1) & 3)) * 16) =
+            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+__device__ __forceinline__ void stage_floats(char *buffer, const float *v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<float4 *>(buffer + lane * 64 + (j ^ ((lane >> 1) & 3)) * 16) =
+            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+__device__ __forceinline__ void stage_narrow(char *buffer, const unsigned (&w)[kChunk / 2]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<uint4 *>(buffer + lane * 32 + (j ^ ((lane >> 2) & 1)) * 16) =
+            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+// Before the buffer is written again: its last stores have read it.
+__device__ __forceinline__ void buffer_free() {
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, const char *buffer, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+        "r"(x), "r"(y), "r"(z), "r"(smem_u32(buffer))
+        : "memory");
+}
+// Stores one staged block, or two of neighbouring results.
+__device__ __forceinline__ void store_buffer(const CUtensorMap *map, const CUtensorMap *map2,
+                                             const char *buffer, int x, int y, int z) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (elect_one()) {
+        tma_store(map, buffer, x, y, z);
+        if (map2) tma_store(map2, buffer + kBufferBytes / 2, x, y, z);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+}
+
+// Sums of the 16 columns over the warp's 32 rows: lanes l and l + 16 return
+// column l's.
 __device__ __forceinline__ float column_sums(float (&v)[kChunk]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int w = 16; w >= 1; w >>= 1) {
+    for (int w = kChunk / 2; w >= 1; w >>= 1) {
         const bool up = lane & w;
 #pragma unroll
         for (int i = 0; i < w; ++i) {
@@ -273,18 +363,20 @@ __device__ __forceinline__ float column_sums(float (&v)[kChunk]) {
             v[i] = mine + __shfl_xor_sync(0xffffffffu, other, w);
         }
     }
-    return v[0];
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
-template <int ACT>
-__device__ __forceinline__ void apply_act(float (&v)[kChunk]) {
+template <int ACT, int C>
+__device__ __forceinline__ void apply_act(float (&v)[C]) {
+    float s;
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) v[i] = act_value<ACT>(v[i]);
+    for (int i = 0; i < C; ++i) v[i] = act_both<ACT>(v[i], s);
 }
-template <int ACT>
-__device__ __forceinline__ void apply_gated(float (&g)[kChunk], const float (&u)[kChunk]) {
+template <int ACT, int C>
+__device__ __forceinline__ void apply_gated(float (&g)[C], const float (&u)[C]) {
+    float s;
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) g[i] = act_value<ACT>(g[i]) * u[i];
+    for (int i = 0; i < C; ++i) g[i] = act_both<ACT>(g[i], s) * u[i];
 }
 template <int ACT>
 __device__ __forceinline__ void apply_slope(float (&z)[kChunk], const float (&dy)[kChunk]) {
@@ -308,162 +400,365 @@ __device__ __forceinline__ void apply_gated_bwd(float (&g)[kChunk], float (&u)[k
     }
 }
 
-// f<ACT>(...) for the run's activation, switched once per 32 columns.
-#define PDR_BY_ACT(act, f, ...)                                   \
-    switch (act) {                                                \
-        case PDR_ACT_RELU: f<PDR_ACT_RELU>(__VA_ARGS__); break;   \
-        case PDR_ACT_SILU: f<PDR_ACT_SILU>(__VA_ARGS__); break;   \
-        case PDR_ACT_GELU: f<PDR_ACT_GELU>(__VA_ARGS__); break;   \
-        case PDR_ACT_GELU_TANH: f<PDR_ACT_GELU_TANH>(__VA_ARGS__); break; \
-        default: f<PDR_ACT_NONE>(__VA_ARGS__); break;             \
-    }
-
 struct Tile {
-    int m, n, z, split, k0, k1;
+    int m, n, z, split;  // m: this block's 128 rows
 };
-__device__ __forceinline__ Tile tile_of(const GemmParams &p, int t) {
+struct KRange {
+    int first, end;
+};
+__device__ __forceinline__ int quotient(int n, const Divisor &d) {
+    return d.d == 1 ? n : (int)(__umulhi((unsigned)n, d.mul) >> d.shift);
+}
+__device__ __forceinline__ Tile tile_of(const GemmParams &p, int t, int rank) {
     Tile r;
-    r.n = t % p.nn;
-    t /= p.nn;
-    r.m = t % p.nm;
-    t /= p.nm;
-    r.z = t % p.nz;
-    r.split = t / p.nz;
-    r.k0 = (int)((long long)p.kb * r.split / p.splits);
-    r.k1 = (int)((long long)p.kb * (r.split + 1) / p.splits);
+    // Down the columns of tiles, or along the rows: neighbouring pairs share A rows in L2.
+    const Divisor &inner = p.stationary ? p.nm : p.nn, &outer = p.stationary ? p.nn : p.nm;
+    const int q = quotient(t, inner), i = t - q * inner.d;
+    t = quotient(q, outer);
+    const int o = q - t * outer.d;
+    r.m = 2 * (p.stationary ? i : o) + rank;
+    r.n = p.stationary ? o : i;
+    r.z = 0;
+    r.split = t;
+    if (p.nz == 2) {
+        r.z = t & 1;
+        r.split = t >> 1;
+    }
     return r;
 }
+__device__ __forceinline__ KRange k_range(const GemmParams &p, const Tile &t) {
+    if (p.splits == 1) return {0, p.kb};
+    return {(int)((unsigned)(p.kb * t.split) / (unsigned)p.splits),  // kb * splits < 2^31
+            (int)((unsigned)(p.kb * (t.split + 1)) / (unsigned)p.splits)};
+}
+// The tiles of a pair: a contiguous run of the columns, or every so many.
+struct Range {
+    int first, end, step;
+};
+__device__ __forceinline__ Range my_tiles(const GemmParams &p) {
+    const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    if (p.stationary)
+        return {(int)((long long)p.tiles * pair / pairs), (int)((long long)p.tiles * (pair + 1) / pairs), 1};
+    return {pair, p.tiles, pairs};
+}
 
-__device__ __forceinline__ void load_stage(const GemmParams &p, const Tile &t, int kb, char *stage,
-                                           unsigned long long *bar) {
+__device__ __forceinline__ void load_a(const GemmParams &p, const Tile &t, int kb, unsigned A,
+                                       unsigned bar) {
     const bool second = p.mode == kTwoSources && kb >= p.kb0;
     const int k = (second ? kb - p.kb0 : kb) * p.kelems;
-    const CUtensorMap *ma = &p.a[second || (p.mode == kBatchA && t.z) ? 1 : 0];
-    const CUtensorMap *mb = &p.b[second ? 1 : 0];
-    char *A = stage, *B = stage + kABytes;
-    const int m0 = t.m * kBM, n0 = t.n * p.bcols;
+    const CUtensorMap *map = &p.a[second || (p.mode == kBatchA && t.z) ? 1 : 0];
+    const int m0 = t.m * kBM;
     if (p.a_mn) {
-        tma_load(A, ma, m0, k, bar);
-        tma_load(A + kABytes / 2, ma, m0 + 64, k, bar);
+        tma_load(A, map, m0, k, bar);
+        tma_load(A + kABytes / 2, map, m0 + 64, k, bar);
     } else {
-        tma_load(A, ma, k, m0, bar);
+        tma_load(A, map, k, m0, bar);
     }
+}
+// This block's half of the B rows (in the gated modes: all of Wg's or of Wu's).
+__device__ __forceinline__ void load_b(const GemmParams &p, const Tile &t, int kb, int rank,
+                                       unsigned B, unsigned bar) {
+    const bool second = p.mode == kTwoSources && kb >= p.kb0;
+    const int k = (second ? kb - p.kb0 : kb) * p.kelems;
+    const bool dual = p.mode == kDualB;
+    const CUtensorMap *map = &p.b[second || (dual && rank) ? 1 : 0];
+    const int n0 = t.n * p.bcols + (dual ? 0 : rank * (p.bn / 2));
     if (p.b_mn) {
-        for (int j = 0; j < p.b_bytes; j += 8192) tma_load(B + j, mb, n0 + j / 128, k, bar);
+        for (int j = 0; j < p.b_bytes; j += 8192) tma_load(B + j, map, n0 + j / 128, k, bar);
     } else {
-        tma_load(B, mb, k, n0, bar);
-        if (p.mode == kDualB) tma_load(B + p.b_bytes / 2, &p.b[1], k, n0, bar);
+        tma_load(B, map, k, n0, bar);
     }
 }
 
-// A 32-column chunk of one warp's 32 rows of tile t, columns c0 ... of the tile.
-template <int EPI>
-__device__ __forceinline__ void epilogue_chunk(const GemmParams &p, const Tile &t, unsigned acc,
-                                               int c0, int quarter, float scale_m,
-                                               float *columns, float *trans) {
-    const long long row0 = (long long)t.m * kBM + 32 * quarter;
-    const long long left = (long long)p.M - row0;
-    const int rows = left < 0 ? 0 : left > 32 ? 32 : (int)left;
-    const int col0 = t.n * p.bcols + c0;
-    const int cols = p.N - col0;
-    // This chunk's bias and column scales, in the warp's own shared memory
-    // (read back as broadcasts).
-    const float *bias = columns, *scale = columns + kChunk, *scale2 = columns + 2 * kChunk;
-    if (p.bias || p.fp8) {
-        const int lane = threadIdx.x & 31, n = col0 + lane;
-        const bool in = lane < cols;
-        __syncwarp();
-        if (p.bias) columns[lane] = in ? img_load(p.bias, n, p.bias_dtype) : 0.0f;
-        if (p.fp8) columns[kChunk + lane] = in ? p.scale_n[n] : 0.0f;
-        if (p.fp8 && p.scale_n2) columns[2 * kChunk + lane] = in ? p.scale_n2[n] : 0.0f;
-        __syncwarp();
+// One warp's 32 rows of a tile, from column c0 to c1 (32 columns or 64).
+// `columns`: the warp's bias and column scales, [3][kMaxCols]; `have_n`: the
+// column of tiles that they are of.  Here results leave by TMA, and rows of the
+// input are aligned and a multiple of 16 wide.
+template <int EPI, int ACT>
+__device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t, unsigned acc,
+                                              unsigned ready, unsigned phase, int c0, int c1,
+                                              int quarter, float *columns, int &have_n,
+                                              float *buffer, int *abort, unsigned release) {
+    constexpr bool kTwo = EPI == kEpiGated || EPI == kEpiGatedBwd;  // g and u
+    constexpr int C = EPI == kEpiGated ? 32 : 16;                   // columns at once
+    const int lane = threadIdx.x & 31;
+    const int row0 = t.m * kBM + 32 * quarter, n0 = t.n * p.bcols;
+    char *const stage = reinterpret_cast<char *>(buffer);
+    c1 = min(c1, p.N - n0);
+    // (A warp behind the last row of a tile still writes its column sums: zeros.)
+    const bool any = (EPI == kEpiSlope ? t.m * kBM : row0) < p.M && c0 < c1, on = row0 + lane < p.M;
+    const bool has_in = EPI != kEpiGated && p.in;
+    unsigned raw[kChunk];
+    const char *in_row = nullptr;
+    auto fetch = [&](int c) {
+        const int ib = p.in_dtype == PDR_F32 ? 4 : 2;
+        load8(on, in_row + c * ib, raw);
+        if (p.in_dtype == PDR_F32) load8(on, in_row + c * ib + 32, raw + 8);
+    };
+    float scale_m = 1.0f;
+    if (any) {  // on their way while the products finish
+        if (has_in) {
+            in_row = static_cast<const char *>(p.in) +
+                     ((long long)(row0 + lane) * p.ldi + n0) * (p.in_dtype == PDR_F32 ? 4 : 2);
+            fetch(c0);
+        }
+        if (p.fp8 && on) scale_m = p.scale_m[row0 + lane];
+        if ((p.bias || p.fp8) && have_n != t.n) {
+            have_n = t.n;
+            __syncwarp();
+            for (int c = lane; c < c1 - c0; c += 32) {
+                const int n = n0 + c0 + c;
+                if (p.bias) columns[c] = img_load(p.bias, n, p.bias_dtype);
+                if (p.fp8) columns[kMaxCols + c] = p.scale_n[n];
+                if (p.fp8 && p.scale_n2) columns[2 * kMaxCols + c] = p.scale_n2[n];
+            }
+            __syncwarp();
+        }
     }
-    float v[kChunk];
-    __syncwarp();
-    tmem_load32(acc + c0, v);
-    if constexpr (EPI == kEpiLinear) {
-        float r[kChunk];
-        if (p.in) read_block(p.in, p.ldi, p.in_dtype, p.in_vec, row0, rows, col0, cols, trans, r);
+    if (!__all_sync(0xffffffffu, bar_wait(ready, phase, abort))) return false;
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    for (int c = c0; c < c1 && any; c += C) {
+        float v[C], u[kTwo ? C : 1];
+#pragma unroll
+        for (int i = 0; i < C; i += kChunk) {
+            tmem_load(acc + c + i, v + i);
+            if constexpr (kTwo) tmem_load(acc + p.bcols + c + i, u + i);
+        }
         tmem_load_wait();
         settled(v);
+        if constexpr (kTwo) settled(u);
+        if (c + C >= c1) {  // the accumulator is read: the next products may overwrite it
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) bar_arrive_at(release);
+        }
+        float x[kChunk];
+        if (has_in) {
+            unpack_row(p.in_dtype, raw, x);
+            if (c + C < c1) fetch(c + C);
+        }
         if (p.fp8) {
+            const float *s = columns + kMaxCols + c - c0;
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) v[i] *= scale_m * scale[i];
+            for (int i = 0; i < C; ++i) {
+                v[i] *= scale_m * s[i];
+                if constexpr (EPI == kEpiGated) u[i] *= scale_m * s[kMaxCols + i];
+            }
         }
-        if (p.bias) {
+        if (!kTwo && p.bias) {
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) v[i] += bias[i];
+            for (int i = 0; i < C; ++i) v[i] += columns[c - c0 + i];
         }
-        PDR_BY_ACT(p.act, apply_act, v);
-        if (p.in) {
+        if constexpr (EPI == kEpiLinear) {
+            apply_act<ACT>(v);
+            if (has_in) {
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) v[i] += r[i];
+                for (int i = 0; i < C; ++i) v[i] += x[i];
+            }
+        } else if constexpr (EPI == kEpiGated) {
+            apply_gated<ACT>(v, u);
+        } else if constexpr (EPI == kEpiSlope) {
+            apply_slope<ACT>(v, x);
+        } else {
+            apply_gated_bwd<ACT>(v, u, x);
         }
-        const long long off = t.z * p.out_z + t.split * p.out_split;
-        char *out = static_cast<char *>(p.out2 && t.z ? p.out2 : p.out) +
-                    off * dtype_bytes(p.out_dtype);
-        write_block(out, p.ldo, p.out_dtype, p.out_vec, row0, rows, col0, cols, trans, v);
-    } else if constexpr (EPI == kEpiGated) {
-        float u[kChunk];
-        tmem_load32(acc + p.bcols + c0, u);
-        tmem_load_wait();
-        settled(v);
-        settled(u);
+        unsigned w[kChunk / 2];
+        const int half = C == 32 ? 0 : (c - c0) / kChunk & 1;
+        const int slice = t.split * p.nz + t.z;
+        if constexpr (EPI == kEpiGatedBwd) {
+            buffer_free();
+            pack_row(p.out_dtype, v, w);
+            stage_narrow(stage, w);
+            pack_row(p.out_dtype, u, w);
+            stage_narrow(stage + kBufferBytes / 2, w);
+            store_buffer(&p.o[0], &p.o[1], stage, n0 + c, row0, 0);
+        } else if (EPI == kEpiLinear && p.out_dtype == PDR_F32) {
+            buffer_free();
+            stage_floats(stage, v);
+            store_buffer(&p.o[0], nullptr, stage, n0 + c, row0, slice);
+        } else {
+            if (half == 0) buffer_free();
+#pragma unroll
+            for (int i = 0; i < C; i += kChunk) {
+                pack_row(p.out_dtype, v + i, w);
+                stage_half(stage, half + i / kChunk, w);
+            }
+            if ((C == 32 || half == 1 || c + C >= c1) && row0 < p.M)
+                store_buffer(&p.o[p.mode == kBatchA && t.z], nullptr, stage, n0 + c - half * kChunk,
+                             row0, p.mode == kBatchA ? 0 : slice);
+        }
+        if constexpr (EPI == kEpiSlope)
+            if (p.colsum) {
+#pragma unroll
+                for (int i = 0; i < C; ++i) v[i] = on ? v[i] : 0.0f;  // rows outside count nothing
+                const float s = column_sums(v);
+                if (lane < kChunk && c + lane < c1)
+                    p.colsum[((long long)t.m * 4 + quarter) * p.N + n0 + c + lane] = s;
+            }
+    }
+    if (!any && lane == 0) bar_arrive_at(release);
+    return true;
+}
+
+// The same for any alignment and width (rows that TMA cannot store, results or
+// inputs of a width that is no multiple of 16); the next 16 columns are on their way from tensor memory while 16 are computed.
+// `columns`: the warp's bias and column scales, [3][kMaxCols]; `have_n`: the
+// column of tiles that they are of.
+template <int EPI, int ACT>
+__device__ __forceinline__ bool epilogue_any(const GemmParams &p, const Tile &t, unsigned acc,
+                                              unsigned ready, unsigned phase, int c0, int c1,
+                                              int quarter, float *columns, int &have_n,
+                                              float *buffer, int *abort, unsigned release) {
+    constexpr bool kTwo = EPI == kEpiGated || EPI == kEpiGatedBwd;  // g and u
+    const int lane = threadIdx.x & 31;
+    const bool has_in = EPI != kEpiGated && p.in;
+    Block b;
+    b.row0 = t.m * kBM + 32 * quarter;
+    b.rows = max(0, min(32, p.M - b.row0));
+    const int n0 = t.n * p.bcols, ncols = p.N - n0;
+    c1 = min(c1, ncols);
+    // The pair's second block may lie behind the last row, a group behind the last column.
+    const bool any = t.m * kBM < p.M && c0 < c1, on = lane < b.rows;
+    const int ib = p.in_dtype == PDR_F32 ? 4 : 2;
+    const long long row = b.row0 + lane;
+    const char *in_row = static_cast<const char *>(p.in) + (row * p.ldi + n0) * ib;
+    unsigned raw[kChunk];
+    float scale_m = 1.0f;
+    auto fetch = [&](int c) {
+        if (p.in_vec && c + kChunk <= ncols) {
+            load8(on, in_row + c * ib, raw);
+            if (p.in_dtype == PDR_F32) load8(on, in_row + c * ib + 32, raw + 8);
+        } else {
+            b.col0 = n0 + c;
+            b.cols = ncols - c;
+            fetch_edge(p.in, p.ldi, p.in_dtype, b, raw);
+        }
+    };
+    if (any) {  // on their way while the products finish
+        if (has_in) fetch(c0);
+        if (p.fp8 && on) scale_m = p.scale_m[row];
+        if ((p.bias || p.fp8) && have_n != t.n) {
+            have_n = t.n;
+            __syncwarp();
+            for (int c = lane; c < c1 - c0; c += 32) {
+                const int n = n0 + c0 + c;
+                if (p.bias) columns[c] = img_load(p.bias, n, p.bias_dtype);
+                if (p.fp8) columns[kMaxCols + c] = p.scale_n[n];
+                if (p.fp8 && p.scale_n2) columns[2 * kMaxCols + c] = p.scale_n2[n];
+            }
+            __syncwarp();
+        }
+    }
+    if (!__all_sync(0xffffffffu, bar_wait(ready, phase, abort))) return false;
+    if (!any) {
+        if (lane == 0) bar_arrive_at(release);
+        return true;
+    }
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    auto read = [&](int c, float (&v)[kChunk], float (&u)[kChunk]) {
+        tmem_load(acc + c, v);
+        if constexpr (kTwo) tmem_load(acc + p.bcols + c, u);
+    };
+    auto write = [&](void *out, int c, const float (&v)[kChunk]) {
+        const int ob = p.out_dtype == PDR_F32 ? 4 : 2;
+        char *to = static_cast<char *>(out) + (t.z * p.out_z + t.split * p.out_split) * ob;
+        if (p.out_vec && c + kChunk <= ncols) {
+            write_row(on, to + (row * p.ldo + n0 + c) * ob, p.out_dtype, v);
+        } else {
+            b.col0 = n0 + c;
+            b.cols = ncols - c;
+            write_edge(to, p.ldo, p.out_dtype, b, buffer, v);
+        }
+    };
+    auto finish = [&](int c, float (&v)[kChunk], float (&u)[kChunk]) {
+        float x[kChunk];
+        if (has_in) {
+            if (p.in_vec && c + kChunk <= ncols)
+                unpack_row(p.in_dtype, raw, x);
+            else
+                unpack_edge(buffer, raw, x);
+            if (c + kChunk < c1) fetch(c + kChunk);
+        }
         if (p.fp8) {
+            const float *s = columns + kMaxCols + c - c0;
 #pragma unroll
             for (int i = 0; i < kChunk; ++i) {
-                v[i] *= scale_m * scale[i];
-                u[i] *= scale_m * scale2[i];
+                v[i] *= scale_m * s[i];
+                if constexpr (EPI == kEpiGated) u[i] *= scale_m * s[kMaxCols + i];
             }
         }
-        PDR_BY_ACT(p.act, apply_gated, v, u);
-        write_block(p.out, p.ldo, p.out_dtype, p.out_vec, row0, rows, col0, cols, trans, v);
-    } else if constexpr (EPI == kEpiSlope) {
-        float dy[kChunk];
-        read_block(p.in, p.ldi, p.in_dtype, p.in_vec, row0, rows, col0, cols, trans, dy);
-        tmem_load_wait();
-        settled(v);
-        if (p.bias) {
+        if (!kTwo && p.bias) {
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) v[i] += bias[i];
+            for (int i = 0; i < kChunk; ++i) v[i] += columns[c - c0 + i];
         }
-        PDR_BY_ACT(p.act, apply_slope, v, dy);
-        write_block(p.out, p.ldo, p.out_dtype, p.out_vec, row0, rows, col0, cols, trans, v);
-        if (p.colsum) {
-            // Rows outside count nothing, whatever act'(bias) is there.
-            if ((int)(threadIdx.x & 31) >= rows) {
+        if constexpr (EPI == kEpiLinear) {
+            apply_act<ACT>(v);
+            if (has_in) {
 #pragma unroll
-                for (int i = 0; i < kChunk; ++i) v[i] = 0.0f;
+                for (int i = 0; i < kChunk; ++i) v[i] += x[i];
             }
-            const float s = column_sums(v);
-            const int lane = threadIdx.x & 31;
-            if (lane < cols)
-                p.colsum[((long long)t.m * 4 + quarter) * p.N + col0 + lane] = s;
+        } else if constexpr (EPI == kEpiGated) {
+            apply_gated<ACT>(v, u);
+        } else if constexpr (EPI == kEpiSlope) {
+            apply_slope<ACT>(v, x);
+        } else {
+            apply_gated_bwd<ACT>(v, u, x);
         }
-    } else {
-        float u[kChunk], dh[kChunk];
-        tmem_load32(acc + p.bcols + c0, u);
-        read_block(p.in, p.ldi, p.in_dtype, p.in_vec, row0, rows, col0, cols, trans, dh);
-        tmem_load_wait();
-        settled(v);
-        settled(u);
-        PDR_BY_ACT(p.act, apply_gated_bwd, v, u, dh);
-        write_block(p.out, p.ldo, p.out_dtype, p.out_vec, row0, rows, col0, cols, trans, v);
-        write_block(p.out2, p.ldo, p.out_dtype, p.out_vec, row0, rows, col0, cols, trans, u);
+        write(EPI == kEpiLinear && p.out2 && t.z ? p.out2 : p.out, c, v);
+        if constexpr (EPI == kEpiGatedBwd) write(p.out2, c, u);
+        if constexpr (EPI == kEpiSlope)
+            if (p.colsum) {
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) v[i] = on ? v[i] : 0.0f;  // rows outside count nothing
+                const float s = column_sums(v);
+                if (lane < kChunk && lane < ncols - c)
+                    p.colsum[((long long)t.m * 4 + quarter) * p.N + n0 + c + lane] = s;
+            }
+    };
+    // Two sets of registers, the next columns' and these; dg and du leave room for one.
+    constexpr int kSets = EPI == kEpiGatedBwd ? 1 : 2;
+    float v[kSets][kChunk], u[kSets][kChunk];
+    __syncwarp();
+    if constexpr (kSets == 2) read(c0, v[0], u[0]);
+    for (int c = c0; c < c1; c += kStore) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int at = c + half * kChunk, set = half % kSets;
+            if (at >= c1) break;
+            if constexpr (kSets == 1) {
+                __syncwarp();
+                read(at, v[set], u[set]);
+            }
+            tmem_load_wait();
+            settled(v[set]);
+            if constexpr (kTwo) settled(u[set]);
+            if (at + kChunk >= c1) {  // the accumulator is read: the next products may overwrite it
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) bar_arrive_at(release);
+            } else if constexpr (kSets == 2) {
+                read(at + kChunk, v[1 - set], u[1 - set]);
+            }
+            finish(at, v[set], u[set]);
+        }
     }
+    return true;
 }
 
-template <int EPI>
-__global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ GemmParams p) {
+template <int EPI, int ACT, bool ANY>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_gemm(const __grid_constant__ GemmParams p) {
     extern __shared__ char raw[];
-    // Stages first, at a 1024-byte boundary (the swizzle's period).
+    // Tiles first, at a 1024-byte boundary (the swizzle's period).
     char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    const int stage_bytes = kABytes + p.b_bytes;
-    char *after = smem + p.stages * stage_bytes;
-    Barriers *bars = reinterpret_cast<Barriers *>(after);
-    float *columns_all = reinterpret_cast<float *>(after + 512);  // [8 warps][3][32]
-    float *trans_all = columns_all + 8 * 3 * kChunk;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int stage_bytes = kABytes + (p.stationary ? 0 : p.b_bytes);
+    char *held = smem + p.stages * stage_bytes;  // B of all k, where it stays
+    char *after = held + (p.stationary ? p.kb * p.b_bytes : 0);
+    float *buffers = reinterpret_cast<float *>(after);  // one per epilogue warp, 1024-byte aligned
+    float *columns_all = buffers + kEpiWarps * kBufferBytes / 4;  // [warp][3][kMaxCols]
+    Barriers *bars = reinterpret_cast<Barriers *>(columns_all + kEpiWarps * 3 * kMaxCols);
+    const int warp = threadIdx.x >> 5;
+    const int rank = blockIdx.x & 1;  // in the pair; block 0 leads
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
@@ -472,136 +767,195 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Ge
         }
         for (int i = 0; i < p.nacc; ++i) {
             bar_init(&bars->acc_full[i], 1);
-            bar_init(&bars->acc_empty[i], p.split_cols ? 8 : 4);
+            bar_init(&bars->acc_empty[i], 2 * 4 * p.sharing);
         }
+        bar_init(&bars->b_full, 1);
+        bar_init(&bars->b_empty, 1);
         bar_init(&bars->drain, 1);
         bars->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+    if (warp == kProductWarp) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&bars->tmem)),
                      "r"(512)
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    __syncthreads();
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    const unsigned tmem = bars->tmem;
-    grid_dep_wait();
-
-    if (warp == 0 && lane == 0) {
-        int stage = 0, issued = 0;
-        unsigned phase = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
-            const Tile tile = tile_of(p, t);
-            for (int kb = tile.k0; kb < tile.k1; ++kb) {
-                ok = bar_wait(&bars->empty[stage], phase ^ 1, &bars->abort);
-                if (!ok) break;
-                bar_expect(&bars->full[stage], stage_bytes);
-                load_stage(p, tile, kb, smem + stage * stage_bytes, &bars->full[stage]);
-                ++issued;
-                if (++stage == p.stages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-        if (!ok) {
-            // Copies in flight end before the block does (waits bounded).
-            const int n = issued < p.stages ? issued : p.stages;
-            for (int i = 0; i < n; ++i) {
-                if (stage == 0) {
-                    stage = p.stages;
-                    phase ^= 1;
-                }
-                --stage;
-                for (int j = 0; j < kWaitTries && !bar_try(&bars->full[stage], phase); ++j) {
-                }
-            }
-        }
-    } else if (warp == 1 && lane == 0) {
-        int stage = 0, acc = 0;
-        unsigned phase = 0, acc_phase = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
-            const Tile tile = tile_of(p, t);
-            ok = bar_wait(&bars->acc_empty[acc], acc_phase ^ 1, &bars->abort);
-            if (!ok) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const unsigned d = tmem + acc * p.bn;
-            bool more = false;
-            for (int kb = tile.k0; kb < tile.k1; ++kb) {
-                ok = bar_wait(&bars->full[stage], phase, &bars->abort);
-                if (!ok) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const unsigned at = smem_u32(smem + stage * stage_bytes);
-                unsigned long long da = p.adesc | ((at >> 4) & 0x3fff);
-                unsigned long long db = p.bdesc | (((at + kABytes) >> 4) & 0x3fff);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    mma(d, da, db, p.idesc, more, p.fp8);
-                    more = true;
-                    da += p.a_step;
-                    db += p.b_step;
-                }
-                mma_commit(&bars->empty[stage]);
-                if (++stage == p.stages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-            if (!ok) break;
-            mma_commit(&bars->acc_full[acc]);
-            if (++acc == p.nacc) {
-                acc = 0;
-                acc_phase ^= 1;
-            }
-        }
-        if (!ok) {
-            mma_commit(&bars->drain);  // products in flight end before their memory is freed
-            for (int j = 0; j < kWaitTries && !bar_try(&bars->drain, 0); ++j) {
-            }
-        }
-    } else if (warp >= kEpiWarp) {
-        const int ew = warp - kEpiWarp, group = ew >> 2, quarter = warp & 3;
-        float *trans = trans_all + ew * (kTransBytes / 4);
-        float *columns = columns_all + ew * 3 * kChunk;
-        const int cols = p.split_cols ? p.bcols / 2 : p.bcols;
-        const int cfirst = p.split_cols ? group * cols : 0;
-        int acc = 0, it = 0;
-        unsigned acc_phase = 0;
-        for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, ++it) {
-            const bool mine = p.split_cols || (it & 1) == group;
-            if (mine) {
-                const Tile tile = tile_of(p, t);
-                float scale_m = 1.0f;
-                const long long row = (long long)tile.m * kBM + 32 * quarter + lane;
-                if (p.fp8 && row < p.M) scale_m = p.scale_m[row];
-                if (!bar_wait(&bars->acc_full[acc], acc_phase, &bars->abort)) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const unsigned d = tmem + ((unsigned)(32 * quarter) << 16) + acc * p.bn;
-                for (int c = cfirst; c < cfirst + cols; c += kChunk)
-                    if (tile.n * p.bcols + c < p.N)
-                        epilogue_chunk<EPI>(p, tile, d, c, quarter, scale_m, columns, trans);
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) bar_arrive(&bars->acc_empty[acc]);
-            }
-            if (++acc == p.nacc) {
-                acc = 0;
-                acc_phase ^= 1;
-            }
-        }
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     __syncwarp();
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    __syncthreads();
-    if (warp == 2) {
+    cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const unsigned tmem = bars->tmem;
+    const Range range = my_tiles(p);
+    const unsigned full = smem_u32(bars->full), empty = smem_u32(bars->empty);
+    const unsigned acc_full = smem_u32(bars->acc_full), acc_empty = smem_u32(bars->acc_empty);
+    const unsigned b_full = smem_u32(&bars->b_full), b_empty = smem_u32(&bars->b_empty);
+    int *abort = &bars->abort;
+    grid_dep_wait();
+
+    // The launch gives each thread 96 registers; the epilogue's warps take
+    // what the others do not need.
+    if (warp >= kEpiWarp) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+        const int ew = warp - kEpiWarp, group = ew >> 2, quarter = warp & 3;
+        float *buffer = buffers + ew * (kBufferBytes / 4);
+        float *columns = columns_all + ew * 3 * kMaxCols;
+        // `sharing` groups divide a tile's columns, sets of them take tiles in turn.
+        const int cols = p.bcols / p.sharing, cfirst = group % p.sharing * cols;
+        const int sets = kGroups / p.sharing, set = group / p.sharing;
+        const unsigned release = at_rank(acc_empty, 0);
+        int acc = 0, it = 0, have_n = -1;
+        unsigned acc_phase = 0;
+        Tile tile = tile_of(p, range.first, rank);
+        for (int t = range.first; t < range.end; t += range.step, ++it) {
+            if ((it & (sets - 1)) == set) {
+                const unsigned d = tmem + ((unsigned)(32 * quarter) << 16) + acc * p.bn;
+                bool ok;
+                if constexpr (ANY)
+                    ok = epilogue_any<EPI, ACT>(p, tile, d, acc_full + 8 * acc, acc_phase, cfirst,
+                                                cfirst + cols, quarter, columns, have_n, buffer,
+                                                abort, release + 8 * acc);
+                else
+                    ok = epilogue_tile<EPI, ACT>(p, tile, d, acc_full + 8 * acc, acc_phase, cfirst,
+                                                 cfirst + cols, quarter, columns, have_n, buffer,
+                                                 abort, release + 8 * acc);
+                if (!ok) break;
+            }
+            tile.m += 2;  // down the column, or looked up
+            if (!p.stationary || tile.m >= 2 * (int)p.nm.d) tile = tile_of(p, t + range.step, rank);
+            if (++acc == p.nacc) {
+                acc = 0;
+                acc_phase ^= 1;
+            }
+        }
+        if (!ANY && elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        const unsigned stages0 = smem_u32(smem), held0 = smem_u32(held);
+        if (warp == kCopyWarp && elect_one()) {
+            const unsigned lead_full = at_rank(full, 0), lead_b_full = at_rank(b_full, 0);
+            int stage = 0, issued = 0, column = -1;
+            unsigned phase = 0, b_phase = 0;
+            bool ok = true, ready = true;  // the first stages are empty
+            for (int t = range.first; t < range.end && ok; t += range.step) {
+                const Tile tile = tile_of(p, t, rank);
+                const KRange k = k_range(p, tile);
+                if (p.stationary && column != quotient(t, p.nm)) {
+                    column = quotient(t, p.nm);
+                    ok = bar_wait(b_empty, b_phase ^ 1, abort);
+                    if (!ok) break;
+                    b_phase ^= 1;
+                    if (rank == 0) bar_expect(b_full, 2 * p.kb * p.b_bytes);
+                    for (int kb = 0; kb < p.kb; ++kb)
+                        load_b(p, tile, kb, rank, held0 + kb * p.b_bytes, lead_b_full);
+                }
+                for (int kb = k.first; kb < k.end; ++kb) {
+                    if (!ready) ok = bar_wait(empty + 8 * stage, phase ^ 1, abort);
+                    if (!ok) break;
+                    const unsigned bar = lead_full + 8 * stage, at = stages0 + stage * stage_bytes;
+                    if (rank == 0) bar_expect(full + 8 * stage, 2 * stage_bytes);
+                    ++issued;
+                    if (++stage == p.stages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    ready = bar_try(empty + 8 * stage, phase ^ 1);  // asked early: the answer takes a while
+                    load_a(p, tile, kb, at, bar);
+                    if (!p.stationary) load_b(p, tile, kb, rank, at + kABytes, bar);
+                }
+            }
+            if (!ok && rank == 0) {
+                // The pair's copies in flight end before its blocks do (waits bounded).
+                const int n = issued < p.stages ? issued : p.stages;
+                for (int i = 0; i < n; ++i) {
+                    if (stage == 0) {
+                        stage = p.stages;
+                        phase ^= 1;
+                    }
+                    --stage;
+                    for (int j = 0; j < kWaitTries && !bar_try(full + 8 * stage, phase); ++j) {
+                    }
+                }
+                if (column >= 0)
+                    for (int j = 0; j < kWaitTries && !bar_try(b_full, b_phase ^ 1); ++j) {
+                    }
+            }
+        } else if (warp == kProductWarp && rank == 0 && elect_one()) {
+            const unsigned a_hi = (unsigned)(p.adesc >> 32), b_hi = (unsigned)(p.bdesc >> 32);
+            const unsigned a_lo = (unsigned)p.adesc, b_lo = (unsigned)p.bdesc;
+            // Tiles left in the column of the first one (stationary B).
+            int stage = 0, acc = 0, left = 0;
+            unsigned phase = 0, acc_phase = 0, b_phase = 0;
+            // Whether the next barriers were seen ready: asked before a block's
+            // products are issued, so that the answer is there when they are.
+            bool ok = true, full_ready = false, acc_ready = false;
+            for (int t = range.first; t < range.end; t += range.step) {
+                int nk = p.kb;
+                if (p.splits > 1) {
+                    const KRange k = k_range(p, tile_of(p, t, rank));
+                    nk = k.end - k.first;
+                }
+                if (p.stationary && left == 0) {
+                    left = p.nm.d;
+                    if (t == range.first)
+                        left -= t - quotient(t, p.nm) * p.nm.d;
+                    else
+                        mma_commit(b_empty);  // the last column's B is free
+                    ok = bar_wait(b_full, b_phase, abort);
+                    b_phase ^= 1;
+                    if (!ok) break;
+                }
+                --left;
+                if (!acc_ready) ok = bar_wait(acc_empty + 8 * acc, acc_phase ^ 1, abort);
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const unsigned d = tmem + acc * p.bn, this_full = acc_full + 8 * acc;
+                if (++acc == p.nacc) {
+                    acc = 0;
+                    acc_phase ^= 1;
+                }
+                bool more = false;
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!full_ready) ok = bar_wait(full + 8 * stage, phase, abort);
+                    if (!ok) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const unsigned at = stages0 + stage * stage_bytes, done = empty + 8 * stage;
+                    const unsigned bt = p.stationary ? held0 + kb * p.b_bytes : at + kABytes;
+                    if (++stage == p.stages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    full_ready = bar_try(full + 8 * stage, phase);
+                    if (kb == nk - 1) acc_ready = bar_try(acc_empty + 8 * acc, acc_phase ^ 1);
+                    unsigned al = a_lo | (at >> 4), bl = b_lo | (bt >> 4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        mma(d, al, a_hi, bl, b_hi, p.idesc, more, p.fp8);
+                        more = true;
+                        al += p.a_step;
+                        bl += p.b_step;
+                    }
+                    mma_commit(done);
+                }
+                if (!ok) break;
+                mma_commit(this_full);
+            }
+            if (!ok) {
+                const unsigned drain = smem_u32(&bars->drain);
+                mma_commit(drain);  // products in flight end before their memory is freed
+                for (int j = 0; j < kWaitTries && !bar_try(drain, 0); ++j) {
+                }
+            }
+        }
+    }
+    // Neither block leaves, or gives up its memory, before both are done.
+    __syncwarp();
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    cluster_sync();
+    if (warp == kProductWarp) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
     }
 }
 
@@ -719,6 +1073,21 @@ bool make_map(CUtensorMap *m, const Operand &o, int bytes, int box_cols, int box
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The map of a result (`slices` of rows x cols, one behind the other) for the
+// stores of 32 rows by 64 bytes, or (narrow) by 32.
+bool make_store_map(CUtensorMap *m, void *to, int bytes, long long rows, long long cols,
+                    long long ld, int slices, bool narrow) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)slices};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * bytes, (cuuint64_t)ld * bytes * rows};
+    const cuuint32_t box[3] = {(cuuint32_t)((narrow ? 32 : 64) / bytes), 32, 1}, unit[3] = {1, 1, 1};
+    return f(m, bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, to,
+             dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             narrow ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Shared-memory descriptor of an operand tile, without its address: 128-byte
 // swizzle; 8-row (K-major) or 8-k (MN-major) groups 1024 bytes apart, and for
 // MN-major the 64-wide blocks 8192 bytes apart.
@@ -727,15 +1096,36 @@ unsigned long long smem_desc(bool mn) {
            ((unsigned long long)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-template <int EPI>
-cudaError_t launch(const GemmParams &p, int grid, size_t smem, cudaStream_t s) {
+template <int EPI, int ACT, bool ANY>
+cudaError_t launch_as(const GemmParams &p, int grid, size_t smem, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(
-        k_gemm<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        k_gemm<EPI, ACT, ANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(k_gemm<EPI>, dim3((unsigned)grid), dim3(kThreads), smem, s, p);
+    return launch_dependent(k_gemm<EPI, ACT, ANY>, dim3((unsigned)grid), dim3(kThreads), smem, s, p);
+}
+template <int EPI, int ACT>
+cudaError_t launch_as(const GemmParams &p, int grid, size_t smem, cudaStream_t s) {
+    return p.out_tma ? launch_as<EPI, ACT, false>(p, grid, smem, s)
+                     : launch_as<EPI, ACT, true>(p, grid, smem, s);
+}
+template <int EPI>
+cudaError_t launch(const GemmParams &p, int act, int grid, size_t smem, cudaStream_t s) {
+    switch (act) {
+        case PDR_ACT_RELU: return launch_as<EPI, PDR_ACT_RELU>(p, grid, smem, s);
+        case PDR_ACT_SILU: return launch_as<EPI, PDR_ACT_SILU>(p, grid, smem, s);
+        case PDR_ACT_GELU: return launch_as<EPI, PDR_ACT_GELU>(p, grid, smem, s);
+        case PDR_ACT_GELU_TANH: return launch_as<EPI, PDR_ACT_GELU_TANH>(p, grid, smem, s);
+        default: return launch_as<EPI, PDR_ACT_NONE>(p, grid, smem, s);
+    }
 }
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+
+Divisor divisor(int d) {
+    unsigned l = 0;
+    while ((1u << l) < (unsigned)d) ++l;
+    return {(unsigned)d, (unsigned)((1ull << (31 + l)) / (unsigned)d + 1), l - 1};
+}
 
 }  // namespace
 
@@ -751,9 +1141,9 @@ int gemm_tile_columns(int epi, int M, int N, int nz) {
 
 int gemm_splits(int M, int N, int nz, long long K) {
     const int cols = gemm_tile_columns(kEpiLinear, 1 << 30, N, nz);
-    const long long tiles = (long long)ceil_div(M, kBM) * ceil_div(N, cols) * nz;
+    const long long tiles = (long long)ceil_div(M, 2 * kBM) * ceil_div(N, cols) * nz;
     const long long kb = (K + 63) / 64;
-    long long s = kSMs / tiles;
+    long long s = kSMs / 2 / tiles;
     if (s > kb / 4) s = kb / 4;  // at least 4 stages of k each
     return s < 1 ? 1 : (int)s;
 }
@@ -766,29 +1156,31 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     p.mode = g.mode;
     p.a_mn = g.a_mn;
     p.b_mn = g.b_mn;
-    p.act = g.act;
     p.M = g.M;
     p.N = g.N;
     p.nz = g.mode == kBatchA ? 2 : 1;
     p.splits = g.splits;
     p.bcols = gemm_tile_columns(g.epi, g.splits > 1 ? 1 << 30 : g.M, g.N, p.nz);
     p.bn = dual ? 2 * p.bcols : p.bcols;
-    p.nm = ceil_div(g.M, kBM);
-    p.nn = ceil_div(g.N, p.bcols);
-    const long long tiles = (long long)p.nm * p.nn * p.nz * p.splits;
+    p.nm = divisor(ceil_div(g.M, 2 * kBM));
+    p.nn = divisor(ceil_div(g.N, p.bcols));
+    const long long tiles = (long long)p.nm.d * p.nn.d * p.nz * p.splits;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
     p.tiles = (int)tiles;
     p.kb0 = ceil_div(g.K[0], kelems);
     p.kb = p.kb0 + (g.mode == kTwoSources ? ceil_div(g.K[1], kelems) : 0);
     p.kelems = kelems;
-    p.b_bytes = g.b_mn ? ceil_div(p.bn, 64) * 8192 : p.bn * kRowBytes;
+    p.b_bytes = g.b_mn ? ceil_div(p.bn / 2, 64) * 8192 : p.bn / 2 * kRowBytes;
     p.nacc = p.bn >= 256 ? 2 : 4;
-    p.split_cols = p.bcols >= 2 * kChunk;
+    // Two or four groups share a tile, 64 columns a warp, and sets of groups take
+    // tiles in turn; a pair's only tile is shared by all that it has 32 columns for.
+    p.sharing = p.tiles <= kSMs / 2 ? p.bcols / kStore : p.bcols / kMaxCols;
+    p.sharing = p.sharing < 1 ? 1 : p.sharing > kGroups ? kGroups : p.sharing;
     p.fp8 = bytes == 1;
     // D fp32 | A and B: f16 0, bf16 1 (kind::f16) or e4m3 0 (kind::f8f6f4) | majors | N / 8 | M / 16
     const unsigned t = g.dtype == PDR_BF16 ? 1 : 0;
     p.idesc = (1u << 4) | (t << 7) | (t << 10) | ((unsigned)g.a_mn << 15) |
-              ((unsigned)g.b_mn << 16) | ((unsigned)(p.bn / 8) << 17) | ((unsigned)(kBM / 16) << 24);
+              ((unsigned)g.b_mn << 16) | ((unsigned)(p.bn / 8) << 17) | ((unsigned)(2 * kBM / 16) << 24);
     p.adesc = smem_desc(g.a_mn);
     p.bdesc = smem_desc(g.b_mn);
     p.a_step = g.a_mn ? 2048 >> 4 : 32 >> 4;  // 16 k of 128-byte rows, or 32 bytes along k
@@ -800,7 +1192,7 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
             return cudaErrorInvalidValue;
     for (int i = 0; i < nb; ++i)
         if (!make_map(&p.b[i], g.b[i], bytes, g.b_mn ? 64 : kelems,
-                      g.b_mn ? 64 : dual ? p.bn / 2 : p.bn))
+                      g.b_mn ? 64 : p.bn / 2))
             return cudaErrorInvalidValue;
     p.out = g.out;
     p.out2 = g.out2;
@@ -820,19 +1212,31 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     p.in_dtype = g.in_dtype;
     p.ldi = g.ldi;
     p.in_vec = aligned_to(g.in, 32) && g.ldi * ib % 32 == 0;
+    p.out_tma = aligned_to(g.out, 16) && aligned_to(g.out2, 16) && g.ldo * ob % 16 == 0 &&
+                (!g.in || (p.in_vec && g.N % kChunk == 0)) && !(g.epi == kEpiGated && ob == 4);
+    const int slices = g.out_split || g.out_z ? p.splits * p.nz : 1;
+    for (int i = 0; p.out_tma && i < (g.out2 ? 2 : 1); ++i)
+        if (!make_store_map(&p.o[i], i ? g.out2 : g.out, ob, g.M, g.N, g.ldo, slices,
+                            g.epi == kEpiGatedBwd))
+            return cudaErrorInvalidValue;
     p.colsum = g.colsum;
-    const size_t fixed = 1024 + 512 + 8 * 3 * kChunk * 4 + 8 * kTransBytes;
-    const size_t stage = kABytes + p.b_bytes;
-    p.stages = (int)((227 * 1024 - fixed) / stage);
+    const size_t fixed = 1024 + 512 + kEpiWarps * (3 * kMaxCols * 4 + kBufferBytes);
+    const size_t room = 227 * 1024 - fixed, all_b = (size_t)p.kb * p.b_bytes;
+    const int pairs = p.tiles < kSMs / 2 ? p.tiles : kSMs / 2;
+    // B stays where it leaves room for three stages of A and a pair has several
+    // tiles to use it for.
+    p.stationary = g.splits == 1 && all_b + 3 * kABytes <= room && p.tiles >= 2 * pairs;
+    const size_t stage = kABytes + (p.stationary ? 0 : p.b_bytes);
+    p.stages = (int)((room - (p.stationary ? all_b : 0)) / stage);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
-    const size_t smem = fixed + p.stages * stage;
-    const int grid = p.tiles < kSMs ? p.tiles : kSMs;
+    const size_t smem = fixed + p.stages * stage + (p.stationary ? all_b : 0);
+    const int grid = 2 * pairs;
     static_assert(sizeof(Barriers) <= 512, "barriers fit their place");
     switch (g.epi) {
-        case kEpiGated: return launch<kEpiGated>(p, grid, smem, s);
-        case kEpiSlope: return launch<kEpiSlope>(p, grid, smem, s);
-        case kEpiGatedBwd: return launch<kEpiGatedBwd>(p, grid, smem, s);
-        default: return launch<kEpiLinear>(p, grid, smem, s);
+        case kEpiGated: return launch<kEpiGated>(p, g.act, grid, smem, s);
+        case kEpiSlope: return launch<kEpiSlope>(p, g.act, grid, smem, s);
+        case kEpiGatedBwd: return launch<kEpiGatedBwd>(p, g.act, grid, smem, s);
+        default: return launch<kEpiLinear>(p, g.act, grid, smem, s);
     }
 }
 

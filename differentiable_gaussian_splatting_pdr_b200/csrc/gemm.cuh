@@ -19,20 +19,35 @@ constexpr int kSMs = 148;
 
 // ---- activations -----------------------------------------------------------
 
-// 1 / (1 + e^-z).  e^-z overflows to infinity for very negative z: 0.
-__device__ __forceinline__ float logistic(float z) {
-    return __fdividef(1.0f, 1.0f + __expf(-z));
+constexpr float kLog2e = 1.4426950408889634f;
+
+// max that keeps NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// Phi(z) = erfc(-z / sqrt 2) / 2, and e^{-z^2/2} as a by-product.  Abramowitz
-// and Stegun, Handbook of Mathematical Functions, 7.1.26: erfc(x) =
-// (a1 t + ... + a5 t^5) e^{-x^2}, t = 1 / (1 + p x), |error| <= 1.5e-7 for
-// x >= 0 -- below the rounding of every type that an activation is stored in
-// here, and small in the negative tail, where 1 + erf would cancel.
+// 1 / (1 + e^-v).  e^-v may overflow to infinity: 0.  (Two elements can share a
+// reciprocal, 1 / a = b / (a b), which takes the special-function unit from 2 to
+// 1.5 operations an element; the three more instructions, and two that keep a NaN
+// from reaching the neighbour, cost more: PAIRED.)
+__device__ __forceinline__ float logistic(float v) { return rcp(1.0f + ex2(-kLog2e * v)); }
+
+// Phi(z) = erfc(-z / sqrt 2) / 2, and e^{-z^2/2}.  Abramowitz and Stegun, Handbook
+// of Mathematical Functions, 7.1.26: erfc(x) = (a1 t + ... + a5 t^5) e^{-x^2},
+// t = 1 / (1 + p x), |error| <= 1.5e-7 for x >= 0 -- below the rounding of every
+// type that an activation is stored in here, and small in the negative tail,
+// where 1 + erf would cancel.
 __device__ __forceinline__ float normal_cdf(float z, float &gauss) {
     const float x = fabsf(z) * 0.70710678118654752f;
-    gauss = __expf(-x * x);
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    gauss = ex2(-kLog2e * x * x);
+    const float t = rcp(fmaf(0.3275911f, x, 1.0f));
     float p = fmaf(1.061405429f, t, -1.453152027f);
     p = fmaf(p, t, 1.421413741f);
     p = fmaf(p, t, -0.284496736f);
@@ -41,44 +56,30 @@ __device__ __forceinline__ float normal_cdf(float z, float &gauss) {
     return z < 0.0f ? half : 1.0f - half;
 }
 
-template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-    if constexpr (ACT == PDR_ACT_RELU) return z < 0.0f ? 0.0f : z;  // NaN stays NaN
-    if constexpr (ACT == PDR_ACT_SILU) return z * logistic(z);
-    if constexpr (ACT == PDR_ACT_GELU) {
-        float e;
-        return z * normal_cdf(z, e);
-    }
-    if constexpr (ACT == PDR_ACT_GELU_TANH)  // (1 + tanh v) / 2 = logistic(2 v)
-        return z * logistic(1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.0f));
-    return z;
-}
-
-// The value (returned) and the derivative of an activation.
+// Value (returned) and derivative of an activation (an unused slope costs nothing).
 template <int ACT>
 __device__ __forceinline__ float act_both(float z, float &slope) {
     if constexpr (ACT == PDR_ACT_RELU) {
         slope = z > 0.0f ? 1.0f : 0.0f;
-        return z < 0.0f ? 0.0f : z;
-    }
-    if constexpr (ACT == PDR_ACT_SILU) {
-        const float t = logistic(z);
-        slope = t * fmaf(z, 1.0f - t, 1.0f);
-        return z * t;
-    }
-    if constexpr (ACT == PDR_ACT_GELU) {
+        return z < 0.0f ? 0.0f : z;  // NaN stays NaN
+    } else if constexpr (ACT == PDR_ACT_SILU) {
+        const float t = logistic(z), y = z * t;
+        slope = fmaf(y, 1.0f - t, t);
+        return y;
+    } else if constexpr (ACT == PDR_ACT_GELU) {
         float e;
         const float p = normal_cdf(z, e);
         slope = fmaf(0.39894228040143268f * z, e, p);
         return z * p;
+    } else if constexpr (ACT == PDR_ACT_GELU_TANH) {  // (1 + tanh v) / 2 = 1 / (1 + e^{-2 v})
+        const float t = logistic(1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.0f)), y = z * t;
+        const float c = fminf(fabsf(z), 10.0f);  // beyond, y (1 - t) is 0
+        slope = fmaf(y * (1.0f - t), 1.5957691216057308f * fmaf(0.134145f * c, c, 1.0f), t);
+        return y;
+    } else {
+        slope = 1.0f;
+        return z;
     }
-    if constexpr (ACT == PDR_ACT_GELU_TANH) {
-        const float t = logistic(1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.0f));
-        slope = fmaf(z * t * (1.0f - t), 1.5957691216057308f * fmaf(0.134145f * z, z, 1.0f), t);
-        return z * t;
-    }
-    slope = 1.0f;
-    return z;
 }
 
 // ---- element types ---------------------------------------------------------
@@ -102,17 +103,23 @@ __device__ __forceinline__ float2 unpack2(unsigned w, int dtype) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// 32-byte loads and stores (one full sector each; 32-byte aligned).
-__device__ __forceinline__ void load8(const void *p, unsigned (&w)[8]) {
-    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
-                   "=r"(w[6]), "=r"(w[7])
-                 : "l"(p));
+// 32-byte loads and stores (one full sector each; 32-byte aligned) of the
+// threads whose `on` is set.
+__device__ __forceinline__ void load8(bool on, const void *p, unsigned *w) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %9, 0;\n"
+        " @p ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n}"
+        : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3]), "+r"(w[4]), "+r"(w[5]), "+r"(w[6]),
+          "+r"(w[7])
+        : "l"(p), "r"((unsigned)on));
 }
-__device__ __forceinline__ void store8(void *p, const unsigned (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
+__device__ __forceinline__ void store8(bool on, void *p, const unsigned *w) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %9, 0;\n"
+        " @p st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n}" ::"l"(p),
+        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]),
+        "r"((unsigned)on)
+        : "memory");
 }
 
 // ---- host plan -------------------------------------------------------------

@@ -123,13 +123,6 @@ __device__ __forceinline__ void store_row(void *p, size_t at, int D, int t, int 
     }
 }
 
-// max that keeps NaN.
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float m;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
-    return m;
-}
-
 // Sum (or maximum) over the T threads of a row, for all of them; the whole
 // block calls it.  `red`: one float per warp.
 template <bool MAX>
