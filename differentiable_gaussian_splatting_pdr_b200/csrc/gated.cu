@@ -19,7 +19,7 @@ namespace {
 
 struct GatedLayout {
     size_t x, wg, wu, dg, du, part, total;
-    long long ldk, ldf;
+    long long ldk, ldf, ldp;  // rows of x and the weights, of dg and du, of partial dW
     bool pack;
     int splits;
 };
@@ -52,8 +52,9 @@ GatedLayout bwd_layout(int M, int D, int F, int dtype) {
     L.du = L.dg + align256((size_t)M * L.ldf * 2);
     L.part = L.du + align256((size_t)M * L.ldf * 2);
     L.splits = gemm_splits(F, D, 2, M);
+    L.ldp = round_up(D, 4);  // 16 bytes, for TMA stores
     L.total = L.part;
-    if (L.splits > 1) L.total += align256((size_t)L.splits * 2 * F * D * 4);
+    if (L.splits > 1) L.total += align256((size_t)L.splits * 2 * F * L.ldp * 4);
     return L;
 }
 
@@ -212,10 +213,11 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
         g.K[0] = M;
         g.splits = L.splits;
         g.ldo = D;
-        const long long n = (long long)F * D;
+        const long long n = F * L.ldp;
         float *part = reinterpret_cast<float *>(ws + L.part);
         if (L.splits > 1) {
             g.out = part;
+            g.ldo = L.ldp;
             g.out_dtype = PDR_F32;
             g.out_z = n;
             g.out_split = 2 * n;
@@ -226,7 +228,7 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
         }
         e = launch_gemm(g, s);
         if (e == cudaSuccess && L.splits > 1)
-            e = launch_join(part, L.splits, 2 * n, n, grad_gate, grad_up, dtype, s);
+            e = launch_join(part, L.splits, F, D, L.ldp, grad_gate, grad_up, dtype, s);
     }
     return done(e);
 }

@@ -18,6 +18,8 @@
 // What the four epilogues compute is in gemm.cuh (GemmEpi).
 #include <stdint.h>
 
+#include <atomic>
+
 #include <cuda.h>
 
 #include "gemm.cuh"
@@ -33,6 +35,7 @@ constexpr int kGroups = 4, kEpiWarps = 4 * kGroups;  // epilogue warpgroups
 constexpr int kThreads = 32 * (kEpiWarps + 4);
 constexpr int kEpiRegs = 104, kOtherRegs = 64;  // per thread: 512 x 104 + 128 x 64 <= 640 x 96
 constexpr int kCopyWarp = 0, kProductWarp = 1, kEpiWarp = 4;
+constexpr int kSmemBytes = 227 * 1024;
 constexpr int kMaxAcc = 4;            // accumulators in tensor memory
 constexpr int kChunk = 16;            // columns an epilogue warp computes at once
 constexpr int kStore = 2 * kChunk;    // columns that it stores at once
@@ -216,21 +219,25 @@ struct Block {
     int col0, cols;  // first column, columns inside the result from there
 };
 
+// (All 16 loads are under way before the first is used.)
 __device__ __forceinline__ void fetch_edge(const void *p, long long ld, int dtype, const Block &b,
                                            unsigned (&raw)[kChunk]) {
-    const int lane = threadIdx.x & 31, c = lane & 15;
-    const long long at = (long long)(b.row0 + (lane >> 4)) * ld + b.col0 + c;
+    const int lane = threadIdx.x & 31, c = lane & 15, r = lane >> 4;
+    const long long at = (long long)(b.row0 + r) * ld + b.col0 + c;
+    const int rows = c < b.cols ? b.rows - r : 0;
+    if (dtype == PDR_F32) {
+        const float *q = static_cast<const float *>(p) + at;
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-        float x = 0.0f;
-        if (2 * i + (lane >> 4) < b.rows && c < b.cols)
-            x = img_load(p, (size_t)(at + 2 * i * ld), dtype);
-        raw[i] = __float_as_uint(x);
+        for (int i = 0; i < kChunk; ++i) raw[i] = 2 * i < rows ? __float_as_uint(__ldg(q + 2 * i * ld)) : 0;
+    } else {
+        const unsigned short *q = static_cast<const unsigned short *>(p) + at;
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) raw[i] = 2 * i < rows ? __ldg(q + 2 * i * ld) : 0;
     }
 }
 // Place of a value in the transposing buffer (16 floats a row, without bank conflicts).
 __device__ __forceinline__ int buffer_at(int r, int c) { return r * kChunk + (c ^ (r & 15)); }
-__device__ __forceinline__ void unpack_edge(float *buffer, const unsigned (&raw)[kChunk],
+__device__ __forceinline__ void unpack_edge(float *buffer, int dtype, const unsigned (&raw)[kChunk],
                                             float (&v)[kChunk]) {
     const int lane = threadIdx.x & 31;
     __syncwarp();
@@ -240,6 +247,13 @@ __device__ __forceinline__ void unpack_edge(float *buffer, const unsigned (&raw)
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < kChunk; ++j) v[j] = buffer[buffer_at(lane, j)];
+    if (dtype == PDR_F16) {
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) v[j] = unpack2(__float_as_uint(v[j]), PDR_F16).x;
+    } else if (dtype == PDR_BF16) {
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) v[j] = unpack2(__float_as_uint(v[j]), PDR_BF16).x;
+    }
 }
 __device__ __forceinline__ void write_edge(void *p, long long ld, int dtype, const Block &b,
                                            float *buffer, const float (&v)[kChunk]) {
@@ -248,12 +262,21 @@ __device__ __forceinline__ void write_edge(void *p, long long ld, int dtype, con
 #pragma unroll
     for (int j = 0; j < kChunk; ++j) buffer[buffer_at(lane, j)] = v[j];
     __syncwarp();
-    const long long at = (long long)(b.row0 + (lane >> 4)) * ld + b.col0 + c;
+    const int r = lane >> 4, rows = c < b.cols ? b.rows - r : 0;
+    const long long at = (long long)(b.row0 + r) * ld + b.col0 + c;
+    float x[kChunk];
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-        const int r = 2 * i + (lane >> 4);
-        if (r < b.rows && c < b.cols)
-            img_store(p, (size_t)(at + 2 * i * ld), dtype, buffer[buffer_at(r, c)]);
+    for (int i = 0; i < kChunk; ++i) x[i] = buffer[buffer_at(2 * i + r, c)];
+    if (dtype == PDR_F32) {
+        float *q = static_cast<float *>(p) + at;
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+            if (2 * i < rows) q[2 * i * ld] = x[i];
+    } else {
+        unsigned short *q = static_cast<unsigned short *>(p) + at;
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+            if (2 * i < rows) q[2 * i * ld] = half_bits(x[i], dtype);
     }
 }
 
@@ -676,7 +699,7 @@ __device__ __forceinline__ bool epilogue_any(const GemmParams &p, const Tile &t,
             if (p.in_vec && c + kChunk <= ncols)
                 unpack_row(p.in_dtype, raw, x);
             else
-                unpack_edge(buffer, raw, x);
+                unpack_edge(buffer, p.in_dtype, raw, x);
             if (c + kChunk < c1) fetch(c + kChunk);
         }
         if (p.fp8) {
@@ -971,17 +994,43 @@ __global__ void __launch_bounds__(256) k_pack(const T *__restrict__ from, long l
         for (int c = lane; c < cols; c += 32) to[r * ld + c] = from[r * cols + c];
 }
 
-__global__ void __launch_bounds__(256) k_join(const float *__restrict__ part, int splits,
-                                              long long stride, long long n, void *to, void *to2,
+// Four neighbouring columns per thread; the splits are added in order, eight
+// loads under way at once.
+__global__ void __launch_bounds__(256) k_join(const float *__restrict__ part, int splits, int rows,
+                                              int cols, long long ld, void *to, void *to2,
                                               int dtype) {
     grid_dep_wait();
+    const long long n = rows * ld, stride = n * (to2 ? 2 : 1);
     part += blockIdx.y * n;
     if (blockIdx.y) to = to2;
-    const long long step = (long long)gridDim.x * 256;
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-        float s = 0.0f;
-        for (int j = 0; j < splits; ++j) s += part[j * stride + i];
-        img_store(to, (size_t)i, dtype, s);
+    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j = 0; j < splits; j += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (j + k < splits) v[k] = __ldg(reinterpret_cast<const float4 *>(part + (j + k) * stride + i));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (j + k < splits) {
+                s.x += v[k].x;
+                s.y += v[k].y;
+                s.z += v[k].z;
+                s.w += v[k].w;
+            }
+    }
+    const long long r = i / ld;
+    const int c = (int)(i - r * ld);
+    const size_t at = (size_t)(r * cols + c);
+    if (c + 4 <= cols && cols % 4 == 0 && dtype != PDR_F32 && (reinterpret_cast<uintptr_t>(to) & 7) == 0) {
+        const uint2 w = make_uint2(pack2(s.x, s.y, dtype), pack2(s.z, s.w, dtype));
+        *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(to) + at) = w;
+    } else {
+        const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (c + k < cols) img_store(to, at + k, dtype, v[k]);
     }
 }
 
@@ -1098,9 +1147,18 @@ unsigned long long smem_desc(bool mn) {
 
 template <int EPI, int ACT, bool ANY>
 cudaError_t launch_as(const GemmParams &p, int grid, size_t smem, cudaStream_t s) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        k_gemm<EPI, ACT, ANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // The kernel's shared-memory limit, raised once per device.
+    static std::atomic<unsigned long long> raised{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev > 63 || !(raised.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(k_gemm<EPI, ACT, ANY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSmemBytes);
+        if (e != cudaSuccess) return e;
+        raised.fetch_or(bit, std::memory_order_release);
+    }
     return launch_dependent(k_gemm<EPI, ACT, ANY>, dim3((unsigned)grid), dim3(kThreads), smem, s, p);
 }
 template <int EPI, int ACT>
@@ -1221,7 +1279,7 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
             return cudaErrorInvalidValue;
     p.colsum = g.colsum;
     const size_t fixed = 1024 + 512 + kEpiWarps * (3 * kMaxCols * 4 + kBufferBytes);
-    const size_t room = 227 * 1024 - fixed, all_b = (size_t)p.kb * p.b_bytes;
+    const size_t room = kSmemBytes - fixed, all_b = (size_t)p.kb * p.b_bytes;
     const int pairs = p.tiles < kSMs / 2 ? p.tiles : kSMs / 2;
     // B stays where it leaves room for three stages of A and a pair has several
     // tiles to use it for.
@@ -1252,11 +1310,11 @@ cudaError_t launch_pack(const void *from, long long rows, long long cols, int by
                             static_cast<unsigned short *>(to), ld_to);
 }
 
-cudaError_t launch_join(const float *part, int splits, long long stride, long long n, void *to,
+cudaError_t launch_join(const float *part, int splits, int rows, int cols, long long ld, void *to,
                         void *to2, int dtype, cudaStream_t s) {
-    const long long blocks = (n + 255) / 256;
-    return launch_dependent(k_join, dim3((unsigned)(blocks < 8 * kSMs ? blocks : 8 * kSMs), to2 ? 2 : 1),
-                            dim3(256), 0, s, part, splits, stride, n, to, to2, dtype);
+    const long long blocks = (rows * ld / 4 + 255) / 256;
+    return launch_dependent(k_join, dim3((unsigned)blocks, to2 ? 2 : 1), dim3(256), 0, s, part, splits,
+                            rows, cols, ld, to, to2, dtype);
 }
 
 cudaError_t launch_join_columns(const float *part, long long rows, long long cols, void *to,

@@ -179,9 +179,10 @@ cudaError_t read_wait_error(int *bits, cudaStream_t s);
 // Rows of `cols` elements (16 bits or 8) copied to rows of `ld_to` elements.
 cudaError_t launch_pack(const void *from, long long rows, long long cols, int bytes, void *to,
                         long long ld_to, cudaStream_t s);
-// to[i] = sum_s part[s * stride + i], i < n, rounded once to `dtype`; and
-// to2[i] the same of part + n where there is a second result.
-cudaError_t launch_join(const float *part, int splits, long long stride, long long n, void *to,
+// to[r][c] = sum over the splits of part[split][r][c], rounded once to `dtype`;
+// partial rows are ld floats apart (a multiple of 4), results dense.  With a
+// second result the splits are part[split][2][rows][ld].
+cudaError_t launch_join(const float *part, int splits, int rows, int cols, long long ld, void *to,
                         void *to2, int dtype, cudaStream_t s);
 // Column sums of part[rows][cols] (rows in order within fixed groups) to `dtype`.
 cudaError_t launch_join_columns(const float *part, long long rows, long long cols, void *to,

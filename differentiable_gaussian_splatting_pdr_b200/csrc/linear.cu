@@ -24,7 +24,7 @@ namespace {
 
 struct LinearLayout {
     size_t x, w, dz, colsum, part, total;
-    long long ldk, ldz, sum_rows;
+    long long ldk, ldz, ldp, sum_rows;  // rows of x and W, of dz, of partial dW
     bool pack, cast;
     int splits;
 };
@@ -62,8 +62,9 @@ LinearLayout bwd_layout(int M, int N, int K, int dtype, int grad_dtype, int act)
     L.colsum = L.total;
     L.total += align256((size_t)L.sum_rows * N * 4);
     L.splits = gemm_splits(N, K, 1, M);
+    L.ldp = round_up(K, 4);  // 16 bytes, for TMA stores
     L.part = L.total;
-    if (L.splits > 1) L.total += align256((size_t)L.splits * N * K * 4);
+    if (L.splits > 1) L.total += align256((size_t)L.splits * N * L.ldp * 4);
     return L;
 }
 
@@ -241,15 +242,16 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
         if (L.splits > 1) {
             g.out = ws + L.part;
             g.out_dtype = PDR_F32;
-            g.out_split = (long long)N * K;
+            g.ldo = L.ldp;
+            g.out_split = N * L.ldp;
         } else {
             g.out = grad_weight;
             g.out_dtype = dtype;
         }
         e = launch_gemm(g, s);
         if (e == cudaSuccess && L.splits > 1)
-            e = launch_join(reinterpret_cast<float *>(ws + L.part), L.splits, (long long)N * K,
-                            (long long)N * K, grad_weight, nullptr, dtype, s);
+            e = launch_join(reinterpret_cast<float *>(ws + L.part), L.splits, N, K, L.ldp, grad_weight,
+                            nullptr, dtype, s);
     }
     return done(e);
 }

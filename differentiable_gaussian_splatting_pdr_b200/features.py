@@ -28,23 +28,35 @@ ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 _E4M3 = torch.float8_e4m3fn
 _HALF = (torch.float16, torch.bfloat16)
 _TYPE = {**_DTYPES, _E4M3: 3}
+_FLOAT = tuple(_DTYPES)
+_OPERAND = (*_HALF, _E4M3)
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # without the Stream object of torch.cuda.current_stream
+_functions = {}
+
+
+def _function(name: str):
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(_lib.load(), name)
+    return f
 
 
 def _call(name: str, device: torch.device, *args) -> None:
     """One library call on the current stream of `device`, with it current."""
-    f = getattr(_lib.load(), name)
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        status = f(*args, stream)
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = _function(name)(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            status = f(*args, stream)
+            status = _function(name)(*args, _raw_stream(index))
     if status:
         _lib.check(name, status)
 
 
 def _bytes(name: str, *args) -> int:
-    return getattr(_lib.load(), name)(*args)
+    return _function(name)(*args)
 
 
 def _workspace(n: int, device: torch.device):
@@ -67,6 +79,9 @@ def _act(activation: str) -> int:
 
 
 def _check(t, what: str, dtypes, shape=None, device=None):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous() and \
+            (shape is None or t.shape == shape) and (device is None or t.device == device):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % what)
     if t.dtype not in dtypes:
@@ -75,8 +90,7 @@ def _check(t, what: str, dtypes, shape=None, device=None):
         raise ValueError("%s must be %s, got %s" % (what, list(shape), list(t.shape)))
     if device is not None and t.device != device:
         raise ValueError("%s must be on %s like the first tensor, got %s" % (what, device, t.device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % what)
+    raise ValueError("%s must be contiguous" % what)
 
 
 def _check_rows(t, what: str, dtypes):
@@ -122,7 +136,7 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     [..., N] has out_dtype (float32, float16 or bfloat16; by default x's type, or
     bfloat16 for 8-bit operands)."""
     act = _act(activation)
-    M, K = _check_rows(x, "x", (*_HALF, _E4M3))
+    M, K = _check_rows(x, "x", _OPERAND)
     dev = x.device
     _check(weight, "weight", (x.dtype,), device=dev)
     if weight.dim() != 2 or weight.shape[1] != K or weight.shape[0] < 1:
@@ -135,7 +149,7 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
         raise ValueError("out_dtype must be float32, float16 or bfloat16")
     shape = (*x.shape[:-1], N)
     if bias is not None:
-        _check(bias, "bias", tuple(_DTYPES), (N,), dev)
+        _check(bias, "bias", _FLOAT, (N,), dev)
     if residual is not None:
         _check(residual, "residual", (out_dtype,), torch.Size(shape), dev)
     y = _out(out, shape, out_dtype, dev)
@@ -162,9 +176,9 @@ def linear_bwd(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, bias: 
     if weight.dim() != 2 or weight.shape[1] != K or weight.shape[0] < 1:
         raise ValueError("weight must be [N, %d], got %s" % (K, list(weight.shape)))
     N = weight.shape[0]
-    _check(grad, "grad", tuple(_DTYPES), torch.Size((*x.shape[:-1], N)), dev)
+    _check(grad, "grad", _FLOAT, torch.Size((*x.shape[:-1], N)), dev)
     if bias is not None:
-        _check(bias, "bias", tuple(_DTYPES), (N,), dev)
+        _check(bias, "bias", _FLOAT, (N,), dev)
     dx = torch.empty_like(x) if need[0] else None
     dw = torch.empty_like(weight) if need[1] else None
     db = torch.empty_like(bias) if bias is not None and need[2] else None
@@ -218,7 +232,7 @@ def gated_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activat
     float16, bfloat16, or float8_e4m3fn with the scales (x's rows, [F], [F]).
     out_dtype: x's type, or bfloat16 for 8-bit operands, unless given."""
     act = _act(activation)
-    M, D, F = _check_gated(x, w_gate, w_up, (*_HALF, _E4M3))
+    M, D, F = _check_gated(x, w_gate, w_up, _OPERAND)
     dev = x.device
     _check_scales(x, (w_gate, w_up), x_scale, (gate_scale, up_scale), M)
     if out_dtype is None:
@@ -275,7 +289,7 @@ def gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activation:
 
 
 def _check_norm(x, weight):
-    M, D = _check_rows(x, "x", tuple(_DTYPES))
+    M, D = _check_rows(x, "x", _FLOAT)
     _check(weight, "weight", tuple({x.dtype, torch.float32}), (D,), x.device)
     return M, D
 
@@ -352,7 +366,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
 
 def quantize_rows(x: torch.Tensor):
     """(q, scale): x [..., D] as float8_e4m3fn and one fp32 scale per row, q * scale[..., None] ~ x."""
-    M, D = _check_rows(x, "x", tuple(_DTYPES))
+    M, D = _check_rows(x, "x", _FLOAT)
     q = torch.empty(x.shape, dtype=_E4M3, device=x.device)
     scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     _call("pdr_quantize_rows", x.device, x.data_ptr(), _TYPE[x.dtype], M, D, q.data_ptr(), scale.data_ptr())
