@@ -10,8 +10,10 @@
 // forms rstd again from the row it reads anyway (nothing is saved), and keeps
 // dw of its columns in registers over all rows of a block: one partial row
 // per block, added in block order (bitwise reproducible).  Everything is
-// bound by memory traffic.
+// bound by memory traffic: the next row's loads are under way while a row is
+// computed.
 #include <cuda_fp8.h>
+#include <stdint.h>
 
 #include "gemm.cuh"
 
@@ -19,6 +21,7 @@ namespace pdr {
 namespace {
 
 constexpr int kPer = 16;              // row elements per thread
+constexpr int kFwdPerSm = 3, kBwdPerSm = 2;  // blocks of 256 threads per SM
 constexpr float kE4M3Max = 448.0f;    // largest finite e4m3 value
 constexpr float kMinScale = 1.17549435082228751e-38f;  // 2^-126
 
@@ -43,39 +46,110 @@ struct NormBwdArgs {
     int D, T;
 };
 
-// The elements that thread t of a row's T threads holds: vectors of E
-// neighbours, T vectors apart (E = 1: single elements, any alignment).
+// A row as its T threads share it: vectors of E neighbours (16 bytes), T vectors
+// apart.  Rows whose length is no multiple of 16 bytes (SHIFT) start `shift`
+// elements into a vector; the vectors at their ends belong to the neighbouring
+// rows too.  A thread's rows are a multiple of 8 apart, so that its shift, and
+// hence its columns, stay the same.
+template <int E, bool SHIFT>
+struct Row {
+    int D, t, T, shift;
+    long long total;  // elements of the tensor
+    __device__ __forceinline__ int column(int j) const {  // of the thread's element j
+        const int c = ((j / E) * T + t) * E + j % E;
+        return SHIFT ? c - shift : c;
+    }
+    __device__ __forceinline__ bool inside(int c) const {
+        return (!SHIFT || c >= 0) && c < D;
+    }
+};
+
+// A thread's share of a row as it lies in memory.
 template <int E>
-__device__ __forceinline__ int element(int j, int t, int T) {
-    return ((j / E) * T + t) * E + j % E;
+struct Raw {
+    unsigned w[E == 8 ? kPer / 2 : kPer];
+};
+
+// 16 bytes where `on`, else zeros.  (volatile: the compiler leaves it where it is,
+// ahead of the row's arithmetic; predicated: without a branch around each load.)
+__device__ __forceinline__ uint4 load16(bool on, const void *p) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n"
+        " @p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+        : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w)
+        : "l"(p), "r"((unsigned)on));
+    return u;
+}
+
+template <int E, bool SHIFT>
+__device__ __forceinline__ void fetch(Raw<E> &raw, const void *p, long long row, bool on,
+                                      const Row<E, SHIFT> &q) {
+    const long long at = row * q.D;
+#pragma unroll
+    for (int j = 0; j < kPer; j += E) {
+        const int c = q.column(j);
+        const bool some = on && c < q.D && (!SHIFT || c > -E);  // some of it is of the row
+        const bool whole = !SHIFT || at + c + E <= q.total;
+        uint4 u = load16(some && whole, static_cast<const char *>(p) + (at + c) * (E == 8 ? 2 : 4));
+        if (SHIFT && some && !whole) {  // the tensor's last elements
+            unsigned w[4] = {};
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (q.inside(c + i)) {
+                    if constexpr (E == 8)
+                        w[i / 2] |= (unsigned)static_cast<const unsigned short *>(p)[at + c + i] << (16 * (i & 1));
+                    else
+                        w[i] = static_cast<const unsigned *>(p)[at + c + i];
+                }
+            u = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        raw.w[4 * (j / E)] = u.x;
+        raw.w[4 * (j / E) + 1] = u.y;
+        raw.w[4 * (j / E) + 2] = u.z;
+        raw.w[4 * (j / E) + 3] = u.w;
+    }
 }
 
 template <int E>
-__device__ __forceinline__ void load_row(const void *p, size_t at, int D, int t, int T, int dtype,
-                                         float (&v)[kPer]) {
+__device__ __forceinline__ void unpack(const Raw<E> &raw, int dtype, float (&v)[kPer]) {
+    if constexpr (E == 4) {
 #pragma unroll
-    for (int j = 0; j < kPer; j += E) {
-        const int c = element<E>(j, t, T);
-        if (c < D) {
-            if constexpr (E == 1) {
-                v[j] = img_load(p, at + c, dtype);
-            } else if constexpr (E == 4) {
-                const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at + c));
-                v[j] = f.x; v[j + 1] = f.y; v[j + 2] = f.z; v[j + 3] = f.w;
-            } else {
-                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(p) + at + c));
-                const unsigned w[4] = {u.x, u.y, u.z, u.w};
+        for (int j = 0; j < kPer; ++j) v[j] = __uint_as_float(raw.w[j]);
+    } else if (dtype == PDR_F16) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = unpack2(w[i], dtype);
-                    v[j + 2 * i] = f.x;
-                    v[j + 2 * i + 1] = f.y;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i) v[j + i] = 0.0f;
+        for (int j = 0; j < kPer / 2; ++j) {
+            const float2 f = unpack2(raw.w[j], PDR_F16);
+            v[2 * j] = f.x;
+            v[2 * j + 1] = f.y;
         }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPer / 2; ++j) {
+            const float2 f = unpack2(raw.w[j], PDR_BF16);
+            v[2 * j] = f.x;
+            v[2 * j + 1] = f.y;
+        }
+    }
+}
+
+// Zeroes what is of the neighbouring rows.
+template <int E, bool SHIFT>
+__device__ __forceinline__ void keep_row(float (&v)[kPer], const Row<E, SHIFT> &q) {
+    if constexpr (SHIFT) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (!q.inside(q.column(j))) v[j] = 0.0f;
+    }
+}
+
+template <int E, bool SHIFT>
+__device__ __forceinline__ void load_weight(const void *w, int w_dtype, const Row<E, SHIFT> &q,
+                                            float (&v)[kPer]) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int c = q.column(j);
+        v[j] = q.inside(c) ? img_load(w, c, w_dtype) : 0.0f;
     }
 }
 
@@ -83,42 +157,71 @@ __device__ __forceinline__ unsigned short e4m3x2(float a, float b) {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-template <int E>
-__device__ __forceinline__ void store_row(void *p, size_t at, int D, int t, int T, int dtype,
-                                          const float (&v)[kPer]) {
+template <int BYTES>
+__device__ __forceinline__ void store_if(bool on, void *p, unsigned w) {
+    if constexpr (BYTES == 4)
+        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n @p st.global.u32 [%0], %1;\n}" ::"l"(p),
+                     "r"(w), "r"((unsigned)on)
+                     : "memory");
+    else if constexpr (BYTES == 2)
+        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n @p st.global.u16 [%0], %1;\n}" ::"l"(p),
+                     "h"((unsigned short)w), "r"((unsigned)on)
+                     : "memory");
+    else
+        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n @p st.global.u8 [%0], %1;\n}" ::"l"(p),
+                     "r"(w), "r"((unsigned)on)
+                     : "memory");
+}
+
+// (8-bit rows are shifted like wider ones: a vector of E of their elements starts
+// at a multiple of E bytes.)
+template <int E, bool SHIFT>
+__device__ __forceinline__ void store_row(void *p, long long row, bool on, const Row<E, SHIFT> &q,
+                                          int dtype, const float (&v)[kPer]) {
+    const long long at = row * q.D;
 #pragma unroll
     for (int j = 0; j < kPer; j += E) {
-        const int c = element<E>(j, t, T);
-        if (c >= D) continue;
-        if constexpr (E == 1) {
-            if (dtype == PDR_E4M3)
-                static_cast<unsigned char *>(p)[at + c] = (unsigned char)e4m3x2(v[j], 0.0f);
-            else
-                img_store(p, at + c, dtype, v[j]);
-        } else if (dtype == PDR_E4M3) {
+        const int c = q.column(j);
+        const bool whole = on && (SHIFT ? c >= 0 && c + E <= q.D : c < q.D);
+        const bool edge = SHIFT && on && !whole && c < q.D && c > -E;
+        if (dtype == PDR_E4M3) {
             unsigned w[2] = {};
 #pragma unroll
             for (int i = 0; i < E / 2; ++i)
                 w[i / 2] |= (unsigned)e4m3x2(v[j + 2 * i], v[j + 2 * i + 1]) << (16 * (i & 1));
-            unsigned char *q = static_cast<unsigned char *>(p) + at + c;
-            if constexpr (E == 8)
-                *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
-            else
-                *reinterpret_cast<unsigned *>(q) = w[0];
-        } else if (dtype == PDR_F32) {
+            unsigned char *o = static_cast<unsigned char *>(p) + at + c;
+            if (whole) {
+                if constexpr (E == 8)
+                    *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+                else
+                    *reinterpret_cast<unsigned *>(o) = w[0];
+            }
+            if (edge)
 #pragma unroll
-            for (int i = 0; i < E; i += 4)
-                *reinterpret_cast<float4 *>(static_cast<float *>(p) + at + c + i) =
-                    make_float4(v[j + i], v[j + i + 1], v[j + i + 2], v[j + i + 3]);
+                for (int i = 0; i < E; ++i)
+                    store_if<1>(q.inside(c + i), o + i, w[i / 4] >> (8 * (i & 3)) & 255);
         } else {
-            unsigned w[E / 2];
+            unsigned w[4];
+            if constexpr (E == 4) {
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) w[i] = pack2(v[j + 2 * i], v[j + 2 * i + 1], dtype);
-            unsigned short *q = static_cast<unsigned short *>(p) + at + c;
-            if constexpr (E == 8)
-                *reinterpret_cast<uint4 *>(q) = make_uint4(w[0], w[1], w[2], w[3]);
-            else
-                *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
+                for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[j + i]);
+            } else if (dtype == PDR_F16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = pack2(v[j + 2 * i], v[j + 2 * i + 1], PDR_F16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = pack2(v[j + 2 * i], v[j + 2 * i + 1], PDR_BF16);
+            }
+            char *o = static_cast<char *>(p) + (at + c) * (16 / E);
+            if (whole) *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (edge)
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    if constexpr (E == 4)
+                        store_if<4>(q.inside(c + i), o + 4 * i, w[i]);
+                    else
+                        store_if<2>(q.inside(c + i), o + 2 * i, w[i / 2] >> (16 * (i & 1)));
+                }
         }
     }
 }
@@ -144,43 +247,63 @@ __device__ __forceinline__ float row_reduce(float v, int T, float *red) {
     return v;
 }
 
-template <int E>
-__global__ void __launch_bounds__(1024) k_rms_norm(const NormArgs a) {
+// Blocks have 256 threads for rows of at most 4096 elements, 512 or 1024 for wider
+// ones.  The next row is fetched ahead, but for blocks of 1024 threads, which have
+// too few registers.
+template <int THREADS>
+constexpr bool kAhead = THREADS < 1024;
+
+template <int E, bool SHIFT>
+__device__ __forceinline__ Row<E, SHIFT> make_row(long long row, long long M, int D, int T) {
+    Row<E, SHIFT> q;
+    q.D = D;
+    q.T = T;
+    q.t = threadIdx.x & (T - 1);
+    q.shift = SHIFT ? (int)(row * D & (E - 1)) : 0;
+    q.total = M * D;
+    return q;
+}
+
+template <int E, bool SHIFT, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : kFwdPerSm) k_rms_norm(const NormArgs a) {
     __shared__ float red[32];
     grid_dep_wait();
-    const int T = a.T, t = threadIdx.x & (T - 1), per_block = blockDim.x / T;
-    const int D = a.D;
+    const int T = a.T, per_block = blockDim.x / T;
+    const long long step = (long long)gridDim.x * per_block;
+    long long row = (long long)blockIdx.x * per_block + threadIdx.x / T;
+    const Row<E, SHIFT> q = make_row<E, SHIFT>(row, a.M, a.D, T);
     float w[kPer];
-    if (a.w) {
-        if (a.w_dtype == a.dtype)
-            load_row<E>(a.w, 0, D, t, T, a.dtype, w);
-        else  // fp32 weights of 16-bit rows
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const int c = element<E>(j, t, T);
-                w[j] = c < D ? img_load(a.w, c, a.w_dtype) : 0.0f;
-            }
+    if (a.w) load_weight(a.w, a.w_dtype, q, w);
+    Raw<E> x, r, next_x, next_r;
+    if constexpr (kAhead<THREADS>) {  // (nothing of rows behind the last)
+        fetch(x, a.x, row, row < a.M, q);
+        if (a.r) fetch(r, a.r, row, row < a.M, q);
     }
-    for (long long base = (long long)blockIdx.x * per_block; base < a.M;
-         base += (long long)gridDim.x * per_block) {
-        const long long row = base + threadIdx.x / T;
-        const int d = row < a.M ? D : 0;  // nothing of rows behind the last
-        const size_t at = (size_t)row * D;
-        float v[kPer];
-        load_row<E>(a.x, at, d, t, T, a.dtype, v);
-        if (a.r) {
-            float r[kPer];
-            load_row<E>(a.r, at, d, t, T, a.dtype, r);
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) v[j] += r[j];
-            if (a.s) store_row<E>(a.s, at, d, t, T, a.dtype, v);
+    for (long long base = (long long)blockIdx.x * per_block; base < a.M; base += step, row += step) {
+        const bool on = row < a.M;
+        if constexpr (kAhead<THREADS>) {
+            fetch(next_x, a.x, row + step, row + step < a.M, q);
+            if (a.r) fetch(next_r, a.r, row + step, row + step < a.M, q);
+        } else {
+            fetch(x, a.x, row, on, q);
+            if (a.r) fetch(r, a.r, row, on, q);
         }
+        float v[kPer];
+        unpack<E>(x, a.dtype, v);
+        if (a.r) {
+            float f[kPer];
+            unpack<E>(r, a.dtype, f);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) v[j] += f[j];
+            if (a.s) store_row(a.s, row, on, q, a.dtype, v);
+        }
+        keep_row(v, q);
         if (a.w) {
             float ss = 0.0f;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) ss = fmaf(v[j], v[j], ss);
             ss = row_reduce<false>(ss, T, red);
-            const float rstd = rsqrtf(ss / (float)D + a.eps);
+            const float rstd = rsqrtf(ss / (float)a.D + a.eps);
 #pragma unroll
             for (int j = 0; j < kPer; ++j) v[j] *= rstd * w[j];
         }
@@ -192,43 +315,55 @@ __global__ void __launch_bounds__(1024) k_rms_norm(const NormArgs a) {
             const float scale = max_nan(m / kE4M3Max, kMinScale), inv = 1.0f / scale;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) v[j] *= inv;
-            if (t == 0 && d) a.scale[row] = scale;
+            if (q.t == 0 && on) a.scale[row] = scale;
         }
-        store_row<E>(a.y, at, d, t, T, a.y_dtype, v);
+        store_row(a.y, row, on, q, a.y_dtype, v);
+        if constexpr (kAhead<THREADS>) {
+            x = next_x;
+            r = next_r;
+        }
     }
 }
 
-template <int E>
-__global__ void __launch_bounds__(1024) k_rms_norm_bwd(const NormBwdArgs a) {
-    extern __shared__ float part[];  // [rows of a block][T * kPer] when there are several
+template <int E, bool SHIFT, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : kBwdPerSm)
+    k_rms_norm_bwd(const NormBwdArgs a) {
+    extern __shared__ float part[];  // [rows of a block][D] when there are several
     __shared__ float red[32];
     grid_dep_wait();
-    const int T = a.T, t = threadIdx.x & (T - 1), per_block = blockDim.x / T;
-    const int D = a.D;
+    const int T = a.T, per_block = blockDim.x / T;
+    const long long step = (long long)gridDim.x * per_block;
+    long long row = (long long)blockIdx.x * per_block + threadIdx.x / T;
+    const Row<E, SHIFT> q = make_row<E, SHIFT>(row, a.M, a.D, T);
     float w[kPer], dw[kPer];
-    if (a.w_dtype == a.dtype)
-        load_row<E>(a.w, 0, D, t, T, a.dtype, w);
-    else
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int c = element<E>(j, t, T);
-            w[j] = c < D ? img_load(a.w, c, a.w_dtype) : 0.0f;
-        }
+    load_weight(a.w, a.w_dtype, q, w);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) dw[j] = 0.0f;
-    for (long long base = (long long)blockIdx.x * per_block; base < a.M;
-         base += (long long)gridDim.x * per_block) {
-        const long long row = base + threadIdx.x / T;
-        const int d = row < a.M ? D : 0;
-        const size_t at = (size_t)row * D;
+    Raw<E> s, dy, ds, next_s, next_dy;
+    if constexpr (kAhead<THREADS>) {
+        fetch(s, a.s, row, row < a.M, q);
+        fetch(dy, a.dy, row, row < a.M, q);
+    }
+    for (long long base = (long long)blockIdx.x * per_block; base < a.M; base += step, row += step) {
+        const bool on = row < a.M;
+        if constexpr (kAhead<THREADS>) {
+            if (a.ds) fetch(ds, a.ds, row, on, q);  // needed last
+            fetch(next_s, a.s, row + step, row + step < a.M, q);
+            fetch(next_dy, a.dy, row + step, row + step < a.M, q);
+        } else {
+            fetch(s, a.s, row, on, q);
+            fetch(dy, a.dy, row, on, q);
+        }
         float v[kPer], g[kPer];
-        load_row<E>(a.s, at, d, t, T, a.dtype, v);
-        load_row<E>(a.dy, at, d, t, T, a.dtype, g);
+        unpack<E>(s, a.dtype, v);
+        unpack<E>(dy, a.dtype, g);
+        keep_row(v, q);
+        keep_row(g, q);
         float ss = 0.0f;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) ss = fmaf(v[j], v[j], ss);
         ss = row_reduce<false>(ss, T, red);
-        const float rstd = rsqrtf(ss / (float)D + a.eps);
+        const float rstd = rsqrtf(ss / (float)a.D + a.eps);
         float dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
@@ -237,33 +372,36 @@ __global__ void __launch_bounds__(1024) k_rms_norm_bwd(const NormBwdArgs a) {
             g[j] *= w[j];
             dot = fmaf(g[j], v[j], dot);
         }
-        dot = row_reduce<false>(dot, T, red) / (float)D;
+        dot = row_reduce<false>(dot, T, red) / (float)a.D;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) g[j] = rstd * fmaf(-v[j], dot, g[j]);
         if (a.ds) {
-            load_row<E>(a.ds, at, d, t, T, a.dtype, v);
+            if constexpr (!kAhead<THREADS>) fetch(ds, a.ds, row, on, q);
+            unpack<E>(ds, a.dtype, v);
 #pragma unroll
             for (int j = 0; j < kPer; ++j) g[j] += v[j];
         }
-        if (a.dx) store_row<E>(a.dx, at, d, t, T, a.dtype, g);
+        if (a.dx) store_row(a.dx, row, on, q, a.dtype, g);
+        if constexpr (kAhead<THREADS>) {
+            s = next_s;
+            dy = next_dy;
+        }
     }
     if (!a.dw) return;
     // The block's rows, in order; then one partial row per block.
-    const int width = T * kPer, sub = threadIdx.x / T;
-    if (per_block > 1) {
+    const int D = a.D, sub = threadIdx.x / T;
+    float *to = per_block > 1 ? part + sub * D : a.dw + (size_t)blockIdx.x * D;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) part[sub * width + element<E>(j, t, T)] = dw[j];
+    for (int j = 0; j < kPer; ++j) {
+        const int c = q.column(j);
+        if (q.inside(c)) to[c] = dw[j];
+    }
+    if (per_block > 1) {
         __syncthreads();
         for (int c = threadIdx.x; c < D; c += blockDim.x) {
             float s = 0.0f;
-            for (int i = 0; i < per_block; ++i) s += part[i * width + c];
+            for (int i = 0; i < per_block; ++i) s += part[i * D + c];
             a.dw[(size_t)blockIdx.x * D + c] = s;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int c = element<E>(j, t, T);
-            if (c < D) a.dw[(size_t)blockIdx.x * D + c] = dw[j];
         }
     }
 }
@@ -273,41 +411,47 @@ bool float_type(int t) { return t == PDR_F32 || half_type(t); }
 
 // Threads per row, block size and blocks for M rows of D elements.
 struct NormShape {
+    bool shift;
     int T, threads, blocks;
 };
-NormShape norm_shape(long long M, int D, int per_sm) {
+NormShape norm_shape(long long M, int D, int bytes, int per_sm) {  // per_sm: blocks of 256 threads
     NormShape n;
+    const int E = 16 / bytes;
+    n.shift = D % E != 0;
     n.T = 1;
-    while (n.T * kPer < D) n.T *= 2;
+    while (n.T * kPer < D + (n.shift ? E - 1 : 0)) n.T *= 2;
     n.threads = n.T > 256 ? n.T : 256;
     const long long per_block = n.threads / n.T, need = (M + per_block - 1) / per_block;
-    long long most = (long long)kSMs * per_sm * 256 / n.threads;
-    if (most < kSMs) most = kSMs;
+    long long most = n.threads > 256 ? kSMs : kSMs * per_sm;
+    if (n.shift && need > most && per_block < 8)  // a thread's rows 8 apart
+        most = most * per_block / 8 * 8 / per_block;
     n.blocks = (int)(need < most ? need : most);
     return n;
 }
-constexpr int kFwdPerSm = 8, kBwdPerSm = 4;  // blocks of 256 threads per SM
 
-// Every row of each of the tensors starts at a multiple of 16 bytes.
-bool rows_aligned(std::initializer_list<const void *> ps, int D, int dtype) {
-    for (const void *p : ps)
-        if (!aligned_to(p, 16)) return false;
-    return (long long)D * dtype_bytes(dtype) % 16 == 0;
+template <bool BWD, int E, bool SHIFT, int THREADS>
+auto norm_kernel() {
+    if constexpr (BWD)
+        return k_rms_norm_bwd<E, SHIFT, THREADS>;
+    else
+        return k_rms_norm<E, SHIFT, THREADS>;
+}
+template <bool BWD, typename Args>
+cudaError_t launch_norm(const NormShape &n, const Args &a, size_t smem, cudaStream_t s) {
+    using Kernel = void (*)(Args);
+    static const Kernel kernels[2][2][3] = {
+        {{norm_kernel<BWD, 8, false, 256>(), norm_kernel<BWD, 8, false, 512>(), norm_kernel<BWD, 8, false, 1024>()},
+         {norm_kernel<BWD, 8, true, 256>(), norm_kernel<BWD, 8, true, 512>(), norm_kernel<BWD, 8, true, 1024>()}},
+        {{norm_kernel<BWD, 4, false, 256>(), norm_kernel<BWD, 4, false, 512>(), norm_kernel<BWD, 4, false, 1024>()},
+         {norm_kernel<BWD, 4, true, 256>(), norm_kernel<BWD, 4, true, 512>(), norm_kernel<BWD, 4, true, 1024>()}}};
+    return launch_dependent(kernels[a.dtype == PDR_F32][n.shift][n.threads / 512], dim3((unsigned)n.blocks),
+                            dim3((unsigned)n.threads), smem, s, a);
 }
 
 pdr_status run_fwd(NormArgs a, cudaStream_t s) {
-    const NormShape n = norm_shape(a.M, a.D, kFwdPerSm);
+    const NormShape n = norm_shape(a.M, a.D, dtype_bytes(a.dtype), kFwdPerSm);
     a.T = n.T;
-    const bool vec = rows_aligned({a.x, a.r, a.s, a.y, a.w_dtype == a.dtype ? a.w : nullptr}, a.D, a.dtype);
-    const dim3 grid((unsigned)n.blocks), block((unsigned)n.threads);
-    cudaError_t e;
-    if (!vec)
-        e = launch_dependent(k_rms_norm<1>, grid, block, 0, s, a);
-    else if (a.dtype == PDR_F32)
-        e = launch_dependent(k_rms_norm<4>, grid, block, 0, s, a);
-    else
-        e = launch_dependent(k_rms_norm<8>, grid, block, 0, s, a);
-    return e == cudaSuccess ? PDR_OK : PDR_ERR_CUDA;
+    return launch_norm<false>(n, a, 0, s) == cudaSuccess ? PDR_OK : PDR_ERR_CUDA;
 }
 
 bool norm_sizes(int M, int D) { return M >= 0 && D >= 1; }
@@ -330,10 +474,8 @@ pdr_status pdr_rms_norm_fwd(const void *x, const void *residual, int dtype, cons
     if (!weight || (M > 0 && (!x || !y)) || (M > 0 && (y_dtype == PDR_E4M3) != (y_scale != nullptr)) ||
         (!residual && sum))
         return PDR_ERR_INVALID_ARG;
-    const int e = dtype_bytes(dtype);
-    if (!aligned_to(x, e) || !aligned_to(residual, e) || !aligned_to(sum, e) ||
-        !aligned_to(weight, dtype_bytes(weight_dtype)) || !aligned_to(y, dtype_bytes(y_dtype)) ||
-        !aligned_to(y_scale, 4))
+    if (!aligned_to(x, 16) || !aligned_to(residual, 16) || !aligned_to(sum, 16) || !aligned_to(y, 16) ||
+        !aligned_to(weight, dtype_bytes(weight_dtype)) || !aligned_to(y_scale, 4))
         return PDR_ERR_INVALID_ARG;
     if (M == 0) return PDR_OK;
     return run_fwd({x, residual, weight, sum, y, y_scale, dtype, weight_dtype, y_dtype, eps, M, D, 0},
@@ -345,7 +487,7 @@ pdr_status pdr_quantize_rows(const void *x, int dtype, int M, int D, void *y, fl
     if (!norm_sizes(M, D) || !float_type(dtype)) return PDR_ERR_INVALID_ARG;
     if (!norm_in_limits(M, D)) return PDR_ERR_TOO_LARGE;
     if (M > 0 && (!x || !y || !y_scale)) return PDR_ERR_INVALID_ARG;
-    if (!aligned_to(x, dtype_bytes(dtype)) || !aligned_to(y_scale, 4)) return PDR_ERR_INVALID_ARG;
+    if (!aligned_to(x, 16) || !aligned_to(y, 16) || !aligned_to(y_scale, 4)) return PDR_ERR_INVALID_ARG;
     if (M == 0) return PDR_OK;
     return run_fwd({x, nullptr, nullptr, nullptr, y, y_scale, dtype, dtype, PDR_E4M3, 0.0f, M, D, 0},
                    static_cast<cudaStream_t>(stream));
@@ -353,7 +495,9 @@ pdr_status pdr_quantize_rows(const void *x, int dtype, int M, int D, void *y, fl
 
 size_t pdr_rms_norm_bwd_workspace_bytes(int M, int D) {
     if (!norm_sizes(M, D) || !norm_in_limits(M, D)) return 0;
-    return align256((size_t)norm_shape(M, D, kBwdPerSm).blocks * D * 4);
+    // (for the type that takes more blocks)
+    const int a = norm_shape(M, D, 2, kBwdPerSm).blocks, b = norm_shape(M, D, 4, kBwdPerSm).blocks;
+    return align256((size_t)(a > b ? a : b) * D * 4);
 }
 
 pdr_status pdr_rms_norm_bwd(const void *grad, const void *sum, int dtype, const void *weight,
@@ -365,9 +509,9 @@ pdr_status pdr_rms_norm_bwd(const void *grad, const void *sum, int dtype, const 
         return PDR_ERR_INVALID_ARG;
     if (!norm_in_limits(M, D)) return PDR_ERR_TOO_LARGE;
     if (!weight || (M > 0 && (!grad || !sum))) return PDR_ERR_INVALID_ARG;
-    const int e = dtype_bytes(dtype), we = dtype_bytes(weight_dtype);
-    if (!aligned_to(grad, e) || !aligned_to(sum, e) || !aligned_to(grad_sum, e) ||
-        !aligned_to(grad_x, e) || !aligned_to(weight, we) || !aligned_to(grad_weight, we))
+    const int we = dtype_bytes(weight_dtype);
+    if (!aligned_to(grad, 16) || !aligned_to(sum, 16) || !aligned_to(grad_sum, 16) ||
+        !aligned_to(grad_x, 16) || !aligned_to(weight, we) || !aligned_to(grad_weight, we))
         return PDR_ERR_INVALID_ARG;
     const size_t need = pdr_rms_norm_bwd_workspace_bytes(M, D);
     if (need && grad_weight && (!workspace || !aligned_to(workspace, 256))) return PDR_ERR_INVALID_ARG;
@@ -379,19 +523,12 @@ pdr_status pdr_rms_norm_bwd(const void *grad, const void *sum, int dtype, const 
         return err == cudaSuccess ? PDR_OK : PDR_ERR_CUDA;
     }
     if (!grad_x && !grad_weight) return PDR_OK;
-    const NormShape n = norm_shape(M, D, kBwdPerSm);
+    const NormShape n = norm_shape(M, D, dtype_bytes(dtype), kBwdPerSm);
     const NormBwdArgs a = {grad, sum, weight, grad_sum, grad_x,
                            grad_weight ? static_cast<float *>(workspace) : nullptr,
                            dtype, weight_dtype, eps, M, D, n.T};
-    const bool vec = rows_aligned({grad, sum, grad_sum, grad_x, weight_dtype == dtype ? weight : nullptr}, D, dtype);
-    const dim3 grid((unsigned)n.blocks), block((unsigned)n.threads);
-    const size_t smem = n.threads > n.T ? (size_t)n.threads * kPer * 4 : 0;  // 16 KB
-    if (!vec)
-        err = launch_dependent(k_rms_norm_bwd<1>, grid, block, smem, s, a);
-    else if (dtype == PDR_F32)
-        err = launch_dependent(k_rms_norm_bwd<4>, grid, block, smem, s, a);
-    else
-        err = launch_dependent(k_rms_norm_bwd<8>, grid, block, smem, s, a);
+    // One row of dw for each row of a block: at most 256 x 16 floats.
+    err = launch_norm<true>(n, a, n.threads > n.T ? (size_t)(n.threads / n.T) * D * 4 : 0, s);
     if (err == cudaSuccess && grad_weight)
         err = launch_join_columns(static_cast<const float *>(workspace), n.blocks, D, grad_weight,
                                   weight_dtype, s);

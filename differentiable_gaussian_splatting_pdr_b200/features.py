@@ -312,7 +312,9 @@ def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
     y = torch.empty(x.shape, dtype=out_dtype, device=dev)
     s = x if residual is None else torch.empty_like(x)
     scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if out_dtype == _E4M3 else None
-    _call("pdr_rms_norm_fwd", dev, x.data_ptr(), _ptr(residual), _TYPE[x.dtype], weight.data_ptr(),
+    rows = _aligned(x)
+    residual = None if residual is None else _aligned(residual)
+    _call("pdr_rms_norm_fwd", dev, rows.data_ptr(), _ptr(residual), _TYPE[x.dtype], weight.data_ptr(),
           _TYPE[weight.dtype], ctypes.c_float(eps), M, D, None if residual is None else s.data_ptr(),
           y.data_ptr(), _TYPE[out_dtype], _ptr(scale))
     return y, s, scale
@@ -330,6 +332,7 @@ def rms_norm_bwd(grad: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, grad
         _check(grad_s, "grad_s", (s.dtype,), s.shape, dev)
     dx = torch.empty_like(s) if need[0] else None
     dw = torch.empty_like(weight) if need[1] else None
+    grad, s, grad_s = _aligned(grad), _aligned(s), None if grad_s is None else _aligned(grad_s)
     ws, wp, wn = _workspace(_bytes("pdr_rms_norm_bwd_workspace_bytes", M, D), dev) if need[1] else (None, None, 0)
     _call("pdr_rms_norm_bwd", dev, grad.data_ptr(), s.data_ptr(), _TYPE[s.dtype], weight.data_ptr(),
           _TYPE[weight.dtype], _ptr(grad_s), ctypes.c_float(eps), M, D, _ptr(dx), _ptr(dw), wp, wn)
@@ -369,6 +372,7 @@ def quantize_rows(x: torch.Tensor):
     M, D = _check_rows(x, "x", _FLOAT)
     q = torch.empty(x.shape, dtype=_E4M3, device=x.device)
     scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    x = _aligned(x)
     _call("pdr_quantize_rows", x.device, x.data_ptr(), _TYPE[x.dtype], M, D, q.data_ptr(), scale.data_ptr())
     return q, scale
 

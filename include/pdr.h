@@ -305,9 +305,9 @@ pdr_status pdr_loss_l1_ssim(const float *image, const float *target, int B, int 
  * inputs, and are bitwise reproducible.  M = 0 is valid (gradients of weights
  * are zero then; arrays sized by M may be NULL).
  *
- * Pointers: x, weights and grad 16-byte aligned in the products (TMA reads
- * them), otherwise aligned to their element; workspaces 256-byte aligned, NULL
- * where the needed size is 0.  Rows whose length is not a multiple of 16 bytes
+ * Pointers: x, grad and the products' weights, and all rows of rms_norm and
+ * quantize_rows, 16-byte aligned; otherwise aligned to their element; workspaces
+ * 256-byte aligned, NULL where the needed size is 0.  Rows whose length is not a multiple of 16 bytes
  * are first copied to the workspace in padded form.  Violations return
  * PDR_ERR_INVALID_ARG, sizes beyond the limits PDR_ERR_TOO_LARGE, and nothing
  * is launched then.  Streams as above.  A workspace holds nothing between
