@@ -64,6 +64,7 @@ struct __align__(64) GemmParams {
     int bn, bcols, stages, nacc;      // bcols: result columns of a tile
     int sharing;                      // epilogue groups that share a tile
     int stationary;                   // B of a column of tiles stays in shared memory
+    int per_stage;                    // k blocks of a stage
     int b_bytes, kelems;              // a block's B bytes, and k, of a k block
     unsigned idesc;
     unsigned long long adesc, bdesc;  // smem descriptors without the address
@@ -496,7 +497,7 @@ __device__ __forceinline__ void load_b(const GemmParams &p, const Tile &t, int k
 // One warp's 32 rows of a tile, from column c0 to c1 (32 columns or 64).
 // `columns`: the warp's bias and column scales, [3][kMaxCols]; `have_n`: the
 // column of tiles that they are of.  Here results leave by TMA, and rows of the
-// input are aligned and a multiple of 16 wide.
+// input are full 32-byte sectors (a multiple of 16 16-bit, or 8 fp32, wide).
 template <int EPI, int ACT>
 __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t, unsigned acc,
                                               unsigned ready, unsigned phase, int c0, int c1,
@@ -516,7 +517,7 @@ __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t
     auto fetch = [&](int c) {
         const int ib = p.in_dtype == PDR_F32 ? 4 : 2;
         load8(on, in_row + c * ib, raw);
-        if (p.in_dtype == PDR_F32) load8(on, in_row + c * ib + 32, raw + 8);
+        if (p.in_dtype == PDR_F32) load8(on && n0 + c + 8 < p.N, in_row + c * ib + 32, raw + 8);
     };
     float scale_m = 1.0f;
     if (any) {  // on their way while the products finish
@@ -774,7 +775,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     extern __shared__ char raw[];
     // Tiles first, at a 1024-byte boundary (the swizzle's period).
     char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    const int stage_bytes = kABytes + (p.stationary ? 0 : p.b_bytes);
+    const int block_bytes = kABytes + (p.stationary ? 0 : p.b_bytes);  // of a k block
+    const int stage_bytes = p.per_stage * block_bytes;
     char *held = smem + p.stages * stage_bytes;  // B of all k, where it stays
     char *after = held + (p.stationary ? p.kb * p.b_bytes : 0);
     float *buffers = reinterpret_cast<float *>(after);  // one per epilogue warp, 1024-byte aligned
@@ -873,11 +875,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int kb = 0; kb < p.kb; ++kb)
                         load_b(p, tile, kb, rank, held0 + kb * p.b_bytes, lead_b_full);
                 }
-                for (int kb = k.first; kb < k.end; ++kb) {
+                for (int kb = k.first; kb < k.end; kb += p.per_stage) {
+                    const bool two = p.per_stage == 2 && kb + 1 < k.end;
                     if (!ready) ok = bar_wait(empty + 8 * stage, phase ^ 1, abort);
                     if (!ok) break;
                     const unsigned bar = lead_full + 8 * stage, at = stages0 + stage * stage_bytes;
-                    if (rank == 0) bar_expect(full + 8 * stage, 2 * stage_bytes);
+                    if (rank == 0) bar_expect(full + 8 * stage, two ? 4 * block_bytes : 2 * block_bytes);
                     ++issued;
                     if (++stage == p.stages) {
                         stage = 0;
@@ -885,6 +888,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     ready = bar_try(empty + 8 * stage, phase ^ 1);  // asked early: the answer takes a while
                     load_a(p, tile, kb, at, bar);
+                    if (two) load_a(p, tile, kb + 1, at + kABytes, bar);
                     if (!p.stationary) load_b(p, tile, kb, rank, at + kABytes, bar);
                 }
             }
@@ -939,7 +943,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     acc_phase ^= 1;
                 }
                 bool more = false;
-                for (int kb = 0; kb < nk; ++kb) {
+                for (int kb = 0; kb < nk; kb += p.per_stage) {
                     if (!full_ready) ok = bar_wait(full + 8 * stage, phase, abort);
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -950,15 +954,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         phase ^= 1;
                     }
                     full_ready = bar_try(full + 8 * stage, phase);
-                    if (kb == nk - 1) acc_ready = bar_try(acc_empty + 8 * acc, acc_phase ^ 1);
-                    unsigned al = a_lo | (at >> 4), bl = b_lo | (bt >> 4);
+                    if (kb + p.per_stage >= nk) acc_ready = bar_try(acc_empty + 8 * acc, acc_phase ^ 1);
+                    auto block = [&](unsigned a, unsigned b) {
+                        unsigned al = a_lo | (a >> 4), bl = b_lo | (b >> 4);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        mma(d, al, a_hi, bl, b_hi, p.idesc, more, p.fp8);
-                        more = true;
-                        al += p.a_step;
-                        bl += p.b_step;
-                    }
+                        for (int j = 0; j < 4; ++j) {
+                            mma(d, al, a_hi, bl, b_hi, p.idesc, more, p.fp8);
+                            more = true;
+                            al += p.a_step;
+                            bl += p.b_step;
+                        }
+                    };
+                    block(at, bt);
+                    if (p.per_stage == 2 && kb + 1 < nk) block(at + kABytes, bt + p.b_bytes);
                     mma_commit(done);
                 }
                 if (!ok) break;
@@ -1271,7 +1279,7 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     p.ldi = g.ldi;
     p.in_vec = aligned_to(g.in, 32) && g.ldi * ib % 32 == 0;
     p.out_tma = aligned_to(g.out, 16) && aligned_to(g.out2, 16) && g.ldo * ob % 16 == 0 &&
-                (!g.in || (p.in_vec && g.N % kChunk == 0)) && !(g.epi == kEpiGated && ob == 4);
+                (!g.in || p.in_vec) && !(g.epi == kEpiGated && ob == 4);
     const int slices = g.out_split || g.out_z ? p.splits * p.nz : 1;
     for (int i = 0; p.out_tma && i < (g.out2 ? 2 : 1); ++i)
         if (!make_store_map(&p.o[i], i ? g.out2 : g.out, ob, g.M, g.N, g.ldo, slices,
@@ -1284,8 +1292,14 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     // B stays where it leaves room for three stages of A and a pair has several
     // tiles to use it for.
     p.stationary = g.splits == 1 && all_b + 3 * kABytes <= room && p.tiles >= 2 * pairs;
-    const size_t stage = kABytes + (p.stationary ? 0 : p.b_bytes);
-    p.stages = (int)((room - (p.stationary ? all_b : 0)) / stage);
+    // A stage of two k blocks, where there are as many and room for three stages,
+    // halves the waits and counts beside the copies and products: one thread takes some 700
+    // clocks for those of a stage beside a busy epilogue, as long as 16 KB take at
+    // the memory's rate.
+    const size_t left = room - (p.stationary ? all_b : 0);
+    p.per_stage = p.stationary && p.kb > 1 && left >= 6 * kABytes ? 2 : 1;
+    const size_t stage = p.per_stage * (kABytes + (p.stationary ? 0 : p.b_bytes));
+    p.stages = (int)(left / stage);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     const size_t smem = fixed + p.stages * stage + (p.stationary ? all_b : 0);
     const int grid = 2 * pairs;
