@@ -45,11 +45,11 @@ SIGNATURES = {
     "pdr_render_fwd_ex": (_i, [_vp] + [_i] * 6 + [_vp, _i, _vp, _sz, _i, _vp]),
     "pdr_render_bwd_ex": (_i, [_vp, _vp, _i] + [_i] * 6 + [_vp, _vp, _sz, _i, _vp]),
     "pdr_loss_l1_ssim": (_i, [_vp, _vp] + [_i] * 4 + [ctypes.c_float, ctypes.c_float] + [_vp] * 3 + [_sz, _vp]),
-    "pdr_linear_workspace_bytes": (_sz, [_i] * 4),
+    "pdr_linear_workspace_bytes": (_sz, [_i] * 6),
     "pdr_linear_fwd": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _i, _vp] + [_i] * 4 + [_vp, _i, _vp, _sz, _vp]),
     "pdr_linear_bwd_workspace_bytes": (_sz, [_i] * 6),
     "pdr_linear_bwd": (_i, [_vp, _i, _vp, _vp, _i, _vp] + [_i] * 5 + [_vp] * 4 + [_sz, _vp]),
-    "pdr_gated_workspace_bytes": (_sz, [_i] * 4),
+    "pdr_gated_workspace_bytes": (_sz, [_i] * 5),
     "pdr_gated_fwd": (_i, [_vp] * 3 + [_i] + [_vp] * 3 + [_i] * 4 + [_vp, _i, _vp, _sz, _vp]),
     "pdr_gated_bwd_workspace_bytes": (_sz, [_i] * 4),
     "pdr_gated_bwd": (_i, [_vp] * 4 + [_i] * 5 + [_vp] * 4 + [_sz, _vp]),

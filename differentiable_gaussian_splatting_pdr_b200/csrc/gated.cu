@@ -17,11 +17,18 @@
 namespace pdr {
 namespace {
 
+// The workspace: padded copies of what TMA or 32-byte loads cannot address,
+// padded results that are copied out at the end, dg and du, and partial sums.
 struct GatedLayout {
-    size_t x, wg, wu, dg, du, part, total;
-    long long ldk, ldf, ldp;  // rows of x and the weights, of dg and du, of partial dW
-    bool pack;
+    size_t x, wg, wu, in, out, dg, du, part, total;
+    long long ldk, ldi, ldo, ldf, ldp;
+    bool pack_x, pack_in, pack_out;
     int splits;
+    size_t take(size_t bytes) {
+        const size_t at = total;
+        total += align256(bytes);
+        return at;
+    }
 };
 
 bool sizes_ok(int M, int D, int F) { return M >= 0 && D >= 1 && F >= 1; }
@@ -30,31 +37,42 @@ bool in_limits(int M, int D, int F) {
 }
 bool half_type(int t) { return t == PDR_F16 || t == PDR_BF16; }
 bool act_ok(int act) { return act >= PDR_ACT_NONE && act <= PDR_ACT_GELU_TANH; }
-long long round_up(long long a, long long b) { return (a + b - 1) / b * b; }
-
-GatedLayout fwd_layout(int M, int D, int F, int dtype) {
+GatedLayout x_layout(int M, int D, int F, int dtype) {
     GatedLayout L = {};
     const int e = dtype_bytes(dtype);
-    L.ldk = round_up(D, 16 / e);
-    L.pack = L.ldk != D;
-    if (L.pack) {
-        L.wg = align256((size_t)M * L.ldk * e);
-        L.wu = L.wg + align256((size_t)F * L.ldk * e);
-        L.total = L.wu + align256((size_t)F * L.ldk * e);
+    L.ldk = padded(D, e, 16);
+    L.pack_x = L.ldk != D;
+    if (L.pack_x) {
+        L.x = L.take((size_t)M * L.ldk * e);
+        L.wg = L.take((size_t)F * L.ldk * e);
+        L.wu = L.take((size_t)F * L.ldk * e);
     }
     return L;
 }
 
+GatedLayout fwd_layout(int M, int D, int F, int dtype, int h_dtype) {
+    GatedLayout L = x_layout(M, D, F, dtype);
+    const int o = dtype_bytes(h_dtype);
+    L.ldo = padded(F, o, 16);
+    L.pack_out = L.ldo != F;
+    if (L.pack_out) L.out = L.take((size_t)M * L.ldo * o);
+    return L;
+}
+
 GatedLayout bwd_layout(int M, int D, int F, int dtype) {
-    GatedLayout L = fwd_layout(M, D, F, dtype);
-    L.ldf = round_up(F, 16);
-    L.dg = L.total;
-    L.du = L.dg + align256((size_t)M * L.ldf * 2);
-    L.part = L.du + align256((size_t)M * L.ldf * 2);
+    GatedLayout L = x_layout(M, D, F, dtype);
+    L.ldi = L.ldf = padded(F, 2, 32);
+    L.pack_in = L.ldi != F;
+    if (L.pack_in) L.in = L.take((size_t)M * L.ldi * 2);
+    L.dg = L.take((size_t)M * L.ldf * 2);
+    L.du = L.take((size_t)M * L.ldf * 2);
+    L.ldo = padded(D, 2, 16);
+    L.pack_out = L.ldo != D;
+    if (L.pack_out) L.out = L.take((size_t)M * L.ldo * 2);
+    // dW through fp32 partial results, also where only its rows ask for it
     L.splits = gemm_splits(F, D, 2, M);
-    L.ldp = round_up(D, 4);  // 16 bytes, for TMA stores
-    L.total = L.part;
-    if (L.splits > 1) L.total += align256((size_t)L.splits * 2 * F * L.ldp * 4);
+    L.ldp = padded(D, 4, 16);
+    if (L.splits > 1 || D % 8) L.part = L.take((size_t)L.splits * 2 * F * L.ldp * 4);
     return L;
 }
 
@@ -62,7 +80,7 @@ GatedLayout bwd_layout(int M, int D, int F, int dtype) {
 // padded copies.
 cudaError_t pack_rows(const GatedLayout &L, const void *&x, const void *&wg, const void *&wu, int M,
                       int D, int F, int e, char *ws, cudaStream_t s) {
-    if (!L.pack) return cudaSuccess;
+    if (!L.pack_x) return cudaSuccess;
     cudaError_t err = launch_pack(x, M, D, e, ws + L.x, L.ldk, s);
     if (err == cudaSuccess) err = launch_pack(wg, F, D, e, ws + L.wg, L.ldk, s);
     if (err == cudaSuccess) err = launch_pack(wu, F, D, e, ws + L.wu, L.ldk, s);
@@ -81,9 +99,11 @@ using namespace pdr;
 
 extern "C" {
 
-size_t pdr_gated_workspace_bytes(int M, int D, int F, int dtype) {
-    if (!sizes_ok(M, D, F) || !in_limits(M, D, F) || !(half_type(dtype) || dtype == PDR_E4M3)) return 0;
-    return fwd_layout(M, D, F, dtype).total;
+size_t pdr_gated_workspace_bytes(int M, int D, int F, int dtype, int h_dtype) {
+    if (!sizes_ok(M, D, F) || !in_limits(M, D, F) || !(half_type(dtype) || dtype == PDR_E4M3) ||
+        !(half_type(h_dtype) || h_dtype == PDR_F32))
+        return 0;
+    return fwd_layout(M, D, F, dtype, h_dtype).total;
 }
 
 pdr_status pdr_gated_fwd(const void *x, const void *w_gate, const void *w_up, int dtype,
@@ -100,9 +120,9 @@ pdr_status pdr_gated_fwd(const void *x, const void *w_gate, const void *w_up, in
         return PDR_ERR_INVALID_ARG;
     if (!aligned_to(x, 16) || !aligned_to(w_gate, 16) || !aligned_to(w_up, 16) ||
         !aligned_to(x_scale, 4) || !aligned_to(gate_scale, 4) || !aligned_to(up_scale, 4) ||
-        !aligned_to(h, dtype_bytes(h_dtype)))
+        !aligned_to(h, 16))
         return PDR_ERR_INVALID_ARG;
-    const GatedLayout L = fwd_layout(M, D, F, dtype);
+    const GatedLayout L = fwd_layout(M, D, F, dtype, h_dtype);
     if (L.total && (!workspace || !aligned_to(workspace, 256))) return PDR_ERR_INVALID_ARG;
     if (workspace_bytes < L.total) return PDR_ERR_WORKSPACE_TOO_SMALL;
     if (M == 0) return PDR_OK;
@@ -124,10 +144,14 @@ pdr_status pdr_gated_fwd(const void *x, const void *w_gate, const void *w_up, in
     g.scale_m = x_scale;
     g.scale_n = gate_scale;
     g.scale_n2 = up_scale;
-    g.out = h;
+    char *out = static_cast<char *>(workspace) + L.out;
+    g.out = L.pack_out ? out : h;
     g.out_dtype = h_dtype;
-    g.ldo = F;
-    return done(launch_gemm(g, s));
+    g.ldo = L.ldo;
+    cudaError_t e = launch_gemm(g, s);
+    if (e == cudaSuccess && L.pack_out)
+        e = launch_unpack(out, M, F, L.ldo, dtype_bytes(h_dtype), h, s);
+    return done(e);
 }
 
 size_t pdr_gated_bwd_workspace_bytes(int M, int D, int F, int dtype) {
@@ -143,9 +167,9 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
     if (!in_limits(M, D, F)) return PDR_ERR_TOO_LARGE;
     if ((M > 0 && (!grad || !x)) || !w_gate || !w_up || !grad_gate != !grad_up)
         return PDR_ERR_INVALID_ARG;
-    if (!aligned_to(grad, 2) || !aligned_to(x, 16) || !aligned_to(w_gate, 16) ||
-        !aligned_to(w_up, 16) || !aligned_to(grad_x, 2) || !aligned_to(grad_gate, 2) ||
-        !aligned_to(grad_up, 2))
+    if (!aligned_to(grad, 32) || !aligned_to(x, 16) || !aligned_to(w_gate, 16) ||
+        !aligned_to(w_up, 16) || !aligned_to(grad_x, 16) || !aligned_to(grad_gate, 16) ||
+        !aligned_to(grad_up, 16))
         return PDR_ERR_INVALID_ARG;
     const GatedLayout L = bwd_layout(M, D, F, dtype);
     if (L.total && (!workspace || !aligned_to(workspace, 256))) return PDR_ERR_INVALID_ARG;
@@ -160,6 +184,10 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
     if (!grad_x && !grad_gate) return PDR_OK;
     char *ws = static_cast<char *>(workspace);
     if (pack_rows(L, x, w_gate, w_up, M, D, F, 2, ws, s) != cudaSuccess) return PDR_ERR_CUDA;
+    if (L.pack_in) {
+        if (launch_pack(grad, M, F, 2, ws + L.in, L.ldi, s) != cudaSuccess) return PDR_ERR_CUDA;
+        grad = ws + L.in;
+    }
     const Operand ox = {x, M, D, L.ldk}, og = {w_gate, F, D, L.ldk}, ou = {w_up, F, D, L.ldk};
     const Operand odg = {ws + L.dg, M, F, L.ldf}, odu = {ws + L.du, M, F, L.ldf};
     {
@@ -176,7 +204,7 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
         g.act = activation;
         g.in = grad;
         g.in_dtype = dtype;
-        g.ldi = F;
+        g.ldi = L.ldi;
         g.out = ws + L.dg;
         g.out2 = ws + L.du;
         g.out_dtype = dtype;
@@ -195,10 +223,11 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
         g.M = M;
         g.N = D;
         g.K[0] = g.K[1] = F;
-        g.out = grad_x;
+        g.out = L.pack_out ? ws + L.out : grad_x;
         g.out_dtype = dtype;
-        g.ldo = D;
+        g.ldo = L.ldo;
         e = launch_gemm(g, s);
+        if (e == cudaSuccess && L.pack_out) e = launch_unpack(ws + L.out, M, D, L.ldo, 2, grad_x, s);
     }
     if (e == cudaSuccess && grad_gate) {
         GemmArgs g;
@@ -215,7 +244,8 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
         g.ldo = D;
         const long long n = F * L.ldp;
         float *part = reinterpret_cast<float *>(ws + L.part);
-        if (L.splits > 1) {
+        const bool partial = L.splits > 1 || D % 8;
+        if (partial) {
             g.out = part;
             g.ldo = L.ldp;
             g.out_dtype = PDR_F32;
@@ -227,7 +257,7 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
             g.out_dtype = dtype;
         }
         e = launch_gemm(g, s);
-        if (e == cudaSuccess && L.splits > 1)
+        if (e == cudaSuccess && partial)
             e = launch_join(part, L.splits, F, D, L.ldp, grad_gate, grad_up, dtype, s);
     }
     return done(e);

@@ -70,14 +70,13 @@ struct __align__(64) GemmParams {
     unsigned long long adesc, bdesc;  // smem descriptors without the address
     int a_step, b_step;               // descriptor advance (16-byte units) of one mma
     int fp8;
-    void *out, *out2;
-    int out_dtype, out_vec, out_tma;
-    long long ldo, out_z, out_split;
+    void *out;
+    int out_dtype, narrow;
     const void *bias;
     int bias_dtype;
     const float *scale_m, *scale_n, *scale_n2;
     const void *in;
-    int in_dtype, in_vec;
+    int in_dtype;
     long long ldi;
     float *colsum;
 };
@@ -208,78 +207,9 @@ __device__ __forceinline__ void settled(float (&v)[C]) {
     for (int i = 0; i < C; ++i) asm volatile("" : "+f"(v[i]));
 }
 
-// ---- a row's 16 columns between registers and global memory ----------------
+// ---- a row's 16 columns between registers and memory -------------------------
 //
-// Lane l of a warp holds row l of a 32 x 16 block.  Aligned rows move as full
-// 32-byte sectors; other rows, and the last columns of a row, go through the
-// warp's transposing buffer, so that a warp access covers runs of 16
-// neighbouring elements.
-
-struct Block {
-    int row0, rows;  // first row, rows inside the result (of 32)
-    int col0, cols;  // first column, columns inside the result from there
-};
-
-// (All 16 loads are under way before the first is used.)
-__device__ __forceinline__ void fetch_edge(const void *p, long long ld, int dtype, const Block &b,
-                                           unsigned (&raw)[kChunk]) {
-    const int lane = threadIdx.x & 31, c = lane & 15, r = lane >> 4;
-    const long long at = (long long)(b.row0 + r) * ld + b.col0 + c;
-    const int rows = c < b.cols ? b.rows - r : 0;
-    if (dtype == PDR_F32) {
-        const float *q = static_cast<const float *>(p) + at;
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) raw[i] = 2 * i < rows ? __float_as_uint(__ldg(q + 2 * i * ld)) : 0;
-    } else {
-        const unsigned short *q = static_cast<const unsigned short *>(p) + at;
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) raw[i] = 2 * i < rows ? __ldg(q + 2 * i * ld) : 0;
-    }
-}
-// Place of a value in the transposing buffer (16 floats a row, without bank conflicts).
-__device__ __forceinline__ int buffer_at(int r, int c) { return r * kChunk + (c ^ (r & 15)); }
-__device__ __forceinline__ void unpack_edge(float *buffer, int dtype, const unsigned (&raw)[kChunk],
-                                            float (&v)[kChunk]) {
-    const int lane = threadIdx.x & 31;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i)
-        buffer[buffer_at(2 * i + (lane >> 4), lane & 15)] = __uint_as_float(raw[i]);
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < kChunk; ++j) v[j] = buffer[buffer_at(lane, j)];
-    if (dtype == PDR_F16) {
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) v[j] = unpack2(__float_as_uint(v[j]), PDR_F16).x;
-    } else if (dtype == PDR_BF16) {
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) v[j] = unpack2(__float_as_uint(v[j]), PDR_BF16).x;
-    }
-}
-__device__ __forceinline__ void write_edge(void *p, long long ld, int dtype, const Block &b,
-                                           float *buffer, const float (&v)[kChunk]) {
-    const int lane = threadIdx.x & 31, c = lane & 15;
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < kChunk; ++j) buffer[buffer_at(lane, j)] = v[j];
-    __syncwarp();
-    const int r = lane >> 4, rows = c < b.cols ? b.rows - r : 0;
-    const long long at = (long long)(b.row0 + r) * ld + b.col0 + c;
-    float x[kChunk];
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) x[i] = buffer[buffer_at(2 * i + r, c)];
-    if (dtype == PDR_F32) {
-        float *q = static_cast<float *>(p) + at;
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i)
-            if (2 * i < rows) q[2 * i * ld] = x[i];
-    } else {
-        unsigned short *q = static_cast<unsigned short *>(p) + at;
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i)
-            if (2 * i < rows) q[2 * i * ld] = half_bits(x[i], dtype);
-    }
-}
+// Lane l of a warp holds row l of a block of 32 rows.
 
 __device__ __forceinline__ void unpack_row(int dtype, const unsigned (&raw)[kChunk],
                                            float (&v)[kChunk]) {
@@ -311,20 +241,6 @@ __device__ __forceinline__ void pack_row(int dtype, const float *v, unsigned (&w
         for (int j = 0; j < 8; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], PDR_BF16);
     }
 }
-__device__ __forceinline__ void write_row(bool on, char *q, int dtype, const float (&v)[kChunk]) {
-    if (dtype == PDR_F32) {
-        unsigned w[kChunk];
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) w[j] = __float_as_uint(v[j]);
-        store8(on, q, w);
-        store8(on, q + 32, w + 8);
-    } else {
-        unsigned w[kChunk / 2];
-        pack_row(dtype, v, w);
-        store8(on, q, w);
-    }
-}
-
 // Results leave through the warp's buffer and TMA stores of 32 rows, which drop
 // what is behind the last row and column: direct stores of 32 bytes a lane take 32
 // turns of the load-store unit each, this way four.  A block in the buffer has
@@ -596,10 +512,14 @@ __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t
             pack_row(p.out_dtype, u, w);
             stage_narrow(stage + kBufferBytes / 2, w);
             store_buffer(&p.o[0], &p.o[1], stage, n0 + c, row0, 0);
-        } else if (EPI == kEpiLinear && p.out_dtype == PDR_F32) {
-            buffer_free();
-            stage_floats(stage, v);
-            store_buffer(&p.o[0], nullptr, stage, n0 + c, row0, slice);
+        } else if (EPI != kEpiSlope && p.out_dtype == PDR_F32) {
+#pragma unroll
+            for (int i = 0; i < C; i += kChunk) {
+                if (n0 + c + i >= p.N) break;
+                buffer_free();
+                stage_floats(stage, v + i);
+                store_buffer(&p.o[0], nullptr, stage, n0 + c + i, row0, slice);
+            }
         } else {
             if (half == 0) buffer_free();
 #pragma unroll
@@ -624,152 +544,72 @@ __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t
     return true;
 }
 
-// The same for any alignment and width (rows that TMA cannot store, results or
-// inputs of a width that is no multiple of 16); the next 16 columns are on their way from tensor memory while 16 are computed.
-// `columns`: the warp's bias and column scales, [3][kMaxCols]; `have_n`: the
-// column of tiles that they are of.
-template <int EPI, int ACT>
-__device__ __forceinline__ bool epilogue_any(const GemmParams &p, const Tile &t, unsigned acc,
-                                              unsigned ready, unsigned phase, int c0, int c1,
-                                              int quarter, float *columns, int &have_n,
-                                              float *buffer, int *abort, unsigned release) {
-    constexpr bool kTwo = EPI == kEpiGated || EPI == kEpiGatedBwd;  // g and u
-    const int lane = threadIdx.x & 31;
-    const bool has_in = EPI != kEpiGated && p.in;
-    Block b;
-    b.row0 = t.m * kBM + 32 * quarter;
-    b.rows = max(0, min(32, p.M - b.row0));
-    const int n0 = t.n * p.bcols, ncols = p.N - n0;
-    c1 = min(c1, ncols);
-    // The pair's second block may lie behind the last row, a group behind the last column.
-    const bool any = t.m * kBM < p.M && c0 < c1, on = lane < b.rows;
-    const int ib = p.in_dtype == PDR_F32 ? 4 : 2;
-    const long long row = b.row0 + lane;
-    const char *in_row = static_cast<const char *>(p.in) + (row * p.ldi + n0) * ib;
+// The same for results of at most 16 columns whose rows TMA cannot store (Gaussian
+// parameters of 1, 2, 4, 5 ... channels): the warp's 32 rows are one run of memory,
+// and go through its buffer in that order.
+template <int ACT>
+__device__ __forceinline__ bool epilogue_narrow(const GemmParams &p, const Tile &t, unsigned acc,
+                                                unsigned ready, unsigned phase, int quarter,
+                                                float *columns, int &have_n, float *buffer,
+                                                int *abort, unsigned release) {
+    const int lane = threadIdx.x & 31, N = p.N;
+    const int row0 = t.m * kBM + 32 * quarter, rows = max(0, min(32, p.M - row0));
+    const long long at = (long long)row0 * N + lane;
+    const int run = rows * N;
     unsigned raw[kChunk];
     float scale_m = 1.0f;
-    auto fetch = [&](int c) {
-        if (p.in_vec && c + kChunk <= ncols) {
-            load8(on, in_row + c * ib, raw);
-            if (p.in_dtype == PDR_F32) load8(on, in_row + c * ib + 32, raw + 8);
+    if (p.in) {
+        if (p.in_dtype == PDR_F32) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i)
+                if (lane + 32 * i < run) raw[i] = __ldg(static_cast<const unsigned *>(p.in) + at + 32 * i);
         } else {
-            b.col0 = n0 + c;
-            b.cols = ncols - c;
-            fetch_edge(p.in, p.ldi, p.in_dtype, b, raw);
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i)
+                if (lane + 32 * i < run) raw[i] = __ldg(static_cast<const unsigned short *>(p.in) + at + 32 * i);
         }
-    };
-    if (any) {  // on their way while the products finish
-        if (has_in) fetch(c0);
-        if (p.fp8 && on) scale_m = p.scale_m[row];
-        if ((p.bias || p.fp8) && have_n != t.n) {
-            have_n = t.n;
-            __syncwarp();
-            for (int c = lane; c < c1 - c0; c += 32) {
-                const int n = n0 + c0 + c;
-                if (p.bias) columns[c] = img_load(p.bias, n, p.bias_dtype);
-                if (p.fp8) columns[kMaxCols + c] = p.scale_n[n];
-                if (p.fp8 && p.scale_n2) columns[2 * kMaxCols + c] = p.scale_n2[n];
-            }
-            __syncwarp();
+    }
+    if (p.fp8 && lane < rows) scale_m = p.scale_m[row0 + lane];
+    if (have_n < 0) {
+        have_n = 0;
+        if (lane < kChunk) {
+            columns[lane] = p.bias && lane < N ? img_load(p.bias, lane, p.bias_dtype) : 0.0f;
+            columns[kMaxCols + lane] = p.fp8 && lane < N ? p.scale_n[lane] : 1.0f;
         }
+        __syncwarp();
     }
     if (!__all_sync(0xffffffffu, bar_wait(ready, phase, abort))) return false;
-    if (!any) {
-        if (lane == 0) bar_arrive_at(release);
-        return true;
-    }
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    auto read = [&](int c, float (&v)[kChunk], float (&u)[kChunk]) {
-        tmem_load(acc + c, v);
-        if constexpr (kTwo) tmem_load(acc + p.bcols + c, u);
-    };
-    auto write = [&](void *out, int c, const float (&v)[kChunk]) {
-        const int ob = p.out_dtype == PDR_F32 ? 4 : 2;
-        char *to = static_cast<char *>(out) + (t.z * p.out_z + t.split * p.out_split) * ob;
-        if (p.out_vec && c + kChunk <= ncols) {
-            write_row(on, to + (row * p.ldo + n0 + c) * ob, p.out_dtype, v);
-        } else {
-            b.col0 = n0 + c;
-            b.cols = ncols - c;
-            write_edge(to, p.ldo, p.out_dtype, b, buffer, v);
-        }
-    };
-    auto finish = [&](int c, float (&v)[kChunk], float (&u)[kChunk]) {
-        float x[kChunk];
-        if (has_in) {
-            if (p.in_vec && c + kChunk <= ncols)
-                unpack_row(p.in_dtype, raw, x);
-            else
-                unpack_edge(buffer, p.in_dtype, raw, x);
-            if (c + kChunk < c1) fetch(c + kChunk);
-        }
-        if (p.fp8) {
-            const float *s = columns + kMaxCols + c - c0;
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-                v[i] *= scale_m * s[i];
-                if constexpr (EPI == kEpiGated) u[i] *= scale_m * s[kMaxCols + i];
-            }
-        }
-        if (!kTwo && p.bias) {
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i) v[i] += columns[c - c0 + i];
-        }
-        if constexpr (EPI == kEpiLinear) {
-            apply_act<ACT>(v);
-            if (has_in) {
-#pragma unroll
-                for (int i = 0; i < kChunk; ++i) v[i] += x[i];
-            }
-        } else if constexpr (EPI == kEpiGated) {
-            apply_gated<ACT>(v, u);
-        } else if constexpr (EPI == kEpiSlope) {
-            apply_slope<ACT>(v, x);
-        } else {
-            apply_gated_bwd<ACT>(v, u, x);
-        }
-        write(EPI == kEpiLinear && p.out2 && t.z ? p.out2 : p.out, c, v);
-        if constexpr (EPI == kEpiGatedBwd) write(p.out2, c, u);
-        if constexpr (EPI == kEpiSlope)
-            if (p.colsum) {
-#pragma unroll
-                for (int i = 0; i < kChunk; ++i) v[i] = on ? v[i] : 0.0f;  // rows outside count nothing
-                const float s = column_sums(v);
-                if (lane < kChunk && lane < ncols - c)
-                    p.colsum[((long long)t.m * 4 + quarter) * p.N + n0 + c + lane] = s;
-            }
-    };
-    // Two sets of registers, the next columns' and these; dg and du leave room for one.
-    constexpr int kSets = EPI == kEpiGatedBwd ? 1 : 2;
-    float v[kSets][kChunk], u[kSets][kChunk];
+    float v[kChunk];
+    tmem_load(acc, v);
+    tmem_load_wait();
+    settled(v);
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncwarp();
-    if constexpr (kSets == 2) read(c0, v[0], u[0]);
-    for (int c = c0; c < c1; c += kStore) {
+    if (lane == 0) bar_arrive_at(release);
+    if (p.fp8) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int at = c + half * kChunk, set = half % kSets;
-            if (at >= c1) break;
-            if constexpr (kSets == 1) {
-                __syncwarp();
-                read(at, v[set], u[set]);
-            }
-            tmem_load_wait();
-            settled(v[set]);
-            if constexpr (kTwo) settled(u[set]);
-            if (at + kChunk >= c1) {  // the accumulator is read: the next products may overwrite it
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) bar_arrive_at(release);
-            } else if constexpr (kSets == 2) {
-                read(at + kChunk, v[1 - set], u[1 - set]);
-            }
-            finish(at, v[set], u[set]);
-        }
+        for (int i = 0; i < kChunk; ++i) v[i] *= scale_m * columns[kMaxCols + i];
     }
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) v[i] += columns[i];
+    apply_act<ACT>(v);
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j)
+        if (j < N) buffer[lane * N + j] = v[j];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+        if (lane + 32 * i >= run) continue;
+        float x = buffer[lane + 32 * i];
+        if (p.in) x += p.in_dtype == PDR_F32 ? __uint_as_float(raw[i]) : unpack2(raw[i], p.in_dtype).x;
+        img_store(p.out, (size_t)(at + 32 * i), p.out_dtype, x);
+    }
+    __syncwarp();
     return true;
 }
 
-template <int EPI, int ACT, bool ANY>
+template <int EPI, int ACT, bool NARROW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_gemm(const __grid_constant__ GemmParams p) {
     extern __shared__ char raw[];
@@ -837,10 +677,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if ((it & (sets - 1)) == set) {
                 const unsigned d = tmem + ((unsigned)(32 * quarter) << 16) + acc * p.bn;
                 bool ok;
-                if constexpr (ANY)
-                    ok = epilogue_any<EPI, ACT>(p, tile, d, acc_full + 8 * acc, acc_phase, cfirst,
-                                                cfirst + cols, quarter, columns, have_n, buffer,
-                                                abort, release + 8 * acc);
+                if constexpr (NARROW)
+                    ok = epilogue_narrow<ACT>(p, tile, d, acc_full + 8 * acc, acc_phase, quarter,
+                                              columns, have_n, buffer, abort, release + 8 * acc);
                 else
                     ok = epilogue_tile<EPI, ACT>(p, tile, d, acc_full + 8 * acc, acc_phase, cfirst,
                                                  cfirst + cols, quarter, columns, have_n, buffer,
@@ -854,7 +693,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 acc_phase ^= 1;
             }
         }
-        if (!ANY && elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (!NARROW && elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         const unsigned stages0 = smem_u32(smem), held0 = smem_u32(held);
@@ -992,14 +831,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ---- small kernels -----------------------------------------------------------
 
-// Row copy between row lengths, 16-bit or 8-bit elements.
+// Dense rows to rows of ld elements (a multiple of 16 bytes): 16 bytes per thread.
 template <typename T>
 __global__ void __launch_bounds__(256) k_pack(const T *__restrict__ from, long long rows, int cols,
-                                              T *__restrict__ to, long long ld) {
+                                              T *__restrict__ to, int vectors) {
+    constexpr int E = 16 / sizeof(T);
     grid_dep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (long long r = (long long)blockIdx.x * 8 + warp; r < rows; r += (long long)gridDim.x * 8)
-        for (int c = lane; c < cols; c += 32) to[r * ld + c] = from[r * cols + c];
+    for (long long r = (long long)blockIdx.x * 8 + warp; r < rows; r += (long long)gridDim.x * 8) {
+        const T *row = from + r * cols;
+        for (int v = lane; v < vectors; v += 32) {
+            union {
+                T e[E];
+                uint4 u;
+            } w;
+#pragma unroll
+            for (int i = 0; i < E; ++i) w.e[i] = v * E + i < cols ? __ldg(row + v * E + i) : T(0);
+            *reinterpret_cast<uint4 *>(to + (r * vectors + v) * E) = w.u;
+        }
+    }
+}
+
+// And back.  Elements of 16 bits go in pairs that start at 4 bytes.
+template <typename T>
+__global__ void __launch_bounds__(256) k_unpack(const T *__restrict__ from, long long rows, int cols,
+                                                int ld, T *__restrict__ to) {
+    grid_dep_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (long long r = (long long)blockIdx.x * 8 + warp; r < rows; r += (long long)gridDim.x * 8) {
+        const T *row = from + r * ld;
+        T *out = to + r * cols;
+        if constexpr (sizeof(T) == 2) {
+            const int odd = (int)((reinterpret_cast<uintptr_t>(out) >> 1) & 1);
+            for (int c = 2 * lane - odd; c < cols; c += 64) {
+                const unsigned a = c >= 0 ? __ldg(row + c) : 0, b = c + 1 < cols ? __ldg(row + c + 1) : 0;
+                if (c >= 0 && c + 1 < cols)
+                    *reinterpret_cast<unsigned *>(out + c) = a | b << 16;
+                else if (c >= 0)
+                    out[c] = (T)a;
+                else if (cols > 0)
+                    out[0] = (T)b;
+            }
+        } else {
+            for (int c = lane; c < cols; c += 32) out[c] = __ldg(row + c);
+        }
+    }
 }
 
 // Four neighbouring columns per thread; the splits are added in order, eight
@@ -1153,7 +1029,7 @@ unsigned long long smem_desc(bool mn) {
            ((unsigned long long)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-template <int EPI, int ACT, bool ANY>
+template <int EPI, int ACT, bool NARROW>
 cudaError_t launch_as(const GemmParams &p, int grid, size_t smem, cudaStream_t s) {
     // The kernel's shared-memory limit, raised once per device.
     static std::atomic<unsigned long long> raised{0};
@@ -1162,17 +1038,18 @@ cudaError_t launch_as(const GemmParams &p, int grid, size_t smem, cudaStream_t s
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (dev > 63 || !(raised.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(k_gemm<EPI, ACT, ANY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(k_gemm<EPI, ACT, NARROW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSmemBytes);
         if (e != cudaSuccess) return e;
         raised.fetch_or(bit, std::memory_order_release);
     }
-    return launch_dependent(k_gemm<EPI, ACT, ANY>, dim3((unsigned)grid), dim3(kThreads), smem, s, p);
+    return launch_dependent(k_gemm<EPI, ACT, NARROW>, dim3((unsigned)grid), dim3(kThreads), smem, s, p);
 }
 template <int EPI, int ACT>
 cudaError_t launch_as(const GemmParams &p, int grid, size_t smem, cudaStream_t s) {
-    return p.out_tma ? launch_as<EPI, ACT, false>(p, grid, smem, s)
-                     : launch_as<EPI, ACT, true>(p, grid, smem, s);
+    if constexpr (EPI == kEpiLinear)
+        if (p.narrow) return launch_as<EPI, ACT, true>(p, grid, smem, s);
+    return launch_as<EPI, ACT, false>(p, grid, smem, s);
 }
 template <int EPI>
 cudaError_t launch(const GemmParams &p, int act, int grid, size_t smem, cudaStream_t s) {
@@ -1194,6 +1071,11 @@ Divisor divisor(int d) {
 }
 
 }  // namespace
+
+bool gemm_narrow(int N, int out_dtype, bool has_in) {
+    const int row = N * dtype_bytes(out_dtype);
+    return N <= kChunk && (row % 16 || (has_in && row % 32));
+}
 
 int gemm_tile_columns(int epi, int M, int N, int nz) {
     const bool dual = epi == kEpiGated || epi == kEpiGatedBwd;
@@ -1260,15 +1142,20 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
         if (!make_map(&p.b[i], g.b[i], bytes, g.b_mn ? 64 : kelems,
                       g.b_mn ? 64 : p.bn / 2))
             return cudaErrorInvalidValue;
-    p.out = g.out;
-    p.out2 = g.out2;
-    p.out_dtype = g.out_dtype;
-    p.ldo = g.ldo;
-    p.out_z = g.out_z;
-    p.out_split = g.out_split;
     const int ob = dtype_bytes(g.out_dtype), ib = dtype_bytes(g.in_dtype);
-    p.out_vec = aligned_to(g.out, 32) && aligned_to(g.out2, 32) && g.ldo * ob % 32 == 0 &&
-                g.out_z * ob % 32 == 0 && g.out_split * ob % 32 == 0;
+    p.out = g.out;
+    p.out_dtype = g.out_dtype;
+    p.narrow = g.narrow;
+    // Results and inputs as the callers lay them out: see GemmArgs.
+    if (p.narrow ? g.epi != kEpiLinear || p.nz > 1 || g.splits > 1 || g.N > kChunk || g.ldo != g.N || (g.in && g.ldi != g.N)
+                 : g.ldo * ob % 16 || !aligned_to(g.out, 16) || !aligned_to(g.out2, 16) ||
+                       (g.in && (g.ldi * ib % 32 || !aligned_to(g.in, 32))))
+        return cudaErrorInvalidValue;
+    const int slices = g.out_split || g.out_z ? p.splits * p.nz : 1;
+    for (int i = 0; !p.narrow && i < (g.out2 ? 2 : 1); ++i)
+        if (!make_store_map(&p.o[i], i ? g.out2 : g.out, ob, g.M, g.N, g.ldo, slices,
+                            g.epi == kEpiGatedBwd))
+            return cudaErrorInvalidValue;
     p.bias = g.bias;
     p.bias_dtype = g.bias_dtype;
     p.scale_m = g.scale_m;
@@ -1277,14 +1164,6 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     p.in = g.in;
     p.in_dtype = g.in_dtype;
     p.ldi = g.ldi;
-    p.in_vec = aligned_to(g.in, 32) && g.ldi * ib % 32 == 0;
-    p.out_tma = aligned_to(g.out, 16) && aligned_to(g.out2, 16) && g.ldo * ob % 16 == 0 &&
-                (!g.in || p.in_vec) && !(g.epi == kEpiGated && ob == 4);
-    const int slices = g.out_split || g.out_z ? p.splits * p.nz : 1;
-    for (int i = 0; p.out_tma && i < (g.out2 ? 2 : 1); ++i)
-        if (!make_store_map(&p.o[i], i ? g.out2 : g.out, ob, g.M, g.N, g.ldo, slices,
-                            g.epi == kEpiGatedBwd))
-            return cudaErrorInvalidValue;
     p.colsum = g.colsum;
     const size_t fixed = 1024 + 512 + kEpiWarps * (3 * kMaxCols * 4 + kBufferBytes);
     const size_t room = kSmemBytes - fixed, all_b = (size_t)p.kb * p.b_bytes;
@@ -1312,16 +1191,33 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     }
 }
 
+namespace {
+unsigned copy_blocks(long long rows) {
+    return (unsigned)(rows / 8 + 1 < 16 * kSMs ? rows / 8 + 1 : 16 * kSMs);
+}
+template <typename T>
+cudaError_t pack_as(const void *from, long long rows, long long cols, void *to, long long ld, cudaStream_t s) {
+    return launch_dependent(k_pack<T>, dim3(copy_blocks(rows)), dim3(256), 0, s,
+                            static_cast<const T *>(from), rows, (int)cols, static_cast<T *>(to),
+                            (int)(ld * sizeof(T) / 16));
+}
+template <typename T>
+cudaError_t unpack_as(const void *from, long long rows, long long cols, long long ld, void *to, cudaStream_t s) {
+    return launch_dependent(k_unpack<T>, dim3(copy_blocks(rows)), dim3(256), 0, s,
+                            static_cast<const T *>(from), rows, (int)cols, (int)ld, static_cast<T *>(to));
+}
+}  // namespace
+
 cudaError_t launch_pack(const void *from, long long rows, long long cols, int bytes, void *to,
-                        long long ld_to, cudaStream_t s) {
-    const int grid = (int)(rows / 8 + 1 < 8 * kSMs ? rows / 8 + 1 : 8 * kSMs);
-    if (bytes == 1)
-        return launch_dependent(k_pack<unsigned char>, dim3(grid), dim3(256), 0, s,
-                                static_cast<const unsigned char *>(from), rows, (int)cols,
-                                static_cast<unsigned char *>(to), ld_to);
-    return launch_dependent(k_pack<unsigned short>, dim3(grid), dim3(256), 0, s,
-                            static_cast<const unsigned short *>(from), rows, (int)cols,
-                            static_cast<unsigned short *>(to), ld_to);
+                        long long ld, cudaStream_t s) {
+    return bytes == 1   ? pack_as<unsigned char>(from, rows, cols, to, ld, s)
+           : bytes == 2 ? pack_as<unsigned short>(from, rows, cols, to, ld, s)
+                        : pack_as<unsigned>(from, rows, cols, to, ld, s);
+}
+cudaError_t launch_unpack(const void *from, long long rows, long long cols, long long ld, int bytes,
+                          void *to, cudaStream_t s) {
+    return bytes == 2 ? unpack_as<unsigned short>(from, rows, cols, ld, to, s)
+                      : unpack_as<unsigned>(from, rows, cols, ld, to, s);
 }
 
 cudaError_t launch_join(const float *part, int splits, int rows, int cols, long long ld, void *to,

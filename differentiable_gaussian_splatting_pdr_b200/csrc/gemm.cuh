@@ -161,11 +161,18 @@ struct GemmArgs {
     int bias_dtype = PDR_F32;
     const float *scale_m = nullptr, *scale_n = nullptr, *scale_n2 = nullptr;
     const void *in = nullptr;       // residual, dy or dh: rows of ldi elements
+    // Rows of the results start at multiples of 16 bytes and of the input at
+    // multiples of 32 (padded rows); narrow (kEpiLinear, N <= 16): dense rows of any
+    // alignment, the input's too.
+    bool narrow = false;
     int in_dtype = PDR_F32;
     long long ldi = 0;
     float *colsum = nullptr;        // kEpiSlope: [4 * ceil(M / 128)][N] partial column sums
 };
 
+// Whether a linear result of N columns (with an input of its type) is so narrow that
+// rows which TMA could not store, or the input's sectors, are taken as they are.
+bool gemm_narrow(int N, int out_dtype, bool has_in);
 // Columns of a tile that launch_gemm picks for a result of M x N (x nz products).
 int gemm_tile_columns(int epi, int M, int N, int nz);
 // Tiles along k that fill the machine for a weight gradient, at most `most`.
@@ -176,9 +183,16 @@ cudaError_t read_wait_error(int *bits, cudaStream_t s);
 
 // ---- small kernels around the products ---------------------------------------
 
-// Rows of `cols` elements (16 bits or 8) copied to rows of `ld_to` elements.
+// Dense rows of `cols` elements (of 1, 2 or 4 bytes) to rows of `ld` elements, a
+// multiple of 16 bytes (zeros behind), and (2 or 4 bytes) back.
 cudaError_t launch_pack(const void *from, long long rows, long long cols, int bytes, void *to,
-                        long long ld_to, cudaStream_t s);
+                        long long ld, cudaStream_t s);
+cudaError_t launch_unpack(const void *from, long long rows, long long cols, long long ld, int bytes,
+                          void *to, cudaStream_t s);
+// Elements of a row padded to `unit` bytes.
+inline long long padded(long long cols, int bytes, int unit) {
+    return (cols * bytes + unit - 1) / unit * unit / bytes;
+}
 // to[r][c] = sum over the splits of part[split][r][c], rounded once to `dtype`;
 // partial rows are ld floats apart (a multiple of 4), results dense.  With a
 // second result the splits are part[split][2][rows][ld].

@@ -22,11 +22,19 @@
 namespace pdr {
 namespace {
 
+// The workspace: padded copies of what TMA or 32-byte loads cannot address (rows
+// that are no multiple of 16 bytes; of the residual or of dy, of 32), padded
+// results that are copied out at the end, dz, and partial sums.
 struct LinearLayout {
-    size_t x, w, dz, colsum, part, total;
-    long long ldk, ldz, ldp, sum_rows;  // rows of x and W, of dz, of partial dW
-    bool pack, cast;
+    size_t x, w, in, out, dz, colsum, part, total;
+    long long ldk, ldi, ldo, ldz, ldp, sum_rows;
+    bool pack_x, pack_in, pack_out, narrow, cast;
     int splits;
+    size_t take(size_t bytes) {
+        const size_t at = total;
+        total += align256(bytes);
+        return at;
+    }
 };
 
 bool linear_sizes(int M, int N, int K) { return M >= 0 && N >= 1 && K >= 1; }
@@ -34,37 +42,52 @@ bool linear_in_limits(int M, int N, int K) {
     return M <= PDR_MAX_ROWS && N <= PDR_MAX_FEATURES && K <= PDR_MAX_FEATURES;
 }
 
-long long round_up(long long a, long long b) { return (a + b - 1) / b * b; }
-
-LinearLayout fwd_layout(int M, int N, int K, int dtype) {
+LinearLayout fwd_layout(int M, int N, int K, int dtype, int y_dtype, bool residual) {
     LinearLayout L = {};
-    const int e = dtype_bytes(dtype);
-    L.ldk = round_up(K, 16 / e);
-    L.pack = L.ldk != K;
-    if (L.pack) {
-        L.x = 0;
-        L.w = align256((size_t)M * L.ldk * e);
-        L.total = L.w + align256((size_t)N * L.ldk * e);
+    const int e = dtype_bytes(dtype), o = dtype_bytes(y_dtype);
+    L.ldk = padded(K, e, 16);
+    L.pack_x = L.ldk != K;
+    if (L.pack_x) {
+        L.x = L.take((size_t)M * L.ldk * e);
+        L.w = L.take((size_t)N * L.ldk * e);
     }
+    L.ldi = L.ldo = N;
+    L.narrow = gemm_narrow(N, y_dtype, residual);
+    if (L.narrow) return L;
+    L.ldi = padded(N, o, 32);
+    L.ldo = padded(N, o, 16);
+    L.pack_in = residual && L.ldi != N;
+    L.pack_out = L.ldo != N;
+    if (L.pack_in) L.in = L.take((size_t)M * L.ldi * o);
+    if (L.pack_out) L.out = L.take((size_t)M * L.ldo * o);
     return L;
 }
 
 LinearLayout bwd_layout(int M, int N, int K, int dtype, int grad_dtype, int act) {
-    LinearLayout L = fwd_layout(M, N, K, dtype);
-    L.ldz = N;
-    L.cast = act != PDR_ACT_NONE || grad_dtype != dtype || N % 8 != 0;
-    L.dz = L.total;
-    if (L.cast) {
-        L.ldz = round_up(N, 16);
-        L.total += align256((size_t)M * L.ldz * 2);
+    LinearLayout L = {};
+    L.ldk = padded(K, 2, 16);
+    L.pack_x = L.ldk != K;
+    if (L.pack_x) {
+        L.x = L.take((size_t)M * L.ldk * 2);
+        L.w = L.take((size_t)N * L.ldk * 2);
     }
+    const int ge = dtype_bytes(grad_dtype);
+    L.ldi = padded(N, ge, 32);
+    L.pack_in = act != PDR_ACT_NONE && L.ldi != N;
+    if (L.pack_in) L.in = L.take((size_t)M * L.ldi * ge);
+    L.cast = act != PDR_ACT_NONE || grad_dtype != dtype || N % 8 != 0;
+    L.ldz = L.cast ? padded(N, 2, 32) : N;
+    if (L.cast) L.dz = L.take((size_t)M * L.ldz * 2);
+    L.narrow = gemm_narrow(K, dtype, false);  // dx
+    L.ldo = L.narrow ? K : padded(K, 2, 16);
+    L.pack_out = L.ldo != K;
+    if (L.pack_out) L.out = L.take((size_t)M * L.ldo * 2);
     L.sum_rows = act != PDR_ACT_NONE ? 4 * (((long long)M + 127) / 128) : column_groups(M);
-    L.colsum = L.total;
-    L.total += align256((size_t)L.sum_rows * N * 4);
+    L.colsum = L.take((size_t)L.sum_rows * N * 4);
+    // dW through fp32 partial results, also where only its rows ask for it
     L.splits = gemm_splits(N, K, 1, M);
-    L.ldp = round_up(K, 4);  // 16 bytes, for TMA stores
-    L.part = L.total;
-    if (L.splits > 1) L.total += align256((size_t)L.splits * N * L.ldp * 4);
+    L.ldp = padded(K, 4, 16);
+    if (L.splits > 1 || K % 8) L.part = L.take((size_t)L.splits * N * L.ldp * 4);
     return L;
 }
 
@@ -81,10 +104,11 @@ using namespace pdr;
 
 extern "C" {
 
-size_t pdr_linear_workspace_bytes(int M, int N, int K, int dtype) {
-    if (!linear_sizes(M, N, K) || !linear_in_limits(M, N, K) || !(half_type(dtype) || dtype == PDR_E4M3))
+size_t pdr_linear_workspace_bytes(int M, int N, int K, int dtype, int y_dtype, int has_residual) {
+    if (!linear_sizes(M, N, K) || !linear_in_limits(M, N, K) ||
+        !(half_type(dtype) || dtype == PDR_E4M3) || !float_type(y_dtype))
         return 0;
-    return fwd_layout(M, N, K, dtype).total;
+    return fwd_layout(M, N, K, dtype, y_dtype, has_residual != 0).total;
 }
 
 pdr_status pdr_linear_fwd(const void *x, const void *weight, int dtype, const float *x_scale,
@@ -101,10 +125,10 @@ pdr_status pdr_linear_fwd(const void *x, const void *weight, int dtype, const fl
         return PDR_ERR_INVALID_ARG;
     if (bias && !float_type(bias_dtype)) return PDR_ERR_INVALID_ARG;
     if (!aligned_to(x, 16) || !aligned_to(weight, 16) || !aligned_to(x_scale, 4) ||
-        !aligned_to(weight_scale, 4) || !aligned_to(y, dtype_bytes(y_dtype)) ||
-        !aligned_to(residual, dtype_bytes(y_dtype)) || !aligned_to(bias, bias ? dtype_bytes(bias_dtype) : 1))
+        !aligned_to(weight_scale, 4) || !aligned_to(y, 16) || !aligned_to(residual, 32) ||
+        !aligned_to(bias, bias ? dtype_bytes(bias_dtype) : 1))
         return PDR_ERR_INVALID_ARG;
-    const LinearLayout L = fwd_layout(M, N, K, dtype);
+    const LinearLayout L = fwd_layout(M, N, K, dtype, y_dtype, residual != nullptr);
     if (L.total && (!workspace || !aligned_to(workspace, 256))) return PDR_ERR_INVALID_ARG;
     if (workspace_bytes < L.total) return PDR_ERR_WORKSPACE_TOO_SMALL;
     if (M == 0) return PDR_OK;
@@ -116,27 +140,34 @@ pdr_status pdr_linear_fwd(const void *x, const void *weight, int dtype, const fl
     g.K[0] = K;
     g.a[0] = {x, M, K, L.ldk};
     g.b[0] = {weight, N, K, L.ldk};
-    if (L.pack) {
-        char *ws = static_cast<char *>(workspace);
-        const int e = dtype_bytes(dtype);
-        cudaError_t err = launch_pack(x, M, K, e, ws + L.x, L.ldk, s);
+    char *ws = static_cast<char *>(workspace);
+    const int e = dtype_bytes(dtype), o = dtype_bytes(y_dtype);
+    cudaError_t err = cudaSuccess;
+    if (L.pack_x) {
+        err = launch_pack(x, M, K, e, ws + L.x, L.ldk, s);
         if (err == cudaSuccess) err = launch_pack(weight, N, K, e, ws + L.w, L.ldk, s);
-        if (err != cudaSuccess) return PDR_ERR_CUDA;
         g.a[0].p = ws + L.x;
         g.b[0].p = ws + L.w;
     }
+    if (err == cudaSuccess && L.pack_in) {
+        err = launch_pack(residual, M, N, o, ws + L.in, L.ldi, s);
+        residual = ws + L.in;
+    }
+    g.narrow = L.narrow;
     g.act = activation;
-    g.out = y;
+    g.out = L.pack_out ? ws + L.out : y;
     g.out_dtype = y_dtype;
-    g.ldo = N;
+    g.ldo = L.ldo;
     g.bias = bias;
     g.bias_dtype = bias_dtype;
     g.scale_m = x_scale;
     g.scale_n = weight_scale;
     g.in = residual;
     g.in_dtype = y_dtype;
-    g.ldi = N;
-    return done(launch_gemm(g, s));
+    g.ldi = L.ldi;
+    if (err == cudaSuccess) err = launch_gemm(g, s);
+    if (err == cudaSuccess && L.pack_out) err = launch_unpack(ws + L.out, M, N, L.ldo, o, y, s);
+    return done(err);
 }
 
 size_t pdr_linear_bwd_workspace_bytes(int M, int N, int K, int dtype, int grad_dtype,
@@ -157,9 +188,9 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
     if ((M > 0 && (!grad || !x)) || !weight) return PDR_ERR_INVALID_ARG;
     if ((bias || grad_bias) && !float_type(bias_dtype)) return PDR_ERR_INVALID_ARG;
     const int be = bias || grad_bias ? dtype_bytes(bias_dtype) : 1;
-    if (!aligned_to(grad, 16) || !aligned_to(x, 16) || !aligned_to(weight, 16) ||
-        !aligned_to(bias, be) || !aligned_to(grad_bias, be) || !aligned_to(grad_x, 2) ||
-        !aligned_to(grad_weight, 2))
+    if (!aligned_to(grad, 32) || !aligned_to(x, 16) || !aligned_to(weight, 16) ||
+        !aligned_to(bias, be) || !aligned_to(grad_bias, be) || !aligned_to(grad_x, 16) ||
+        !aligned_to(grad_weight, 16))
         return PDR_ERR_INVALID_ARG;
     const LinearLayout L = bwd_layout(M, N, K, dtype, grad_dtype, activation);
     if (L.total && (!workspace || !aligned_to(workspace, 256))) return PDR_ERR_INVALID_ARG;
@@ -174,7 +205,7 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
     char *ws = static_cast<char *>(workspace);
     const bool act = activation != PDR_ACT_NONE, products = grad_x || grad_weight;
     if (!products && !grad_bias) return PDR_OK;
-    if (L.pack) {
+    if (L.pack_x) {
         if (act || grad_weight) {
             e = launch_pack(x, M, K, 2, ws + L.x, L.ldk, s);
             x = ws + L.x;
@@ -183,6 +214,10 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
             e = launch_pack(weight, N, K, 2, ws + L.w, L.ldk, s);
             weight = ws + L.w;
         }
+        if (e != cudaSuccess) return PDR_ERR_CUDA;
+    }
+    if (L.pack_in) {
+        e = launch_pack(grad, M, N, dtype_bytes(grad_dtype), ws + L.in, L.ldi, s);
         if (e != cudaSuccess) return PDR_ERR_CUDA;
     }
     float *colsum = grad_bias ? reinterpret_cast<float *>(ws + L.colsum) : nullptr;
@@ -200,9 +235,9 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
         g.act = activation;
         g.bias = bias;
         g.bias_dtype = bias_dtype;
-        g.in = grad;
+        g.in = L.pack_in ? ws + L.in : grad;
         g.in_dtype = grad_dtype;
-        g.ldi = N;
+        g.ldi = L.ldi;
         g.out = ws + L.dz;
         g.out_dtype = dtype;
         g.ldo = L.ldz;
@@ -223,10 +258,12 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
         g.M = M;
         g.N = K;
         g.K[0] = N;
-        g.out = grad_x;
+        g.narrow = L.narrow;
+        g.out = L.pack_out ? ws + L.out : grad_x;
         g.out_dtype = dtype;
-        g.ldo = K;
+        g.ldo = L.ldo;
         e = launch_gemm(g, s);
+        if (e == cudaSuccess && L.pack_out) e = launch_unpack(ws + L.out, M, K, L.ldo, 2, grad_x, s);
     }
     if (e == cudaSuccess && grad_weight) {
         GemmArgs g;
@@ -239,7 +276,8 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
         g.K[0] = M;
         g.splits = L.splits;
         g.ldo = K;
-        if (L.splits > 1) {
+        const bool partial = L.splits > 1 || K % 8;
+        if (partial) {
             g.out = ws + L.part;
             g.out_dtype = PDR_F32;
             g.ldo = L.ldp;
@@ -249,7 +287,7 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
             g.out_dtype = dtype;
         }
         e = launch_gemm(g, s);
-        if (e == cudaSuccess && L.splits > 1)
+        if (e == cudaSuccess && partial)
             e = launch_join(reinterpret_cast<float *>(ws + L.part), L.splits, N, K, L.ldp, grad_weight,
                             nullptr, dtype, s);
     }

@@ -101,9 +101,9 @@ def _check_rows(t, what: str, dtypes):
     return t.numel() // width, width
 
 
-def _aligned(t):
-    """The tensor, or a copy of it where it does not start at 16 bytes."""
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+def _aligned(t, n: int = 16):
+    """The tensor, or a copy of it where it does not start at a multiple of n bytes."""
+    return t if t.data_ptr() % n == 0 else t.clone()
 
 
 def _check_scales(x, weights, x_scale, scales, M: int):
@@ -119,10 +119,12 @@ def _check_scales(x, weights, x_scale, scales, M: int):
 
 
 def _out(out, shape, dtype, device):
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check(out, "out", (dtype,), torch.Size(shape), device)
-    return out
+    """`out`, or a new tensor where there is none or it does not start at 16 bytes."""
+    if out is not None:
+        _check(out, "out", (dtype,), torch.Size(shape), device)
+        if out.data_ptr() % 16 == 0:
+            return out
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
@@ -154,12 +156,14 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
         _check(residual, "residual", (out_dtype,), torch.Size(shape), dev)
     y = _out(out, shape, out_dtype, dev)
     x, weight = _aligned(x), _aligned(weight)
-    t = _TYPE[x.dtype]
-    ws, wp, wn = _workspace(_bytes("pdr_linear_workspace_bytes", M, N, K, t), dev)
+    if residual is not None:
+        residual = _aligned(residual, 32)
+    t, to = _TYPE[x.dtype], _TYPE[out_dtype]
+    ws, wp, wn = _workspace(_bytes("pdr_linear_workspace_bytes", M, N, K, t, to, residual is not None), dev)
     _call("pdr_linear_fwd", dev, x.data_ptr(), weight.data_ptr(), t, _ptr(x_scale), _ptr(weight_scale),
           _ptr(bias), 0 if bias is None else _TYPE[bias.dtype], _ptr(residual), act, M, N, K,
-          y.data_ptr(), _TYPE[out_dtype], wp, wn)
-    return y
+          y.data_ptr(), to, wp, wn)
+    return y if out is None or y is out else out.copy_(y)
 
 
 def linear_bwd(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
@@ -182,7 +186,7 @@ def linear_bwd(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, bias: 
     dx = torch.empty_like(x) if need[0] else None
     dw = torch.empty_like(weight) if need[1] else None
     db = torch.empty_like(bias) if bias is not None and need[2] else None
-    grad, x, weight = _aligned(grad), _aligned(x), _aligned(weight)
+    grad, x, weight = _aligned(grad, 32), _aligned(x), _aligned(weight)
     t, tg = _TYPE[x.dtype], _TYPE[grad.dtype]
     ws, wp, wn = _workspace(_bytes("pdr_linear_bwd_workspace_bytes", M, N, K, t, tg, act), dev)
     _call("pdr_linear_bwd", dev, grad.data_ptr(), tg, x.data_ptr(), weight.data_ptr(), t, _ptr(bias),
@@ -241,11 +245,11 @@ def gated_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activat
         raise ValueError("out_dtype must be float32, float16 or bfloat16")
     h = _out(out, (*x.shape[:-1], F), out_dtype, dev)
     x, w_gate, w_up = _aligned(x), _aligned(w_gate), _aligned(w_up)
-    t = _TYPE[x.dtype]
-    ws, wp, wn = _workspace(_bytes("pdr_gated_workspace_bytes", M, D, F, t), dev)
+    t, to = _TYPE[x.dtype], _TYPE[out_dtype]
+    ws, wp, wn = _workspace(_bytes("pdr_gated_workspace_bytes", M, D, F, t, to), dev)
     _call("pdr_gated_fwd", dev, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), t, _ptr(x_scale),
-          _ptr(gate_scale), _ptr(up_scale), act, M, D, F, h.data_ptr(), _TYPE[out_dtype], wp, wn)
-    return h
+          _ptr(gate_scale), _ptr(up_scale), act, M, D, F, h.data_ptr(), to, wp, wn)
+    return h if out is None or h is out else out.copy_(h)
 
 
 def gated_bwd(grad: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
@@ -260,7 +264,7 @@ def gated_bwd(grad: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: t
     dx = torch.empty_like(x) if need[0] else None
     dg = torch.empty_like(w_gate) if need[1] else None
     du = torch.empty_like(w_up) if need[1] else None
-    x, w_gate, w_up = _aligned(x), _aligned(w_gate), _aligned(w_up)
+    grad, x, w_gate, w_up = _aligned(grad, 32), _aligned(x), _aligned(w_gate), _aligned(w_up)
     t = _TYPE[x.dtype]
     ws, wp, wn = _workspace(_bytes("pdr_gated_bwd_workspace_bytes", M, D, F, t), dev)
     _call("pdr_gated_bwd", dev, grad.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), t, act,

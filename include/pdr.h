@@ -305,11 +305,11 @@ pdr_status pdr_loss_l1_ssim(const float *image, const float *target, int B, int 
  * inputs, and are bitwise reproducible.  M = 0 is valid (gradients of weights
  * are zero then; arrays sized by M may be NULL).
  *
- * Pointers: x, grad and the products' weights, and all rows of rms_norm and
- * quantize_rows, 16-byte aligned; otherwise aligned to their element; workspaces
- * 256-byte aligned, NULL where the needed size is 0.  Rows whose length is not a multiple of 16 bytes
- * are first copied to the workspace in padded form.  Violations return
- * PDR_ERR_INVALID_ARG, sizes beyond the limits PDR_ERR_TOO_LARGE, and nothing
+ * Pointers: matrices 16-byte aligned, the products' residual and grad 32-byte;
+ * vectors (biases, scales, the norm's weight) to their element; workspaces
+ * 256-byte aligned, NULL where the needed size is 0.  Matrices of the products
+ * whose rows are no multiple of that length go through padded copies in the
+ * workspace.  Violations return PDR_ERR_INVALID_ARG, sizes beyond the limits PDR_ERR_TOO_LARGE, and nothing
  * is launched then.  Streams as above.  A workspace holds nothing between
  * calls; calls that can overlap on the GPU need workspaces of their own. */
 typedef enum {
@@ -330,7 +330,7 @@ typedef enum {
  * which stand for value times scale; NULL otherwise.  Gaussian parameters
  * straight for pdr_render_fwd: N = 5 + C, y_dtype = PDR_F32, the base
  * parameters as residual. */
-size_t pdr_linear_workspace_bytes(int M, int N, int K, int dtype);
+size_t pdr_linear_workspace_bytes(int M, int N, int K, int dtype, int y_dtype, int has_residual);
 pdr_status pdr_linear_fwd(const void *x, const void *weight, int dtype, const float *x_scale,
                           const float *weight_scale, const void *bias, int bias_dtype,
                           const void *residual, int activation, int M, int N, int K, void *y,
@@ -350,7 +350,7 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
 
 /* x [M][D], w_gate and w_up [F][D] of `dtype`; h [M][F] of h_dtype (not
  * PDR_E4M3); scales as in pdr_linear_fwd, gate_scale and up_scale [F]. */
-size_t pdr_gated_workspace_bytes(int M, int D, int F, int dtype);
+size_t pdr_gated_workspace_bytes(int M, int D, int F, int dtype, int h_dtype);
 pdr_status pdr_gated_fwd(const void *x, const void *w_gate, const void *w_up, int dtype,
                          const float *x_scale, const float *gate_scale, const float *up_scale,
                          int activation, int M, int D, int F, void *h, int h_dtype, void *workspace,

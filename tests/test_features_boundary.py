@@ -19,15 +19,20 @@ def lib():
 
 
 def test_workspace_sizes(lib):
-    assert lib.pdr_linear_workspace_bytes(100, 8, 64, BF16) == 0       # rows of 128 bytes: read in place
-    n = lib.pdr_linear_workspace_bytes(100, 8, 63, BF16)               # padded copies of x and weight
+    assert lib.pdr_linear_workspace_bytes(100, 8, 64, BF16, F32, 1) == 0   # rows of 128 and 32 bytes: in place
+    assert lib.pdr_linear_workspace_bytes(100, 6, 64, BF16, F32, 1) == 0   # narrow results: in place
+    n = lib.pdr_linear_workspace_bytes(100, 40, 64, BF16, BF16, 1)         # 80 bytes: the residual padded to 96
+    assert n >= 100 * 48 * 2 and lib.pdr_linear_workspace_bytes(100, 40, 64, BF16, BF16, 0) == 0
+    assert lib.pdr_linear_workspace_bytes(100, 41, 64, BF16, BF16, 1) > n  # and the result to 96
+    n = lib.pdr_linear_workspace_bytes(100, 8, 63, BF16, F32, 1)           # padded copies of x and weight
     assert n >= (100 + 8) * 64 * 2 and n % 256 == 0
-    assert lib.pdr_linear_workspace_bytes(100, 8, 24, E4M3) > 0        # 24 bytes
+    assert lib.pdr_linear_workspace_bytes(100, 8, 24, E4M3, BF16, 0) > 0   # 24 bytes
     assert lib.pdr_linear_bwd_workspace_bytes(0, 8, 64, BF16, F32, 0) >= 0
     a = lib.pdr_linear_bwd_workspace_bytes(1000, 64, 64, BF16, BF16, 0)
     assert lib.pdr_linear_bwd_workspace_bytes(1000, 64, 64, BF16, F32, 0) >= a + 1000 * 64 * 2
     assert lib.pdr_linear_bwd_workspace_bytes(1000, 64, 64, BF16, BF16, 3) > a
-    assert lib.pdr_gated_workspace_bytes(100, 64, 40, F16) == 0
+    assert lib.pdr_gated_workspace_bytes(100, 64, 40, F16, F16) == 0
+    assert lib.pdr_gated_workspace_bytes(100, 64, 41, F16, F16) >= 100 * 48 * 2
     assert lib.pdr_gated_bwd_workspace_bytes(100, 64, 40, F16) >= 2 * 100 * 40 * 2
     assert lib.pdr_rms_norm_bwd_workspace_bytes(100, 64) >= 64 * 4
 
@@ -35,10 +40,12 @@ def test_workspace_sizes(lib):
 @pytest.mark.parametrize("args", [(-1, 8, 64, BF16), (1, 0, 64, BF16), (1, 8, 0, BF16), (1, 8, 64, F32),
                                   (1, 8, 64, 9), (1, 65537, 64, BF16), (1, 8, 65537, BF16)])
 def test_workspace_sizes_of_bad_arguments(lib, args):
-    assert lib.pdr_linear_workspace_bytes(*args) == 0
+    assert lib.pdr_linear_workspace_bytes(4, 8, 64, BF16, E4M3, 0) == 0
+    assert lib.pdr_gated_workspace_bytes(4, 64, 8, BF16, E4M3) == 0
+    assert lib.pdr_linear_workspace_bytes(*args, F32, 1) == 0
     assert lib.pdr_linear_bwd_workspace_bytes(*args, F32, 0) == 0
     M, N, K, t = args
-    assert lib.pdr_gated_workspace_bytes(M, K, N, t) == 0
+    assert lib.pdr_gated_workspace_bytes(M, K, N, t, BF16) == 0
     assert lib.pdr_gated_bwd_workspace_bytes(M, K, N, t) == 0
 
 
@@ -55,7 +62,7 @@ def test_linear_fwd_refusals(lib):
     for bad in [dict(M=-1), dict(N=0), dict(K=0), dict(dtype=F32), dict(dtype=7), dict(yt=E4M3), dict(act=5),
                 dict(act=-1), dict(x=None), dict(w=None), dict(y=None), dict(xs=P), dict(ws=P),
                 dict(dtype=E4M3), dict(dtype=E4M3, xs=P), dict(dtype=E4M3, ws=P), dict(bt=E4M3), dict(bt=9),
-                dict(x=P + 8), dict(w=P + 2), dict(y=P + 2), dict(res=P + 1), dict(bias=P + 2),
+                dict(x=P + 8), dict(w=P + 2), dict(y=P + 8), dict(res=P + 16), dict(bias=P + 2),
                 dict(K=63), dict(K=63, wsp=P + 16, wsn=1 << 30)]:
         assert call(**bad) == INVALID, bad
     assert call(K=63, wsp=P, wsn=100) == SMALL
@@ -73,8 +80,8 @@ def test_linear_bwd_refusals(lib):
                                   a["M"], a["N"], a["K"], a["dx"], a["dw"], a["db"], a["wsp"], a["wsn"], None)
 
     for bad in [dict(M=-1), dict(N=0), dict(K=0), dict(dtype=F32), dict(dtype=E4M3), dict(gt=E4M3), dict(act=9),
-                dict(g=None), dict(x=None), dict(w=None), dict(bt=E4M3), dict(g=P + 4), dict(x=P + 4),
-                dict(w=P + 4), dict(dx=P + 1), dict(dw=P + 1), dict(db=P + 1), dict(wsp=None), dict(wsp=P + 8)]:
+                dict(g=None), dict(x=None), dict(w=None), dict(bt=E4M3), dict(g=P + 16), dict(x=P + 4),
+                dict(w=P + 4), dict(dx=P + 8), dict(dw=P + 8), dict(db=P + 1), dict(wsp=None), dict(wsp=P + 8)]:
         assert call(**bad) == INVALID, bad
     assert call(wsn=8) == SMALL
     assert call(K=65537) == LARGE
@@ -87,7 +94,7 @@ def test_gated_refusals(lib):
 
     for bad in [dict(M=-1), dict(D=0), dict(Fw=0), dict(t=F32), dict(ht=E4M3), dict(act=7), dict(x=None),
                 dict(g=None), dict(u=None), dict(h=None), dict(xs=P), dict(gs=P), dict(t=E4M3, xs=P, gs=P),
-                dict(x=P + 2), dict(g=P + 2), dict(u=P + 2), dict(h=P + 1), dict(D=63)]:
+                dict(x=P + 2), dict(g=P + 2), dict(u=P + 2), dict(h=P + 8), dict(D=63)]:
         assert fwd(**bad) == INVALID, bad
     assert fwd(D=63, w=P, n=1) == SMALL
     assert fwd(D=70000) == LARGE
@@ -96,7 +103,7 @@ def test_gated_refusals(lib):
         return lib.pdr_gated_bwd(g, x, wg, wu, t, act, M, D, Fw, dx, dg, du, w, n, None)
 
     for bad in [dict(M=-1), dict(t=E4M3), dict(t=F32), dict(g=None), dict(x=None), dict(wg=None), dict(wu=None),
-                dict(dg=None), dict(du=None), dict(w=None), dict(w=P + 32), dict(x=P + 2), dict(g=P + 1)]:
+                dict(dg=None), dict(du=None), dict(w=None), dict(w=P + 32), dict(x=P + 2), dict(g=P + 16)]:
         assert bwd(**bad) == INVALID, bad
     assert bwd(n=16) == SMALL
 
