@@ -65,6 +65,7 @@ struct __align__(64) GemmParams {
     int sharing;                      // epilogue groups that share a tile
     int stationary;                   // B of a column of tiles stays in shared memory
     int per_stage;                    // k blocks of a stage
+    int nbuf;                         // buffers of an epilogue warp (1 or 2)
     int b_bytes, kelems;              // a block's B bytes, and k, of a k block
     unsigned idesc;
     unsigned long long adesc, bdesc;  // smem descriptors without the address
@@ -267,11 +268,21 @@ __device__ __forceinline__ void stage_narrow(char *buffer, const unsigned (&w)[k
         *reinterpret_cast<uint4 *>(buffer + lane * 32 + (j ^ ((lane >> 2) & 1)) * 16) =
             make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
-// Before the buffer is written again: its last stores have read it.
-__device__ __forceinline__ void buffer_free() {
-    if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    __syncwarp();
-}
+// A warp's buffers in turn: the next one, when the stores before have read it.
+struct Staging {
+    char *base;
+    int nbuf, turn;
+    __device__ __forceinline__ char *next() {
+        if (nbuf == 2) {
+            if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            turn ^= kBufferBytes;
+        } else {
+            if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        }
+        __syncwarp();
+        return base + turn;
+    }
+};
 __device__ __forceinline__ void tma_store(const CUtensorMap *map, const char *buffer, int x, int y, int z) {
     asm volatile(
         "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
@@ -418,12 +429,12 @@ template <int EPI, int ACT>
 __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t, unsigned acc,
                                               unsigned ready, unsigned phase, int c0, int c1,
                                               int quarter, float *columns, int &have_n,
-                                              float *buffer, int *abort, unsigned release) {
+                                              Staging &staging, int *abort, unsigned release) {
     constexpr bool kTwo = EPI == kEpiGated || EPI == kEpiGatedBwd;  // g and u
     constexpr int C = EPI == kEpiGated ? 32 : 16;                   // columns at once
     const int lane = threadIdx.x & 31;
     const int row0 = t.m * kBM + 32 * quarter, n0 = t.n * p.bcols;
-    char *const stage = reinterpret_cast<char *>(buffer);
+    char *stage = nullptr;
     c1 = min(c1, p.N - n0);
     // (A warp behind the last row of a tile still writes its column sums: zeros.)
     const bool any = (EPI == kEpiSlope ? t.m * kBM : row0) < p.M && c0 < c1, on = row0 + lane < p.M;
@@ -506,7 +517,7 @@ __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t
         const int half = C == 32 ? 0 : (c - c0) / kChunk & 1;
         const int slice = t.split * p.nz + t.z;
         if constexpr (EPI == kEpiGatedBwd) {
-            buffer_free();
+            stage = staging.next();
             pack_row(p.out_dtype, v, w);
             stage_narrow(stage, w);
             pack_row(p.out_dtype, u, w);
@@ -516,12 +527,12 @@ __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t
 #pragma unroll
             for (int i = 0; i < C; i += kChunk) {
                 if (n0 + c + i >= p.N) break;
-                buffer_free();
+                stage = staging.next();
                 stage_floats(stage, v + i);
                 store_buffer(&p.o[0], nullptr, stage, n0 + c + i, row0, slice);
             }
         } else {
-            if (half == 0) buffer_free();
+            if (half == 0) stage = staging.next();
 #pragma unroll
             for (int i = 0; i < C; i += kChunk) {
                 pack_row(p.out_dtype, v + i, w);
@@ -619,8 +630,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int stage_bytes = p.per_stage * block_bytes;
     char *held = smem + p.stages * stage_bytes;  // B of all k, where it stays
     char *after = held + (p.stationary ? p.kb * p.b_bytes : 0);
-    float *buffers = reinterpret_cast<float *>(after);  // one per epilogue warp, 1024-byte aligned
-    float *columns_all = buffers + kEpiWarps * kBufferBytes / 4;  // [warp][3][kMaxCols]
+    char *buffers = after;  // nbuf per epilogue warp, 1024-byte aligned
+    float *columns_all = reinterpret_cast<float *>(buffers + kEpiWarps * p.nbuf * kBufferBytes);  // [warp][3][kMaxCols]
     Barriers *bars = reinterpret_cast<Barriers *>(columns_all + kEpiWarps * 3 * kMaxCols);
     const int warp = threadIdx.x >> 5;
     const int rank = blockIdx.x & 1;  // in the pair; block 0 leads
@@ -664,7 +675,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp >= kEpiWarp) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         const int ew = warp - kEpiWarp, group = ew >> 2, quarter = warp & 3;
-        float *buffer = buffers + ew * (kBufferBytes / 4);
+        Staging staging = {buffers + ew * p.nbuf * kBufferBytes, p.nbuf, 0};
         float *columns = columns_all + ew * 3 * kMaxCols;
         // `sharing` groups divide a tile's columns, sets of them take tiles in turn.
         const int cols = p.bcols / p.sharing, cfirst = group % p.sharing * cols;
@@ -679,10 +690,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 bool ok;
                 if constexpr (NARROW)
                     ok = epilogue_narrow<ACT>(p, tile, d, acc_full + 8 * acc, acc_phase, quarter,
-                                              columns, have_n, buffer, abort, release + 8 * acc);
+                                              columns, have_n, reinterpret_cast<float *>(staging.base), abort,
+                                              release + 8 * acc);
                 else
                     ok = epilogue_tile<EPI, ACT>(p, tile, d, acc_full + 8 * acc, acc_phase, cfirst,
-                                                 cfirst + cols, quarter, columns, have_n, buffer,
+                                                 cfirst + cols, quarter, columns, have_n, staging,
                                                  abort, release + 8 * acc);
                 if (!ok) break;
             }
@@ -878,36 +890,54 @@ __global__ void __launch_bounds__(256) k_unpack(const T *__restrict__ from, long
     }
 }
 
-// Four neighbouring columns per thread; the splits are added in order, eight
-// loads under way at once.
+// Four neighbouring columns per thread.  Y rows of threads add a Y-th of the splits
+// each, in order, and their sums are added in order: 8 where there are too few columns to
+// fill the machine.
+template <int Y>
 __global__ void __launch_bounds__(256) k_join(const float *__restrict__ part, int splits, int rows,
                                               int cols, long long ld, void *to, void *to2,
                                               int dtype) {
+    constexpr int X = 256 / Y;
+    __shared__ float4 sums[Y][X];
     grid_dep_wait();
     const long long n = rows * ld, stride = n * (to2 ? 2 : 1);
     part += blockIdx.y * n;
     if (blockIdx.y) to = to2;
-    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (i >= n) return;
+    const int x = threadIdx.x % X, y = threadIdx.x / X;
+    const long long i = ((long long)blockIdx.x * X + x) * 4;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int j = 0; j < splits; j += 8) {
-        float4 v[8];
+    const int j1 = (y + 1) * splits / Y;
+    if (i < n)
+        for (int j = y * splits / Y; j < j1; j += 8) {
+            float4 v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (j + k < splits) v[k] = __ldg(reinterpret_cast<const float4 *>(part + (j + k) * stride + i));
+            for (int k = 0; k < 8; ++k)
+                if (j + k < j1) v[k] = __ldg(reinterpret_cast<const float4 *>(part + (j + k) * stride + i));
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (j + k < splits) {
-                s.x += v[k].x;
-                s.y += v[k].y;
-                s.z += v[k].z;
-                s.w += v[k].w;
-            }
+            for (int k = 0; k < 8; ++k)
+                if (j + k < j1) {
+                    s.x += v[k].x;
+                    s.y += v[k].y;
+                    s.z += v[k].z;
+                    s.w += v[k].w;
+                }
+        }
+    if constexpr (Y > 1) {
+        sums[y][x] = s;
+        __syncthreads();
+    }
+    if (y || i >= n) return;
+#pragma unroll
+    for (int k = 1; k < Y; ++k) {
+        s.x += sums[k][x].x;
+        s.y += sums[k][x].y;
+        s.z += sums[k][x].z;
+        s.w += sums[k][x].w;
     }
     const long long r = i / ld;
     const int c = (int)(i - r * ld);
     const size_t at = (size_t)(r * cols + c);
-    if (c + 4 <= cols && cols % 4 == 0 && dtype != PDR_F32 && (reinterpret_cast<uintptr_t>(to) & 7) == 0) {
+    if (c + 4 <= cols && cols % 4 == 0 && dtype != PDR_F32) {  // (results start at 16 bytes)
         const uint2 w = make_uint2(pack2(s.x, s.y, dtype), pack2(s.z, s.w, dtype));
         *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(to) + at) = w;
     } else {
@@ -929,7 +959,13 @@ __global__ void __launch_bounds__(1024) k_join_columns(const float *__restrict__
     const long long c = (long long)blockIdx.x * 32 + x;
     float s = 0.0f;
     if (c < cols)
-        for (long long r = y; r < rows; r += 32) s += part[r * cols + c];
+        for (long long r = y; r < rows; r += 32 * 8) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = r + 32 * k < rows ? __ldg(part + (r + 32 * k) * cols + c) : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += v[k];
+        }
     sums[y][x] = s;
     __syncthreads();
     if (y == 0 && c < cols) {
@@ -939,38 +975,53 @@ __global__ void __launch_bounds__(1024) k_join_columns(const float *__restrict__
     }
 }
 
-constexpr int kGroupRows = 512;  // rows whose column sums one block forms
+// Rows of a group whose column sums one block forms: about four blocks per SM, at
+// least 64 rows.
+long long group_rows(long long M) {
+    const long long r = (M + 4 * kSMs - 1) / (4 * kSMs);
+    return r < 64 ? 64 : r;
+}
 
-// Threads walk over (row, column) of a group of rows; a thread keeps its
-// column (cols <= 256: 256 / cols rows at once; else column after column).
-__global__ void __launch_bounds__(256) k_cast_columns(const void *__restrict__ dy, int dy_dtype,
+template <typename T>
+__device__ __forceinline__ float widen(T v, int dtype) {
+    if constexpr (sizeof(T) == 4)
+        return v;
+    else
+        return unpack2(v, dtype).x;
+}
+
+// A block takes a group of rows and 256 columns (all of them where there are fewer,
+// 256 / N rows at once); a thread keeps its column, four rows under way at once.
+template <typename T>
+__global__ void __launch_bounds__(256) k_cast_columns(const T *__restrict__ dy, int dy_dtype,
                                                       long long M, int N, void *__restrict__ dz,
-                                                      int dz_dtype, long long ldz,
+                                                      int dz_dtype, long long ldz, long long group,
                                                       float *__restrict__ colsum) {
     __shared__ float sums[256];
     grid_dep_wait();
-    const long long r0 = (long long)blockIdx.x * kGroupRows;
-    const long long r1 = r0 + kGroupRows < M ? r0 + kGroupRows : M;
+    const long long r0 = blockIdx.x * group, r1 = r0 + group < M ? r0 + group : M;
+    const int base = blockIdx.y * 256, width = N - base < 256 ? N - base : 256;
     const int per = N < 256 ? 256 / N : 1;  // rows at once
-    for (int base = 0; base < N; base += 256) {
-        const int width = N - base < 256 ? N - base : 256;
-        const int sub = threadIdx.x / width, c = base + threadIdx.x % width;
-        float s = 0.0f;
-        if (sub < per)
-            for (long long r = r0 + sub; r < r1; r += per) {
-                const float v = img_load(dy, (size_t)(r * N + c), dy_dtype);
-                s += v;
-                if (dz) img_store(dz, (size_t)(r * ldz + c), dz_dtype, v);
-            }
-        if (colsum) {
-            __syncthreads();
-            sums[threadIdx.x] = s;
-            __syncthreads();
-            if ((int)threadIdx.x < width) {
-                for (int j = 1; j < per; ++j) s += sums[threadIdx.x + j * width];
-                colsum[(long long)blockIdx.x * N + c] = s;
+    const int sub = threadIdx.x / width, c = base + threadIdx.x % width;
+    float s = 0.0f;
+    if (sub < per)
+        for (long long r = r0 + sub; r < r1; r += 4 * per) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[k] = r + k * per < r1 ? widen<T>(__ldg(dy + (r + k * per) * N + c), dy_dtype) : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                s += v[k];
+                if (dz && r + k * per < r1) img_store(dz, (size_t)((r + k * per) * ldz + c), dz_dtype, v[k]);
             }
         }
+    if (!colsum) return;
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    if ((int)threadIdx.x < width) {
+        for (int j = 1; j < per; ++j) s += sums[threadIdx.x + j * width];
+        colsum[(long long)blockIdx.x * N + c] = s;
     }
 }
 
@@ -1077,18 +1128,30 @@ bool gemm_narrow(int N, int out_dtype, bool has_in) {
     return N <= kChunk && (row % 16 || (has_in && row % 32));
 }
 
-int gemm_tile_columns(int epi, int M, int N, int nz) {
+int gemm_tile_columns(int epi, int M, int N, int nz, long long kb) {
     const bool dual = epi == kEpiGated || epi == kEpiGatedBwd;
-    const int least = 32, most = dual ? 128 : 256;
-    int c = most;
-    // No wider than the result, and narrower while the tiles do not fill the machine.
-    while (c > least && c / 2 >= N) c /= 2;
-    while (c > least && (long long)ceil_div(M, kBM) * ceil_div(N, c) * nz < kSMs) c /= 2;
-    return c;
+    // The width whose rounds of tiles over the pairs take least, in clocks as
+    // measured: 560 + 4/3 per accumulator column and k block (the copies' way
+    // from L2 bounds them), 16 per column in the epilogue beside the next tile's
+    // products, and the first tile's start and the last one's end.
+    int best = 32;
+    double least = -1;
+    for (int c = dual ? 128 : 256; c >= 32; c /= 2) {
+        const long long tiles = (long long)ceil_div(M, 2 * kBM) * ceil_div(N, c) * nz;
+        const int bn = dual ? 2 * c : c;
+        const double products = kb * (560 + 4 * bn / 3), ends = 16.0 * bn;
+        const double cost = (tiles + kSMs / 2 - 1) / (kSMs / 2) * (products > ends ? products : ends) +
+                            3000 + ends;
+        if (least < 0 || cost < least) {
+            least = cost;
+            best = c;
+        }
+    }
+    return best;
 }
 
 int gemm_splits(int M, int N, int nz, long long K) {
-    const int cols = gemm_tile_columns(kEpiLinear, 1 << 30, N, nz);
+    const int cols = gemm_tile_columns(kEpiLinear, 1 << 30, N, nz, 32);
     const long long tiles = (long long)ceil_div(M, 2 * kBM) * ceil_div(N, cols) * nz;
     const long long kb = (K + 63) / 64;
     long long s = kSMs / 2 / tiles;
@@ -1108,16 +1171,17 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     p.N = g.N;
     p.nz = g.mode == kBatchA ? 2 : 1;
     p.splits = g.splits;
-    p.bcols = gemm_tile_columns(g.epi, g.splits > 1 ? 1 << 30 : g.M, g.N, p.nz);
+    p.kb0 = ceil_div(g.K[0], kelems);
+    p.kb = p.kb0 + (g.mode == kTwoSources ? ceil_div(g.K[1], kelems) : 0);
+    p.kelems = kelems;
+    p.bcols = g.splits > 1 ? gemm_tile_columns(g.epi, 1 << 30, g.N, p.nz, 32)
+                           : gemm_tile_columns(g.epi, g.M, g.N, p.nz, p.kb);
     p.bn = dual ? 2 * p.bcols : p.bcols;
     p.nm = divisor(ceil_div(g.M, 2 * kBM));
     p.nn = divisor(ceil_div(g.N, p.bcols));
     const long long tiles = (long long)p.nm.d * p.nn.d * p.nz * p.splits;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
     p.tiles = (int)tiles;
-    p.kb0 = ceil_div(g.K[0], kelems);
-    p.kb = p.kb0 + (g.mode == kTwoSources ? ceil_div(g.K[1], kelems) : 0);
-    p.kelems = kelems;
     p.b_bytes = g.b_mn ? ceil_div(p.bn / 2, 64) * 8192 : p.bn / 2 * kRowBytes;
     p.nacc = p.bn >= 256 ? 2 : 4;
     // Two or four groups share a tile, 64 columns a warp, and sets of groups take
@@ -1165,12 +1229,16 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     p.in_dtype = g.in_dtype;
     p.ldi = g.ldi;
     p.colsum = g.colsum;
-    const size_t fixed = 1024 + 512 + kEpiWarps * (3 * kMaxCols * 4 + kBufferBytes);
-    const size_t room = kSmemBytes - fixed, all_b = (size_t)p.kb * p.b_bytes;
+    const size_t all_b = (size_t)p.kb * p.b_bytes;
     const int pairs = p.tiles < kSMs / 2 ? p.tiles : kSMs / 2;
+    const size_t fixed = 1024 + 512 + kEpiWarps * 3 * kMaxCols * 4, buffers = kEpiWarps * kBufferBytes;
+    size_t room = kSmemBytes - fixed - buffers;
     // B stays where it leaves room for three stages of A and a pair has several
     // tiles to use it for.
     p.stationary = g.splits == 1 && all_b + 3 * kABytes <= room && p.tiles >= 2 * pairs;
+    // A second buffer for each epilogue warp, where that takes no stage that is needed.
+    p.nbuf = p.stationary && all_b + 4 * kABytes + buffers <= room ? 2 : 1;
+    room -= (p.nbuf - 1) * buffers;
     // A stage of two k blocks, where there are as many and room for three stages,
     // halves the waits and counts beside the copies and products: one thread takes some 700
     // clocks for those of a stage beside a busy epilogue, as long as 16 KB take at
@@ -1180,7 +1248,7 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     const size_t stage = p.per_stage * (kABytes + (p.stationary ? 0 : p.b_bytes));
     p.stages = (int)(left / stage);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
-    const size_t smem = fixed + p.stages * stage + (p.stationary ? all_b : 0);
+    const size_t smem = fixed + p.nbuf * buffers + p.stages * stage + (p.stationary ? all_b : 0);
     const int grid = 2 * pairs;
     static_assert(sizeof(Barriers) <= 512, "barriers fit their place");
     switch (g.epi) {
@@ -1222,9 +1290,11 @@ cudaError_t launch_unpack(const void *from, long long rows, long long cols, long
 
 cudaError_t launch_join(const float *part, int splits, int rows, int cols, long long ld, void *to,
                         void *to2, int dtype, cudaStream_t s) {
-    const long long blocks = (rows * ld / 4 + 255) / 256;
-    return launch_dependent(k_join, dim3((unsigned)blocks, to2 ? 2 : 1), dim3(256), 0, s, part, splits,
-                            rows, cols, ld, to, to2, dtype);
+    const long long vectors = rows * ld / 4;
+    const bool few = vectors < 256 * kSMs;
+    const dim3 grid((unsigned)((vectors + (few ? 31 : 255)) / (few ? 32 : 256)), to2 ? 2 : 1);
+    return launch_dependent(few ? k_join<8> : k_join<1>, grid, dim3(256), 0, s, part, splits, rows, cols, ld,
+                            to, to2, dtype);
 }
 
 cudaError_t launch_join_columns(const float *part, long long rows, long long cols, void *to,
@@ -1233,12 +1303,20 @@ cudaError_t launch_join_columns(const float *part, long long rows, long long col
                             part, rows, cols, to, dtype);
 }
 
-long long column_groups(long long M) { return (M + kGroupRows - 1) / kGroupRows; }
+long long column_groups(long long M) {
+    const long long g = group_rows(M);
+    return (M + g - 1) / g;
+}
 
 cudaError_t launch_cast_columns(const void *dy, int dy_dtype, long long M, int N, void *dz,
                                 int dz_dtype, long long ldz, float *colsum, cudaStream_t s) {
-    return launch_dependent(k_cast_columns, dim3((unsigned)column_groups(M)), dim3(256), 0, s, dy,
-                            dy_dtype, M, N, dz, dz_dtype, ldz, colsum);
+    const dim3 grid((unsigned)column_groups(M), (unsigned)((N + 255) / 256));
+    if (dy_dtype == PDR_F32)
+        return launch_dependent(k_cast_columns<float>, grid, dim3(256), 0, s, static_cast<const float *>(dy),
+                                dy_dtype, M, N, dz, dz_dtype, ldz, group_rows(M), colsum);
+    return launch_dependent(k_cast_columns<unsigned short>, grid, dim3(256), 0, s,
+                            static_cast<const unsigned short *>(dy), dy_dtype, M, N, dz, dz_dtype, ldz,
+                            group_rows(M), colsum);
 }
 
 cudaError_t read_wait_error(int *bits, cudaStream_t s) {

@@ -173,8 +173,9 @@ struct GemmArgs {
 // Whether a linear result of N columns (with an input of its type) is so narrow that
 // rows which TMA could not store, or the input's sectors, are taken as they are.
 bool gemm_narrow(int N, int out_dtype, bool has_in);
-// Columns of a tile that launch_gemm picks for a result of M x N (x nz products).
-int gemm_tile_columns(int epi, int M, int N, int nz);
+// Columns of a tile that launch_gemm picks for a result of M x N (x nz products) over
+// kb k blocks.
+int gemm_tile_columns(int epi, int M, int N, int nz, long long kb);
 // Tiles along k that fill the machine for a weight gradient, at most `most`.
 int gemm_splits(int M, int N, int nz, long long K);
 cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s);
