@@ -76,18 +76,24 @@ GatedLayout bwd_layout(int M, int D, int F, int dtype) {
     return L;
 }
 
-// Rows that no TMA copy can address (not a multiple of 16 bytes long) in
-// padded copies.
-cudaError_t pack_rows(const GatedLayout &L, const void *&x, const void *&wg, const void *&wu, int M,
-                      int D, int F, int e, char *ws, cudaStream_t s) {
-    if (!L.pack_x) return cudaSuccess;
-    cudaError_t err = launch_pack(x, M, D, e, ws + L.x, L.ldk, s);
-    if (err == cudaSuccess) err = launch_pack(wg, F, D, e, ws + L.wg, L.ldk, s);
-    if (err == cudaSuccess) err = launch_pack(wu, F, D, e, ws + L.wu, L.ldk, s);
-    x = ws + L.x;
-    wg = ws + L.wg;
-    wu = ws + L.wu;
-    return err;
+// Padded copies of x and the weights, and (backward) of dh.
+cudaError_t pack_rows(const GatedLayout &L, const void *&x, const void *&wg, const void *&wu,
+                      const void **dh, int M, int D, int F, int e, char *ws, cudaStream_t s) {
+    PackJob jobs[4];
+    int n = 0;
+    if (L.pack_x) {
+        jobs[n++] = {x, ws + L.x, M, D, L.ldk, e};
+        jobs[n++] = {wg, ws + L.wg, F, D, L.ldk, e};
+        jobs[n++] = {wu, ws + L.wu, F, D, L.ldk, e};
+        x = ws + L.x;
+        wg = ws + L.wg;
+        wu = ws + L.wu;
+    }
+    if (dh && L.pack_in) {
+        jobs[n++] = {*dh, ws + L.in, M, F, L.ldi, 2};
+        *dh = ws + L.in;
+    }
+    return launch_pack(jobs, n, s);
 }
 
 pdr_status done(cudaError_t e) { return e == cudaSuccess ? PDR_OK : PDR_ERR_CUDA; }
@@ -127,7 +133,7 @@ pdr_status pdr_gated_fwd(const void *x, const void *w_gate, const void *w_up, in
     if (workspace_bytes < L.total) return PDR_ERR_WORKSPACE_TOO_SMALL;
     if (M == 0) return PDR_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (pack_rows(L, x, w_gate, w_up, M, D, F, dtype_bytes(dtype), static_cast<char *>(workspace),
+    if (pack_rows(L, x, w_gate, w_up, nullptr, M, D, F, dtype_bytes(dtype), static_cast<char *>(workspace),
                   s) != cudaSuccess)
         return PDR_ERR_CUDA;
     GemmArgs g;
@@ -183,11 +189,7 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
     }
     if (!grad_x && !grad_gate) return PDR_OK;
     char *ws = static_cast<char *>(workspace);
-    if (pack_rows(L, x, w_gate, w_up, M, D, F, 2, ws, s) != cudaSuccess) return PDR_ERR_CUDA;
-    if (L.pack_in) {
-        if (launch_pack(grad, M, F, 2, ws + L.in, L.ldi, s) != cudaSuccess) return PDR_ERR_CUDA;
-        grad = ws + L.in;
-    }
+    if (pack_rows(L, x, w_gate, w_up, &grad, M, D, F, 2, ws, s) != cudaSuccess) return PDR_ERR_CUDA;
     const Operand ox = {x, M, D, L.ldk}, og = {w_gate, F, D, L.ldk}, ou = {w_up, F, D, L.ldk};
     const Operand odg = {ws + L.dg, M, F, L.ldf}, odu = {ws + L.du, M, F, L.ldf};
     {

@@ -843,25 +843,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ---- small kernels -----------------------------------------------------------
 
-// Dense rows to rows of ld elements (a multiple of 16 bytes): 16 bytes per thread.
+// Dense rows to padded rows, 16 bytes per thread, a row per warp; several matrices
+// in one launch.
+struct PackJobs {
+    PackJob job[4];
+    int n;
+    unsigned first[5];  // block of each job
+};
 template <typename T>
-__global__ void __launch_bounds__(256) k_pack(const T *__restrict__ from, long long rows, int cols,
-                                              T *__restrict__ to, int vectors) {
+__device__ __forceinline__ uint4 padded_vector(const T *row, int v, int cols) {
     constexpr int E = 16 / sizeof(T);
-    grid_dep_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (long long r = (long long)blockIdx.x * 8 + warp; r < rows; r += (long long)gridDim.x * 8) {
-        const T *row = from + r * cols;
-        for (int v = lane; v < vectors; v += 32) {
-            union {
-                T e[E];
-                uint4 u;
-            } w;
+    if constexpr (sizeof(T) == 2)
+        if (v * E + E <= cols) {  // by words of 4 bytes, whatever the row's parity
+            const bool odd = reinterpret_cast<uintptr_t>(row) & 2;
+            const unsigned *q = reinterpret_cast<const unsigned *>(row + v * E - odd);
+            unsigned w[5];
 #pragma unroll
-            for (int i = 0; i < E; ++i) w.e[i] = v * E + i < cols ? __ldg(row + v * E + i) : T(0);
-            *reinterpret_cast<uint4 *>(to + (r * vectors + v) * E) = w.u;
+            for (int i = 0; i < 4; ++i) w[i] = __ldg(q + i);
+            w[4] = odd ? __ldg(q + 4) : 0;  // (odd rows have no multiple of 8 elements: it is inside)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = odd ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+            return make_uint4(w[0], w[1], w[2], w[3]);
         }
+    union {
+        T e[E];
+        uint4 u;
+    } w;
+#pragma unroll
+    for (int i = 0; i < E; ++i) w.e[i] = v * E + i < cols ? __ldg(row + v * E + i) : T(0);
+    return w.u;
+}
+template <typename T>
+__device__ __forceinline__ void pack_rows(const PackJob &j, unsigned block, unsigned blocks) {
+    constexpr int E = 16 / sizeof(T);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, vectors = (int)(j.ld / E);
+    for (long long r = (long long)block * 8 + warp; r < j.rows; r += (long long)blocks * 8) {
+        const T *row = static_cast<const T *>(j.from) + r * j.cols;
+        uint4 *to = static_cast<uint4 *>(j.to) + r * vectors;
+        for (int v = lane; v < vectors; v += 32) to[v] = padded_vector(row, v, (int)j.cols);
     }
+}
+__global__ void __launch_bounds__(256) k_pack(const PackJobs p) {
+    grid_dep_wait();
+    int i = 0;
+    while (i + 1 < p.n && blockIdx.x >= p.first[i + 1]) ++i;
+    const PackJob &j = p.job[i];
+    const unsigned block = blockIdx.x - p.first[i], blocks = p.first[i + 1] - p.first[i];
+    if (j.bytes == 1)
+        pack_rows<unsigned char>(j, block, blocks);
+    else if (j.bytes == 2)
+        pack_rows<unsigned short>(j, block, blocks);
+    else
+        pack_rows<unsigned>(j, block, blocks);
 }
 
 // And back.  Elements of 16 bits go in pairs that start at 4 bytes.
@@ -1264,23 +1297,22 @@ unsigned copy_blocks(long long rows) {
     return (unsigned)(rows / 8 + 1 < 16 * kSMs ? rows / 8 + 1 : 16 * kSMs);
 }
 template <typename T>
-cudaError_t pack_as(const void *from, long long rows, long long cols, void *to, long long ld, cudaStream_t s) {
-    return launch_dependent(k_pack<T>, dim3(copy_blocks(rows)), dim3(256), 0, s,
-                            static_cast<const T *>(from), rows, (int)cols, static_cast<T *>(to),
-                            (int)(ld * sizeof(T) / 16));
-}
-template <typename T>
 cudaError_t unpack_as(const void *from, long long rows, long long cols, long long ld, void *to, cudaStream_t s) {
     return launch_dependent(k_unpack<T>, dim3(copy_blocks(rows)), dim3(256), 0, s,
                             static_cast<const T *>(from), rows, (int)cols, (int)ld, static_cast<T *>(to));
 }
 }  // namespace
 
-cudaError_t launch_pack(const void *from, long long rows, long long cols, int bytes, void *to,
-                        long long ld, cudaStream_t s) {
-    return bytes == 1   ? pack_as<unsigned char>(from, rows, cols, to, ld, s)
-           : bytes == 2 ? pack_as<unsigned short>(from, rows, cols, to, ld, s)
-                        : pack_as<unsigned>(from, rows, cols, to, ld, s);
+cudaError_t launch_pack(const PackJob *jobs, int n, cudaStream_t s) {
+    PackJobs p = {};
+    for (int i = 0; i < n; ++i)
+        if (jobs[i].rows > 0) {
+            p.job[p.n] = jobs[i];
+            p.first[p.n + 1] = p.first[p.n] + copy_blocks(jobs[i].rows);
+            ++p.n;
+        }
+    if (p.n == 0) return cudaSuccess;
+    return launch_dependent(k_pack, dim3(p.first[p.n]), dim3(256), 0, s, p);
 }
 cudaError_t launch_unpack(const void *from, long long rows, long long cols, long long ld, int bytes,
                           void *to, cudaStream_t s) {

@@ -184,10 +184,16 @@ cudaError_t read_wait_error(int *bits, cudaStream_t s);
 
 // ---- small kernels around the products ---------------------------------------
 
-// Dense rows of `cols` elements (of 1, 2 or 4 bytes) to rows of `ld` elements, a
-// multiple of 16 bytes (zeros behind), and (2 or 4 bytes) back.
-cudaError_t launch_pack(const void *from, long long rows, long long cols, int bytes, void *to,
-                        long long ld, cudaStream_t s);
+// Dense rows of `cols` elements (of 1, 2 or 4 bytes; 16-byte aligned) to rows of
+// `ld` elements, a multiple of 16 bytes (zeros behind), up to four matrices in one
+// launch; and (2 or 4 bytes) back.
+struct PackJob {
+    const void *from;
+    void *to;
+    long long rows, cols, ld;
+    int bytes;
+};
+cudaError_t launch_pack(const PackJob *jobs, int n, cudaStream_t s);
 cudaError_t launch_unpack(const void *from, long long rows, long long cols, long long ld, int bytes,
                           void *to, cudaStream_t s);
 // Elements of a row padded to `unit` bytes.

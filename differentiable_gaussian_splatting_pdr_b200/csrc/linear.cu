@@ -142,17 +142,19 @@ pdr_status pdr_linear_fwd(const void *x, const void *weight, int dtype, const fl
     g.b[0] = {weight, N, K, L.ldk};
     char *ws = static_cast<char *>(workspace);
     const int e = dtype_bytes(dtype), o = dtype_bytes(y_dtype);
-    cudaError_t err = cudaSuccess;
+    PackJob jobs[3];
+    int n = 0;
     if (L.pack_x) {
-        err = launch_pack(x, M, K, e, ws + L.x, L.ldk, s);
-        if (err == cudaSuccess) err = launch_pack(weight, N, K, e, ws + L.w, L.ldk, s);
+        jobs[n++] = {x, ws + L.x, M, K, L.ldk, e};
+        jobs[n++] = {weight, ws + L.w, N, K, L.ldk, e};
         g.a[0].p = ws + L.x;
         g.b[0].p = ws + L.w;
     }
-    if (err == cudaSuccess && L.pack_in) {
-        err = launch_pack(residual, M, N, o, ws + L.in, L.ldi, s);
+    if (L.pack_in) {
+        jobs[n++] = {residual, ws + L.in, M, N, L.ldi, o};
         residual = ws + L.in;
     }
+    cudaError_t err = launch_pack(jobs, n, s);
     g.narrow = L.narrow;
     g.act = activation;
     g.out = L.pack_out ? ws + L.out : y;
@@ -205,21 +207,18 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
     char *ws = static_cast<char *>(workspace);
     const bool act = activation != PDR_ACT_NONE, products = grad_x || grad_weight;
     if (!products && !grad_bias) return PDR_OK;
-    if (L.pack_x) {
-        if (act || grad_weight) {
-            e = launch_pack(x, M, K, 2, ws + L.x, L.ldk, s);
-            x = ws + L.x;
-        }
-        if (e == cudaSuccess && (act || grad_x)) {
-            e = launch_pack(weight, N, K, 2, ws + L.w, L.ldk, s);
-            weight = ws + L.w;
-        }
-        if (e != cudaSuccess) return PDR_ERR_CUDA;
+    PackJob jobs[3];
+    int n = 0;
+    if (L.pack_x && (act || grad_weight)) {
+        jobs[n++] = {x, ws + L.x, M, K, L.ldk, 2};
+        x = ws + L.x;
     }
-    if (L.pack_in) {
-        e = launch_pack(grad, M, N, dtype_bytes(grad_dtype), ws + L.in, L.ldi, s);
-        if (e != cudaSuccess) return PDR_ERR_CUDA;
+    if (L.pack_x && (act || grad_x)) {
+        jobs[n++] = {weight, ws + L.w, N, K, L.ldk, 2};
+        weight = ws + L.w;
     }
+    if (L.pack_in) jobs[n++] = {grad, ws + L.in, M, N, L.ldi, dtype_bytes(grad_dtype)};
+    if (launch_pack(jobs, n, s) != cudaSuccess) return PDR_ERR_CUDA;
     float *colsum = grad_bias ? reinterpret_cast<float *>(ws + L.colsum) : nullptr;
     const Operand ox = {x, M, K, L.ldk}, ow = {weight, N, K, L.ldk};
     Operand oz = {L.cast ? ws + L.dz : grad, M, N, L.ldz};

@@ -16,7 +16,7 @@ and limits are in include/pdr.h.
 """
 from __future__ import annotations
 
-import ctypes
+import functools
 from dataclasses import dataclass, replace
 
 import torch
@@ -55,15 +55,24 @@ def _call(name: str, device: torch.device, *args) -> None:
         _lib.check(name, status)
 
 
-def _bytes(name: str, *args) -> int:
-    return _function(name)(*args)
+@functools.lru_cache(maxsize=4096)
+def _bytes(name: str, *sizes) -> int:
+    """Workspace bytes: a function of the sizes and types alone."""
+    return _function(name)(*sizes)
+
+
+def _new(shape, dtype, device):
+    """torch.empty (for matrices by the entry point that takes half the time)."""
+    if len(shape) == 2:
+        return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _workspace(n: int, device: torch.device):
     """(tensor, pointer, bytes) of a workspace of n bytes."""
     if n == 0:
         return None, None, 0
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws = torch.empty_strided((n,), (1,), dtype=torch.uint8, device=device)
     return ws, ws.data_ptr(), n
 
 
@@ -95,10 +104,11 @@ def _check(t, what: str, dtypes, shape=None, device=None):
 
 def _check_rows(t, what: str, dtypes):
     _check(t, what, dtypes)
-    if t.dim() < 1 or t.shape[-1] < 1:
+    shape = t.shape
+    if not shape or shape[-1] < 1:
         raise ValueError("%s must be [..., features] with at least one feature" % what)
-    width = t.shape[-1]
-    return t.numel() // width, width
+    width = shape[-1]
+    return (shape[0] if len(shape) == 2 else t.numel() // width), width
 
 
 def _aligned(t, n: int = 16):
@@ -121,10 +131,10 @@ def _check_scales(x, weights, x_scale, scales, M: int):
 def _out(out, shape, dtype, device):
     """`out`, or a new tensor where there is none or it does not start at 16 bytes."""
     if out is not None:
-        _check(out, "out", (dtype,), torch.Size(shape), device)
+        _check(out, "out", (dtype,), shape, device)
         if out.data_ptr() % 16 == 0:
             return out
-    return torch.empty(shape, dtype=dtype, device=device)
+    return _new(shape, dtype, device)
 
 
 def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
@@ -144,16 +154,17 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     if weight.dim() != 2 or weight.shape[1] != K or weight.shape[0] < 1:
         raise ValueError("weight must be [N, %d], got %s" % (K, list(weight.shape)))
     N = weight.shape[0]
-    _check_scales(x, (weight,), x_scale, (weight_scale,), M)
+    if x_scale is not None or weight_scale is not None or x.dtype == _E4M3:
+        _check_scales(x, (weight,), x_scale, (weight_scale,), M)
     if out_dtype is None:
         out_dtype = torch.bfloat16 if x.dtype == _E4M3 else x.dtype
     if out_dtype not in _DTYPES:
         raise ValueError("out_dtype must be float32, float16 or bfloat16")
-    shape = (*x.shape[:-1], N)
+    shape = (M, N) if x.dim() == 2 else (*x.shape[:-1], N)
     if bias is not None:
         _check(bias, "bias", _FLOAT, (N,), dev)
     if residual is not None:
-        _check(residual, "residual", (out_dtype,), torch.Size(shape), dev)
+        _check(residual, "residual", (out_dtype,), shape, dev)
     y = _out(out, shape, out_dtype, dev)
     x, weight = _aligned(x), _aligned(weight)
     if residual is not None:
@@ -238,12 +249,13 @@ def gated_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activat
     act = _act(activation)
     M, D, F = _check_gated(x, w_gate, w_up, _OPERAND)
     dev = x.device
-    _check_scales(x, (w_gate, w_up), x_scale, (gate_scale, up_scale), M)
+    if x_scale is not None or gate_scale is not None or up_scale is not None or x.dtype == _E4M3:
+        _check_scales(x, (w_gate, w_up), x_scale, (gate_scale, up_scale), M)
     if out_dtype is None:
         out_dtype = torch.bfloat16 if x.dtype == _E4M3 else x.dtype
     if out_dtype not in _DTYPES:
         raise ValueError("out_dtype must be float32, float16 or bfloat16")
-    h = _out(out, (*x.shape[:-1], F), out_dtype, dev)
+    h = _out(out, (M, F) if x.dim() == 2 else (*x.shape[:-1], F), out_dtype, dev)
     x, w_gate, w_up = _aligned(x), _aligned(w_gate), _aligned(w_up)
     t, to = _TYPE[x.dtype], _TYPE[out_dtype]
     ws, wp, wn = _workspace(_bytes("pdr_gated_workspace_bytes", M, D, F, t, to), dev)
@@ -294,7 +306,7 @@ def gated(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activation:
 
 def _check_norm(x, weight):
     M, D = _check_rows(x, "x", _FLOAT)
-    _check(weight, "weight", tuple({x.dtype, torch.float32}), (D,), x.device)
+    _check(weight, "weight", (x.dtype, torch.float32), (D,), x.device)
     return M, D
 
 
@@ -313,13 +325,13 @@ def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
         out_dtype = x.dtype
     if out_dtype not in (x.dtype, _E4M3):
         raise ValueError("out_dtype must be x's type or float8_e4m3fn")
-    y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+    y = _new(x.shape, out_dtype, dev)
     s = x if residual is None else torch.empty_like(x)
     scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if out_dtype == _E4M3 else None
     rows = _aligned(x)
     residual = None if residual is None else _aligned(residual)
     _call("pdr_rms_norm_fwd", dev, rows.data_ptr(), _ptr(residual), _TYPE[x.dtype], weight.data_ptr(),
-          _TYPE[weight.dtype], ctypes.c_float(eps), M, D, None if residual is None else s.data_ptr(),
+          _TYPE[weight.dtype], eps, M, D, None if residual is None else s.data_ptr(),
           y.data_ptr(), _TYPE[out_dtype], _ptr(scale))
     return y, s, scale
 
@@ -339,7 +351,7 @@ def rms_norm_bwd(grad: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, grad
     grad, s, grad_s = _aligned(grad), _aligned(s), None if grad_s is None else _aligned(grad_s)
     ws, wp, wn = _workspace(_bytes("pdr_rms_norm_bwd_workspace_bytes", M, D), dev) if need[1] else (None, None, 0)
     _call("pdr_rms_norm_bwd", dev, grad.data_ptr(), s.data_ptr(), _TYPE[s.dtype], weight.data_ptr(),
-          _TYPE[weight.dtype], _ptr(grad_s), ctypes.c_float(eps), M, D, _ptr(dx), _ptr(dw), wp, wn)
+          _TYPE[weight.dtype], _ptr(grad_s), eps, M, D, _ptr(dx), _ptr(dw), wp, wn)
     return dx, dw
 
 
