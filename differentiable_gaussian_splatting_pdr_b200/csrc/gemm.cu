@@ -739,8 +739,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     ready = bar_try(empty + 8 * stage, phase ^ 1);  // asked early: the answer takes a while
                     load_a(p, tile, kb, at, bar);
-                    if (two) load_a(p, tile, kb + 1, at + kABytes, bar);
                     if (!p.stationary) load_b(p, tile, kb, rank, at + kABytes, bar);
+                    if (two) {
+                        load_a(p, tile, kb + 1, at + block_bytes, bar);
+                        if (!p.stationary) load_b(p, tile, kb + 1, rank, at + block_bytes + kABytes, bar);
+                    }
                 }
             }
             if (!ok && rank == 0) {
@@ -817,7 +820,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     };
                     block(at, bt);
-                    if (p.per_stage == 2 && kb + 1 < nk) block(at + kABytes, bt + p.b_bytes);
+                    if (p.per_stage == 2 && kb + 1 < nk)
+                        block(at + block_bytes, bt + (p.stationary ? p.b_bytes : block_bytes));
                     mma_commit(done);
                 }
                 if (!ok) break;
@@ -1278,6 +1282,9 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     // the memory's rate.
     const size_t left = room - (p.stationary ? all_b : 0);
     p.per_stage = p.stationary && p.kb > 1 && left >= 6 * kABytes ? 2 : 1;
+#ifdef X_PS
+    if (!p.stationary && p.kb > 1 && left >= X_PS * (kABytes + p.b_bytes)) p.per_stage = 2;
+#endif
     const size_t stage = p.per_stage * (kABytes + (p.stationary ? 0 : p.b_bytes));
     p.stages = (int)(left / stage);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
