@@ -635,3 +635,131 @@ def test_backward_with_unused_outputs_and_frozen_weights():
     h = F.gated(x, w, w)
     (gx,) = torch.autograd.grad(h.float().sum(), [x])
     assert gx.shape == x.shape
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 8, 65536), (2, 65536, 5), (130, 1000, 4100), (100001, 24, 9), (70000, 33, 14)])
+def test_extreme_sizes(M, K, N):
+    """The widest operands, long sums of few columns, many rows: forward and all gradients."""
+    rng = np.random.default_rng(M + K)
+    x, w, b, r = rand(rng, (M, K), BF16), rand(rng, (N, K), BF16, K ** -0.5), rand(rng, (N,), F32), rand(rng, (M, N), F32)
+    X, W, B, R = f64(x), f64(w), f64(b), f64(r)
+    want = O.linear(X, W, B, R)
+    close(F.linear_fwd(x, w, b, r, out_dtype=F32), want, z_error(X, W, B) + STEP * (np.abs(want) + np.abs(R)), F32, "y")
+    check_linear_bwd(M, K, N, BF16, F32, "none")
+
+
+def test_norm_rows_behind_the_last_stay_as_they_were():
+    """Rows of every residue of 16 bytes: what lies behind the outputs is not touched."""
+    from differentiable_gaussian_splatting_pdr_b200 import _lib
+    lib, stream = _lib.load(), torch.cuda.current_stream().cuda_stream
+    rng = np.random.default_rng(30)
+    for D in list(range(1, 18)) + [77, 100, 333, 4099, 8191]:
+        for M in (1, 5, 33, 100):
+            for dt, code in ((F32, 0), (BF16, 2)):
+                x, g, w = rand(rng, (M, D), dt), rand(rng, (M, D), dt), rand(rng, (D,), dt)
+                n = M * D
+                bufs = {k: torch.full((n + 512,), 7.0, device="cuda", dtype=dt) for k in ("s", "y", "dx")}
+                q, sc = torch.full((n + 512,), 7, device="cuda", dtype=torch.uint8), torch.full((M + 64,), 7.0, device="cuda")
+                dw = torch.full((D + 64,), 7.0, device="cuda", dtype=dt)
+                ws = torch.empty(lib.pdr_rms_norm_bwd_workspace_bytes(M, D), device="cuda", dtype=torch.uint8)
+                a = {k: v.data_ptr() for k, v in bufs.items()}
+                assert lib.pdr_rms_norm_fwd(x.data_ptr(), x.data_ptr(), code, w.data_ptr(), code, 1e-6, M, D, a["s"], a["y"], code, None, stream) == 0
+                assert lib.pdr_quantize_rows(x.data_ptr(), code, M, D, q.data_ptr(), sc.data_ptr(), stream) == 0
+                assert lib.pdr_rms_norm_bwd(g.data_ptr(), x.data_ptr(), code, w.data_ptr(), code, None, 1e-6, M, D, a["dx"], dw.data_ptr(), ws.data_ptr(), ws.numel(), stream) == 0
+                for t in bufs.values():
+                    assert (t[n:] == 7).all() and torch.isfinite(t[:n]).all()
+                assert (q[n:] == 7).all() and (sc[M:] == 7).all() and (dw[D:] == 7).all()
+                assert torch.equal(bufs["s"][:n].view(M, D), x + x)
+
+
+def test_calls_from_several_threads():
+    import threading
+    rng = np.random.default_rng(31)
+    x, w, wu, g = rand(rng, (900, 72), BF16), rand(rng, (64, 72), BF16), rand(rng, (64, 72), BF16), rand(rng, (900, 64), BF16)
+    want = (F.linear_fwd(x, w, activation="silu"), F.gated_fwd(x, w, wu), *F.gated_bwd(g, x, w, wu))
+    torch.cuda.synchronize()
+    got, errors = [None] * 6, []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(10):
+                    out = (F.linear_fwd(x, w, activation="silu"), F.gated_fwd(x, w, wu), *F.gated_bwd(g, x, w, wu))
+                torch.cuda.current_stream().synchronize()
+                got[i] = out
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for out in got:
+        for a, e in zip(out, want):
+            assert torch.equal(a, e)
+
+
+def test_adapter_captured_with_its_renderer():
+    """A training step (forward, loss, gradients) captured and replayed on new features gives the eager step's bits."""
+    from differentiable_gaussian_splatting_pdr_b200 import l1_ssim, render
+    rng = np.random.default_rng(32)
+    B, N, C, H, W, D = 1, 128, 1, 32, 32, 64
+    w = _weights(rng, D, 96, 5 + C, BF16)
+    f = rand(rng, (B, N, D), BF16)
+    base = torch.rand(B, N, 5 + C, device="cuda") * 30
+    base[..., 2:5] = 0.3
+    target = torch.rand(B, C, H, W, device="cuda")
+    leaves = [getattr(w, n).requires_grad_(True) for n in NAMES]
+
+    def step():
+        loss = l1_ssim(render(F.adapter(f, w, base), H, W, 7), target)
+        return (loss.detach(), *torch.autograd.grad(loss, leaves))
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in range(2):
+        f.copy_(rand(np.random.default_rng(100 + seed), (B, N, D), BF16))
+        want = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, e in zip(out, want):
+            assert torch.equal(a, e)
+
+
+def test_given_workspaces_hold_nothing_between_calls():
+    """One workspace full of NaN bytes serves calls of any size: nothing is read from it that the call did not write."""
+    from differentiable_gaussian_splatting_pdr_b200 import _lib
+    lib, stream = _lib.load(), torch.cuda.current_stream().cuda_stream
+    rng = np.random.default_rng(33)
+    ws = torch.full((64 << 20,), 255, device="cuda", dtype=torch.uint8)
+    for M, K, N, act in [(300, 77, 45, 3), (64, 130, 260, 2), (1000, 40, 6, 0), (129, 64, 41, 1)]:
+        x, w, b, g = rand(rng, (M, K), BF16), rand(rng, (N, K), BF16), rand(rng, (N,), F32), rand(rng, (M, N), BF16)
+        kind = ACTS[act]
+        want_y, want = F.linear_fwd(x, w, b, g, kind), F.linear_bwd(g, x, w, b, kind)
+        y = torch.empty(M, N, device="cuda", dtype=BF16)
+        d = [torch.empty_like(t) for t in (x, w, b)]
+        for _ in range(2):
+            ws.fill_(255)
+            assert lib.pdr_linear_fwd(x.data_ptr(), w.data_ptr(), 2, None, None, b.data_ptr(), 0, g.data_ptr(), act, M, N, K,
+                                      y.data_ptr(), 2, ws.data_ptr(), ws.numel(), stream) == 0
+            assert torch.equal(y, want_y)
+            ws.fill_(255)
+            assert lib.pdr_linear_bwd(g.data_ptr(), 2, x.data_ptr(), w.data_ptr(), 2, b.data_ptr(), 0, act, M, N, K,
+                                      *(t.data_ptr() for t in d), ws.data_ptr(), ws.numel(), stream) == 0
+            for a, e in zip(d, want):
+                assert torch.equal(a, e)
+        wu = rand(rng, (N, K), BF16)
+        want = F.gated_bwd(g, x, w, wu)
+        d = [torch.empty_like(t) for t in (x, w, wu)]
+        ws.fill_(255)
+        assert lib.pdr_gated_bwd(g.data_ptr(), x.data_ptr(), w.data_ptr(), wu.data_ptr(), 2, 2, M, K, N,
+                                 *(t.data_ptr() for t in d), ws.data_ptr(), ws.numel(), stream) == 0
+        for a, e in zip(d, want):
+            assert torch.equal(a, e)
