@@ -3,9 +3,9 @@
 // Pairs of blocks (a cluster of two SMs) walk over 256 x BN tiles of the
 // result, one persistent pair per two SMs.  Each block holds 128 rows of A, half
 // of the BN rows of B and its 128 rows of the accumulator; tcgen05.mma with
-// cta_group::2 multiplies over both blocks' shared memory.  (Single blocks with
-// 128 x 256 tiles were bound by the operands' way from L2: 7.7 TB/s at any
-// width; a pair reads a third less.)  A block's warps have fixed parts:
+// cta_group::2 multiplies over both blocks' shared memory, which reads a third
+// less from L2 than single blocks with 128 x 256 tiles do.  A block's warps have
+// fixed parts:
 //   warp 0   copies its A rows and B half to shared memory with TMA (128-byte
 //            swizzle, 64 16-bit or 128 8-bit k per stage, as many stages as
 //            fit).  Where all k of a tile's B half leave room for three
@@ -56,7 +56,7 @@ struct Divisor {
 };
 
 struct __align__(64) GemmParams {
-    CUtensorMap a[2], b[2], o[2];     // o: 16-bit results that TMA can store
+    CUtensorMap a[2], b[2], o[2];     // operands, results
     int mode, a_mn, b_mn;
     int M, N, nz, splits, tiles;
     Divisor nm, nn;                   // tiles of 256 rows, of bcols columns
@@ -104,7 +104,7 @@ __device__ __forceinline__ unsigned at_rank(unsigned addr, unsigned rank) {
 // Arrives at a barrier of the pair (its cluster address).  Relaxed: what it
 // orders are reads of tensor memory, which tcgen05.wait::ld and the fence before
 // it have ended; a release at this scope would also wait for the warp's stores
-// to global memory (118 against 70 us for 65536 rows of 256 to 1024 gated).
+// to global memory (1.8 of an SM's epilogue warps stood there at any time).
 __device__ __forceinline__ void bar_arrive_at(unsigned addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
@@ -245,8 +245,8 @@ __device__ __forceinline__ void pack_row(int dtype, const float *v, unsigned (&w
 // Results leave through the warp's buffer and TMA stores of 32 rows, which drop
 // what is behind the last row and column: direct stores of 32 bytes a lane take 32
 // turns of the load-store unit each, this way four.  A block in the buffer has
-// rows of 64 bytes (32 columns of 16 bits or 16 of 32) or of 32 bytes (16 of 16
-// bits), their 16-byte pieces swizzled as the map says.
+// rows of 64 bytes (32 columns of 16 bits or 16 of 32), their 16-byte pieces
+// swizzled as the map says.
 __device__ __forceinline__ void stage_half(char *buffer, int half, const unsigned (&w)[kChunk / 2]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -260,13 +260,6 @@ __device__ __forceinline__ void stage_floats(char *buffer, const float *v) {
     for (int j = 0; j < 4; ++j)
         *reinterpret_cast<float4 *>(buffer + lane * 64 + (j ^ ((lane >> 1) & 3)) * 16) =
             make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-}
-__device__ __forceinline__ void stage_narrow(char *buffer, const unsigned (&w)[kChunk / 2]) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-        *reinterpret_cast<uint4 *>(buffer + lane * 32 + (j ^ ((lane >> 2) & 1)) * 16) =
-            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 // A warp's buffers in turn: the next one, when the stores before have read it.
 struct Staging {
@@ -282,6 +275,11 @@ struct Staging {
         __syncwarp();
         return base + turn;
     }
+    __device__ __forceinline__ char *all() {
+        if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+        return base;
+    }
 };
 __device__ __forceinline__ void tma_store(const CUtensorMap *map, const char *buffer, int x, int y, int z) {
     asm volatile(
@@ -296,7 +294,7 @@ __device__ __forceinline__ void store_buffer(const CUtensorMap *map, const CUten
     __syncwarp();
     if (elect_one()) {
         tma_store(map, buffer, x, y, z);
-        if (map2) tma_store(map2, buffer + kBufferBytes / 2, x, y, z);
+        if (map2) tma_store(map2, buffer + kBufferBytes, x, y, z);
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
 }
@@ -516,13 +514,14 @@ __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t
         unsigned w[kChunk / 2];
         const int half = C == 32 ? 0 : (c - c0) / kChunk & 1;
         const int slice = t.split * p.nz + t.z;
-        if constexpr (EPI == kEpiGatedBwd) {
-            stage = staging.next();
+        if constexpr (EPI == kEpiGatedBwd) {  // dg in the first buffer, du in the second
+            if (half == 0) stage = staging.all();
             pack_row(p.out_dtype, v, w);
-            stage_narrow(stage, w);
+            stage_half(stage, half, w);
             pack_row(p.out_dtype, u, w);
-            stage_narrow(stage + kBufferBytes / 2, w);
-            store_buffer(&p.o[0], &p.o[1], stage, n0 + c, row0, 0);
+            stage_half(stage + kBufferBytes, half, w);
+            if (half == 1 || c + C >= c1)
+                store_buffer(&p.o[0], &p.o[1], stage, n0 + c - half * kChunk, row0, 0);
         } else if (EPI != kEpiSlope && p.out_dtype == PDR_F32) {
 #pragma unroll
             for (int i = 0; i < C; i += kChunk) {
@@ -1095,18 +1094,18 @@ bool make_map(CUtensorMap *m, const Operand &o, int bytes, int box_cols, int box
 }
 
 // The map of a result (`slices` of rows x cols, one behind the other) for the
-// stores of 32 rows by 64 bytes, or (narrow) by 32.
+// stores of 32 rows by 64 bytes.
 bool make_store_map(CUtensorMap *m, void *to, int bytes, long long rows, long long cols,
-                    long long ld, int slices, bool narrow) {
+                    long long ld, int slices) {
     const EncodeTiled f = encode_tiled();
     if (!f) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)slices};
     const cuuint64_t strides[2] = {(cuuint64_t)ld * bytes, (cuuint64_t)ld * bytes * rows};
-    const cuuint32_t box[3] = {(cuuint32_t)((narrow ? 32 : 64) / bytes), 32, 1}, unit[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)(64 / bytes), 32, 1}, unit[3] = {1, 1, 1};
     return f(m, bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, to,
              dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             narrow ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Shared-memory descriptor of an operand tile, without its address: 128-byte
@@ -1217,7 +1216,7 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     p.nm = divisor(ceil_div(g.M, 2 * kBM));
     p.nn = divisor(ceil_div(g.N, p.bcols));
     const long long tiles = (long long)p.nm.d * p.nn.d * p.nz * p.splits;
-    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+    if (tiles > 1 << 30) return cudaErrorInvalidValue;
     p.tiles = (int)tiles;
     p.b_bytes = g.b_mn ? ceil_div(p.bn / 2, 64) * 8192 : p.bn / 2 * kRowBytes;
     p.nacc = p.bn >= 256 ? 2 : 4;
@@ -1254,8 +1253,7 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
         return cudaErrorInvalidValue;
     const int slices = g.out_split || g.out_z ? p.splits * p.nz : 1;
     for (int i = 0; !p.narrow && i < (g.out2 ? 2 : 1); ++i)
-        if (!make_store_map(&p.o[i], i ? g.out2 : g.out, ob, g.M, g.N, g.ldo, slices,
-                            g.epi == kEpiGatedBwd))
+        if (!make_store_map(&p.o[i], i ? g.out2 : g.out, ob, g.M, g.N, g.ldo, slices))
             return cudaErrorInvalidValue;
     p.bias = g.bias;
     p.bias_dtype = g.bias_dtype;
@@ -1269,13 +1267,14 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     const size_t all_b = (size_t)p.kb * p.b_bytes;
     const int pairs = p.tiles < kSMs / 2 ? p.tiles : kSMs / 2;
     const size_t fixed = 1024 + 512 + kEpiWarps * 3 * kMaxCols * 4, buffers = kEpiWarps * kBufferBytes;
-    size_t room = kSmemBytes - fixed - buffers;
+    const bool both = g.epi == kEpiGatedBwd;  // dg and du have a buffer each
+    size_t room = kSmemBytes - fixed - (both ? 2 : 1) * buffers;
     // B stays where it leaves room for three stages of A and a pair has several
     // tiles to use it for.
     p.stationary = g.splits == 1 && all_b + 3 * kABytes <= room && p.tiles >= 2 * pairs;
     // A second buffer for each epilogue warp, where that takes no stage that is needed.
-    p.nbuf = p.stationary && all_b + 4 * kABytes + buffers <= room ? 2 : 1;
-    room -= (p.nbuf - 1) * buffers;
+    p.nbuf = both || (p.stationary && all_b + 4 * kABytes + buffers <= room) ? 2 : 1;
+    if (!both) room -= (p.nbuf - 1) * buffers;
     // A stage of two k blocks, where there are as many and room for three stages,
     // halves the waits and counts beside the copies and products: one thread takes some 700
     // clocks for those of a stage beside a busy epilogue, as long as 16 KB take at

@@ -33,10 +33,11 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
-// 1 / (1 + e^-v).  e^-v may overflow to infinity: 0.  (Two elements can share a
-// reciprocal, 1 / a = b / (a b), which takes the special-function unit from 2 to
-// 1.5 operations an element; the three more instructions, and two that keep a NaN
-// from reaching the neighbour, cost more: PAIRED.)
+// 1 / (1 + e^-v).  e^-v may overflow to infinity: 0.  Two operations of the
+// special-function unit an element, 2048 clocks for a 128 x 128 gated tile.  Two
+// elements that share a reciprocal (1 / a = b / (a b)) take 1.5 and three more
+// instructions: 61.4 against 60.9 us for 65536 rows of 256 to 1024.  Pairs of
+// elements in one f32x2 instruction took 65.4.
 __device__ __forceinline__ float logistic(float v) { return rcp(1.0f + ex2(-kLog2e * v)); }
 
 // Phi(z) = erfc(-z / sqrt 2) / 2, and e^{-z^2/2}.  Abramowitz and Stegun, Handbook
