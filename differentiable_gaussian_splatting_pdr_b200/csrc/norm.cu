@@ -21,7 +21,10 @@ namespace pdr {
 namespace {
 
 constexpr int kPer = 16;              // row elements per thread
-constexpr int kFwdPerSm = 3, kBwdPerSm = 2;  // blocks of 256 threads per SM
+// Blocks of 256 threads per SM (a thread's share of an fp32 row takes twice the
+// registers): 16384 x 333 in fp32 took 15.0 us with two against 18.7 with three, 65536 x 512 in
+// bf16 to 8 bits 41.0 with three against 44.9 with four.
+constexpr int kFwdPerSm = 3, kFwdPerSm32 = 2, kBwdPerSm = 2;
 constexpr float kE4M3Max = 448.0f;    // largest finite e4m3 value
 constexpr float kMinScale = 1.17549435082228751e-38f;  // 2^-126
 
@@ -31,7 +34,7 @@ struct NormArgs {
     void *s, *y;            // x + r (or null), result
     float *scale;           // e4m3 result: scale of each row
     int dtype, w_dtype, y_dtype;
-    float eps;
+    float eps, inv_d;       // inv_d: 1 / D
     long long M;
     int D, T;
 };
@@ -41,7 +44,7 @@ struct NormBwdArgs {
     void *dx;
     float *dw;              // [blocks][D] partial sums
     int dtype, w_dtype;
-    float eps;
+    float eps, inv_d;       // inv_d: 1 / D
     long long M;
     int D, T;
 };
@@ -226,32 +229,38 @@ __device__ __forceinline__ void store_row(void *p, long long row, bool on, const
     }
 }
 
-// Sum (or maximum) over the T threads of a row, for all of them; the whole
-// block calls it.  `red`: one float per warp.
+// Two sums, or a sum and a maximum, over the T threads of a row, for all of them;
+// the whole block calls it.  `red`: one pair per warp.
 template <bool MAX>
-__device__ __forceinline__ float row_reduce(float v, int T, float *red) {
+__device__ __forceinline__ float2 row_reduce(float a, float b, int T, float2 *red) {
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1)
         if (d < T) {
-            const float o = __shfl_xor_sync(0xffffffffu, v, d);
-            v = MAX ? max_nan(v, o) : v + o;
+            const float oa = __shfl_xor_sync(0xffffffffu, a, d), ob = __shfl_xor_sync(0xffffffffu, b, d);
+            a += oa;
+            b = MAX ? max_nan(b, ob) : b + ob;
         }
     if (T > 32) {
         const int warp = threadIdx.x >> 5, first = (threadIdx.x & ~(T - 1)) >> 5;
         __syncthreads();
-        if ((threadIdx.x & 31) == 0) red[warp] = v;
+        if ((threadIdx.x & 31) == 0) red[warp] = make_float2(a, b);
         __syncthreads();
-        v = red[first];
-        for (int i = 1; i < T >> 5; ++i) v = MAX ? max_nan(v, red[first + i]) : v + red[first + i];
+        a = red[first].x;
+        b = red[first].y;
+        for (int i = 1; i < T >> 5; ++i) {
+            a += red[first + i].x;
+            b = MAX ? max_nan(b, red[first + i].y) : b + red[first + i].y;
+        }
     }
-    return v;
+    return make_float2(a, b);
 }
 
 // Blocks have 256 threads for rows of at most 4096 elements, 512 or 1024 for wider
-// ones.  The next row is fetched ahead, but for blocks of 1024 threads, which have
-// too few registers.
-template <int THREADS>
-constexpr bool kAhead = THREADS < 1024;
+// ones.  The next row is fetched ahead where registers allow it: not for blocks of
+// 1024 threads, nor (`room`) for the two fp32 rows of the backward (60000 x 512:
+// 63 us without, 89 with spilled registers).
+template <int THREADS, bool room>
+constexpr bool kAhead = THREADS < 1024 && room;
 
 template <int E, bool SHIFT>
 __device__ __forceinline__ Row<E, SHIFT> make_row(long long row, long long M, int D, int T) {
@@ -265,8 +274,9 @@ __device__ __forceinline__ Row<E, SHIFT> make_row(long long row, long long M, in
 }
 
 template <int E, bool SHIFT, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : kFwdPerSm) k_rms_norm(const NormArgs a) {
-    __shared__ float red[32];
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : E == 4 ? kFwdPerSm32 : kFwdPerSm)
+    k_rms_norm(const NormArgs a) {
+    __shared__ float2 red[32];
     grid_dep_wait();
     const int T = a.T, per_block = blockDim.x / T;
     const long long step = (long long)gridDim.x * per_block;
@@ -275,13 +285,13 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : kFwdPerSm) k_rms_
     float w[kPer];
     if (a.w) load_weight(a.w, a.w_dtype, q, w);
     Raw<E> x, r, next_x, next_r;
-    if constexpr (kAhead<THREADS>) {  // (nothing of rows behind the last)
+    if constexpr (kAhead<THREADS, true>) {  // (nothing of rows behind the last)
         fetch(x, a.x, row, row < a.M, q);
         if (a.r) fetch(r, a.r, row, row < a.M, q);
     }
     for (long long base = (long long)blockIdx.x * per_block; base < a.M; base += step, row += step) {
         const bool on = row < a.M;
-        if constexpr (kAhead<THREADS>) {
+        if constexpr (kAhead<THREADS, true>) {
             fetch(next_x, a.x, row + step, row + step < a.M, q);
             if (a.r) fetch(next_r, a.r, row + step, row + step < a.M, q);
         } else {
@@ -298,27 +308,30 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : kFwdPerSm) k_rms_
             if (a.s) store_row(a.s, row, on, q, a.dtype, v);
         }
         keep_row(v, q);
+        // y = v w rstd: the sum of v^2 and the largest |v w| in one reduction.
+        float ss = 0.0f, m = 0.0f;
         if (a.w) {
-            float ss = 0.0f;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) ss = fmaf(v[j], v[j], ss);
-            ss = row_reduce<false>(ss, T, red);
-            const float rstd = rsqrtf(ss / (float)a.D + a.eps);
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) v[j] *= rstd * w[j];
+            for (int j = 0; j < kPer; ++j) {
+                ss = fmaf(v[j], v[j], ss);
+                v[j] *= w[j];
+            }
         }
         if (a.scale) {
-            float m = 0.0f;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) m = max_nan(m, fabsf(v[j]));
-            m = row_reduce<true>(m, T, red);
-            const float scale = max_nan(m / kE4M3Max, kMinScale), inv = 1.0f / scale;
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) v[j] *= inv;
+        }
+        const float2 both = row_reduce<true>(ss, m, T, red);
+        float k = a.w ? rsqrtf(fmaf(both.x, a.inv_d, a.eps)) : 1.0f;
+        if (a.scale) {
+            const float scale = max_nan(both.y * k * (1.0f / kE4M3Max), kMinScale);
+            k *= rcp(scale);
             if (q.t == 0 && on) a.scale[row] = scale;
         }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) v[j] *= k;
         store_row(a.y, row, on, q, a.y_dtype, v);
-        if constexpr (kAhead<THREADS>) {
+        if constexpr (kAhead<THREADS, true>) {
             x = next_x;
             r = next_r;
         }
@@ -329,7 +342,7 @@ template <int E, bool SHIFT, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : kBwdPerSm)
     k_rms_norm_bwd(const NormBwdArgs a) {
     extern __shared__ float part[];  // [rows of a block][D] when there are several
-    __shared__ float red[32];
+    __shared__ float2 red[32];
     grid_dep_wait();
     const int T = a.T, per_block = blockDim.x / T;
     const long long step = (long long)gridDim.x * per_block;
@@ -340,13 +353,13 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : kBwdPerSm)
 #pragma unroll
     for (int j = 0; j < kPer; ++j) dw[j] = 0.0f;
     Raw<E> s, dy, ds, next_s, next_dy;
-    if constexpr (kAhead<THREADS>) {
+    if constexpr (kAhead<THREADS, E == 8>) {
         fetch(s, a.s, row, row < a.M, q);
         fetch(dy, a.dy, row, row < a.M, q);
     }
     for (long long base = (long long)blockIdx.x * per_block; base < a.M; base += step, row += step) {
         const bool on = row < a.M;
-        if constexpr (kAhead<THREADS>) {
+        if constexpr (kAhead<THREADS, E == 8>) {
             if (a.ds) fetch(ds, a.ds, row, on, q);  // needed last
             fetch(next_s, a.s, row + step, row + step < a.M, q);
             fetch(next_dy, a.dy, row + step, row + step < a.M, q);
@@ -359,30 +372,29 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : kBwdPerSm)
         unpack<E>(dy, a.dtype, g);
         keep_row(v, q);
         keep_row(g, q);
-        float ss = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) ss = fmaf(v[j], v[j], ss);
-        ss = row_reduce<false>(ss, T, red);
-        const float rstd = rsqrtf(ss / (float)a.D + a.eps);
-        float dot = 0.0f;
+        // With p = dy w: sum v^2 and sum p v in one reduction; n = v rstd.
+        float ss = 0.0f, pv = 0.0f;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            v[j] *= rstd;
-            dw[j] = fmaf(g[j], v[j], dw[j]);
-            g[j] *= w[j];
-            dot = fmaf(g[j], v[j], dot);
+            ss = fmaf(v[j], v[j], ss);
+            pv = fmaf(g[j] * w[j], v[j], pv);
         }
-        dot = row_reduce<false>(dot, T, red) / (float)a.D;
+        const float2 sums = row_reduce<false>(ss, pv, T, red);
+        const float rstd = rsqrtf(fmaf(sums.x, a.inv_d, a.eps));
+        const float dot = rstd * rstd * sums.y * a.inv_d;  // mean(p n) / |v|_rms
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) g[j] = rstd * fmaf(-v[j], dot, g[j]);
+        for (int j = 0; j < kPer; ++j) {
+            dw[j] = fmaf(g[j] * rstd, v[j], dw[j]);
+            g[j] = rstd * fmaf(-v[j], dot, g[j] * w[j]);
+        }
         if (a.ds) {
-            if constexpr (!kAhead<THREADS>) fetch(ds, a.ds, row, on, q);
+            if constexpr (!kAhead<THREADS, E == 8>) fetch(ds, a.ds, row, on, q);
             unpack<E>(ds, a.dtype, v);
 #pragma unroll
             for (int j = 0; j < kPer; ++j) g[j] += v[j];
         }
         if (a.dx) store_row(a.dx, row, on, q, a.dtype, g);
-        if constexpr (kAhead<THREADS>) {
+        if constexpr (kAhead<THREADS, E == 8>) {
             s = next_s;
             dy = next_dy;
         }
@@ -449,7 +461,7 @@ cudaError_t launch_norm(const NormShape &n, const Args &a, size_t smem, cudaStre
 }
 
 pdr_status run_fwd(NormArgs a, cudaStream_t s) {
-    const NormShape n = norm_shape(a.M, a.D, dtype_bytes(a.dtype), kFwdPerSm);
+    const NormShape n = norm_shape(a.M, a.D, dtype_bytes(a.dtype), a.dtype == PDR_F32 ? kFwdPerSm32 : kFwdPerSm);
     a.T = n.T;
     return launch_norm<false>(n, a, 0, s) == cudaSuccess ? PDR_OK : PDR_ERR_CUDA;
 }
@@ -478,7 +490,7 @@ pdr_status pdr_rms_norm_fwd(const void *x, const void *residual, int dtype, cons
         !aligned_to(weight, dtype_bytes(weight_dtype)) || !aligned_to(y_scale, 4))
         return PDR_ERR_INVALID_ARG;
     if (M == 0) return PDR_OK;
-    return run_fwd({x, residual, weight, sum, y, y_scale, dtype, weight_dtype, y_dtype, eps, M, D, 0},
+    return run_fwd({x, residual, weight, sum, y, y_scale, dtype, weight_dtype, y_dtype, eps, 1.0f / D, M, D, 0},
                    static_cast<cudaStream_t>(stream));
 }
 
@@ -489,7 +501,7 @@ pdr_status pdr_quantize_rows(const void *x, int dtype, int M, int D, void *y, fl
     if (M > 0 && (!x || !y || !y_scale)) return PDR_ERR_INVALID_ARG;
     if (!aligned_to(x, 16) || !aligned_to(y, 16) || !aligned_to(y_scale, 4)) return PDR_ERR_INVALID_ARG;
     if (M == 0) return PDR_OK;
-    return run_fwd({x, nullptr, nullptr, nullptr, y, y_scale, dtype, dtype, PDR_E4M3, 0.0f, M, D, 0},
+    return run_fwd({x, nullptr, nullptr, nullptr, y, y_scale, dtype, dtype, PDR_E4M3, 0.0f, 1.0f / D, M, D, 0},
                    static_cast<cudaStream_t>(stream));
 }
 
@@ -526,7 +538,7 @@ pdr_status pdr_rms_norm_bwd(const void *grad, const void *sum, int dtype, const 
     const NormShape n = norm_shape(M, D, dtype_bytes(dtype), kBwdPerSm);
     const NormBwdArgs a = {grad, sum, weight, grad_sum, grad_x,
                            grad_weight ? static_cast<float *>(workspace) : nullptr,
-                           dtype, weight_dtype, eps, M, D, n.T};
+                           dtype, weight_dtype, eps, 1.0f / D, M, D, n.T};
     // One row of dw for each row of a block: at most 256 x 16 floats.
     err = launch_norm<true>(n, a, n.threads > n.T ? (size_t)(n.threads / n.T) * D * 4 : 0, s);
     if (err == cudaSuccess && grad_weight)
