@@ -258,7 +258,7 @@ __device__ __forceinline__ float2 row_reduce(float a, float b, int T, float2 *re
 // Blocks have 256 threads for rows of at most 4096 elements, 512 or 1024 for wider
 // ones.  The next row is fetched ahead where registers allow it: not for blocks of
 // 1024 threads, nor (`room`) for the two fp32 rows of the backward (60000 x 512:
-// 63 us without, 89 with spilled registers).
+// 82 us without, 89 with spilled registers).
 template <int THREADS, bool room>
 constexpr bool kAhead = THREADS < 1024 && room;
 
