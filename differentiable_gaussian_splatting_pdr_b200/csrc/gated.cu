@@ -213,55 +213,47 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
         g.ldo = L.ldf;
         e = launch_gemm(g, s);
     }
-    if (e == cudaSuccess && grad_x) {
-        GemmArgs g;
-        g.mode = kTwoSources;
-        g.dtype = dtype;
-        g.a[0] = odg;
-        g.a[1] = odu;
-        g.b[0] = og;
-        g.b[1] = ou;
-        g.b_mn = true;
-        g.M = M;
-        g.N = D;
-        g.K[0] = g.K[1] = F;
-        g.out = L.pack_out ? ws + L.out : grad_x;
-        g.out_dtype = dtype;
-        g.ldo = L.ldo;
-        e = launch_gemm(g, s);
-        if (e == cudaSuccess && L.pack_out) e = launch_unpack(ws + L.out, M, D, L.ldo, 2, grad_x, s);
+    GemmArgs gx, gw;  // dx = dg Wg + du Wu; dWg = dg^T x and dWu = du^T x
+    gx.mode = kTwoSources;
+    gw.mode = kBatchA;
+    gx.dtype = gw.dtype = dtype;
+    gx.a[0] = gw.a[0] = odg;
+    gx.a[1] = gw.a[1] = odu;
+    gx.b[0] = og;
+    gx.b[1] = ou;
+    gw.b[0] = ox;
+    gx.b_mn = gw.a_mn = gw.b_mn = true;
+    gx.M = M;
+    gw.M = F;
+    gx.N = gw.N = D;
+    gx.K[0] = gx.K[1] = F;
+    gw.K[0] = M;
+    gx.out = L.pack_out ? ws + L.out : grad_x;
+    gx.out_dtype = dtype;
+    gx.ldo = L.ldo;
+    const bool partial = L.splits > 1 || D % 8;
+    const long long n = F * L.ldp;
+    float *part = reinterpret_cast<float *>(ws + L.part);
+    gw.splits = L.splits;
+    if (partial) {
+        gw.out = part;
+        gw.out_dtype = PDR_F32;
+        gw.ldo = L.ldp;
+        gw.out_z = n;
+        gw.out_split = 2 * n;
+    } else {
+        gw.out = grad_gate;
+        gw.out2 = grad_up;
+        gw.out_dtype = dtype;
+        gw.ldo = D;
     }
-    if (e == cudaSuccess && grad_gate) {
-        GemmArgs g;
-        g.mode = kBatchA;
-        g.dtype = dtype;
-        g.a[0] = odg;
-        g.a[1] = odu;
-        g.b[0] = ox;
-        g.a_mn = g.b_mn = true;
-        g.M = F;
-        g.N = D;
-        g.K[0] = M;
-        g.splits = L.splits;
-        g.ldo = D;
-        const long long n = F * L.ldp;
-        float *part = reinterpret_cast<float *>(ws + L.part);
-        const bool partial = L.splits > 1 || D % 8;
-        if (partial) {
-            g.out = part;
-            g.ldo = L.ldp;
-            g.out_dtype = PDR_F32;
-            g.out_z = n;
-            g.out_split = 2 * n;
-        } else {
-            g.out = grad_gate;
-            g.out2 = grad_up;
-            g.out_dtype = dtype;
-        }
-        e = launch_gemm(g, s);
-        if (e == cudaSuccess && partial)
-            e = launch_join(part, L.splits, F, D, L.ldp, grad_gate, grad_up, dtype, s);
-    }
+    if (e == cudaSuccess && grad_x && grad_gate)
+        e = launch_gemm2(gx, gw, s);
+    else if (e == cudaSuccess)
+        e = launch_gemm(grad_x ? gx : gw, s);
+    if (e == cudaSuccess && grad_x && L.pack_out) e = launch_unpack(ws + L.out, M, D, L.ldo, 2, grad_x, s);
+    if (e == cudaSuccess && grad_gate && partial)
+        e = launch_join(part, L.splits, F, D, L.ldp, grad_gate, grad_up, dtype, s);
     return done(e);
 }
 

@@ -82,6 +82,14 @@ struct __align__(64) GemmParams {
     float *colsum;
 };
 
+// One product, or two that run one behind the other in the same launch: tiles of the
+// same size, so that the pairs go from one to the other without a stop (no
+// stationary B).
+template <int NP>
+struct GemmLaunch {
+    GemmParams p[NP];
+};
+
 struct Barriers {
     unsigned long long full[kMaxStages], empty[kMaxStages], acc_full[kMaxAcc], acc_empty[kMaxAcc];
     unsigned long long b_full, b_empty, drain;
@@ -384,11 +392,13 @@ __device__ __forceinline__ KRange k_range(const GemmParams &p, const Tile &t) {
 struct Range {
     int first, end, step;
 };
-__device__ __forceinline__ Range my_tiles(const GemmParams &p) {
+// (`before`: tiles of the product in front, after which the turn goes on.)
+__device__ __forceinline__ Range my_tiles(const GemmParams &p, int before) {
     const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
     if (p.stationary)
         return {(int)((long long)p.tiles * pair / pairs), (int)((long long)p.tiles * (pair + 1) / pairs), 1};
-    return {pair, p.tiles, pairs};
+    const int first = pair - before % pairs;
+    return {first < 0 ? first + pairs : first, p.tiles, pairs};
 }
 
 __device__ __forceinline__ void load_a(const GemmParams &p, const Tile &t, int kb, unsigned A,
@@ -486,17 +496,33 @@ __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t
             unpack_row(p.in_dtype, raw, x);
             if (c + C < c1) fetch(c + C);
         }
+        const float4 *column = reinterpret_cast<const float4 *>(columns + c - c0);
         if (p.fp8) {
-            const float *s = columns + kMaxCols + c - c0;
 #pragma unroll
-            for (int i = 0; i < C; ++i) {
-                v[i] *= scale_m * s[i];
-                if constexpr (EPI == kEpiGated) u[i] *= scale_m * s[kMaxCols + i];
+            for (int i = 0; i < C; i += 4) {
+                const float4 f = column[(kMaxCols + i) / 4];
+                v[i] *= scale_m * f.x;
+                v[i + 1] *= scale_m * f.y;
+                v[i + 2] *= scale_m * f.z;
+                v[i + 3] *= scale_m * f.w;
+                if constexpr (EPI == kEpiGated) {
+                    const float4 h = column[(2 * kMaxCols + i) / 4];
+                    u[i] *= scale_m * h.x;
+                    u[i + 1] *= scale_m * h.y;
+                    u[i + 2] *= scale_m * h.z;
+                    u[i + 3] *= scale_m * h.w;
+                }
             }
         }
         if (!kTwo && p.bias) {
 #pragma unroll
-            for (int i = 0; i < C; ++i) v[i] += columns[c - c0 + i];
+            for (int i = 0; i < C; i += 4) {
+                const float4 f = column[i / 4];
+                v[i] += f.x;
+                v[i + 1] += f.y;
+                v[i + 2] += f.z;
+                v[i + 3] += f.w;
+            }
         }
         if constexpr (EPI == kEpiLinear) {
             apply_act<ACT>(v);
@@ -619,10 +645,11 @@ __device__ __forceinline__ bool epilogue_narrow(const GemmParams &p, const Tile 
     return true;
 }
 
-template <int EPI, int ACT, bool NARROW>
+template <int EPI, int ACT, bool NARROW, int NP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    k_gemm(const __grid_constant__ GemmParams p) {
+    k_gemm(const __grid_constant__ GemmLaunch<NP> launch) {
     extern __shared__ char raw[];
+    const GemmParams &p = launch.p[0];  // (both have the same tiles and shared memory)
     // Tiles first, at a 1024-byte boundary (the swizzle's period).
     char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     const int block_bytes = kABytes + (p.stationary ? 0 : p.b_bytes);  // of a k block
@@ -662,7 +689,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const unsigned tmem = bars->tmem;
-    const Range range = my_tiles(p);
     const unsigned full = smem_u32(bars->full), empty = smem_u32(bars->empty);
     const unsigned acc_full = smem_u32(bars->acc_full), acc_empty = smem_u32(bars->acc_empty);
     const unsigned b_full = smem_u32(&bars->b_full), b_empty = smem_u32(&bars->b_empty);
@@ -680,28 +706,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int cols = p.bcols / p.sharing, cfirst = group % p.sharing * cols;
         const int sets = kGroups / p.sharing, set = group / p.sharing;
         const unsigned release = at_rank(acc_empty, 0);
-        int acc = 0, it = 0, have_n = -1;
+        int acc = 0, it = 0;
         unsigned acc_phase = 0;
-        Tile tile = tile_of(p, range.first, rank);
-        for (int t = range.first; t < range.end; t += range.step, ++it) {
-            if ((it & (sets - 1)) == set) {
-                const unsigned d = tmem + ((unsigned)(32 * quarter) << 16) + acc * p.bn;
-                bool ok;
-                if constexpr (NARROW)
-                    ok = epilogue_narrow<ACT>(p, tile, d, acc_full + 8 * acc, acc_phase, quarter,
-                                              columns, have_n, reinterpret_cast<float *>(staging.base), abort,
-                                              release + 8 * acc);
-                else
-                    ok = epilogue_tile<EPI, ACT>(p, tile, d, acc_full + 8 * acc, acc_phase, cfirst,
-                                                 cfirst + cols, quarter, columns, have_n, staging,
-                                                 abort, release + 8 * acc);
-                if (!ok) break;
-            }
-            tile.m += 2;  // down the column, or looked up
-            if (!p.stationary || tile.m >= 2 * (int)p.nm.d) tile = tile_of(p, t + range.step, rank);
-            if (++acc == p.nacc) {
-                acc = 0;
-                acc_phase ^= 1;
+        bool ok = true;
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            const GemmParams &p = launch.p[q];
+            const Range range = my_tiles(p, q ? launch.p[0].tiles : 0);
+            int have_n = -1;
+            Tile tile = tile_of(p, range.first, rank);
+            for (int t = range.first; t < range.end && ok; t += range.step, ++it) {
+                if ((it & (sets - 1)) == set) {
+                    const unsigned d = tmem + ((unsigned)(32 * quarter) << 16) + acc * p.bn;
+                    if constexpr (NARROW)
+                        ok = epilogue_narrow<ACT>(p, tile, d, acc_full + 8 * acc, acc_phase, quarter,
+                                                  columns, have_n, reinterpret_cast<float *>(staging.base), abort,
+                                                  release + 8 * acc);
+                    else
+                        ok = epilogue_tile<EPI, ACT>(p, tile, d, acc_full + 8 * acc, acc_phase, cfirst,
+                                                     cfirst + cols, quarter, columns, have_n, staging,
+                                                     abort, release + 8 * acc);
+                    if (!ok) break;
+                }
+                tile.m += 2;  // down the column, or looked up
+                if (!p.stationary || tile.m >= 2 * (int)p.nm.d) tile = tile_of(p, t + range.step, rank);
+                if (++acc == p.nacc) {
+                    acc = 0;
+                    acc_phase ^= 1;
+                }
             }
         }
         if (!NARROW && elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -713,35 +745,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int stage = 0, issued = 0, column = -1;
             unsigned phase = 0, b_phase = 0;
             bool ok = true, ready = true;  // the first stages are empty
-            for (int t = range.first; t < range.end && ok; t += range.step) {
-                const Tile tile = tile_of(p, t, rank);
-                const KRange k = k_range(p, tile);
-                if (p.stationary && column != quotient(t, p.nm)) {
-                    column = quotient(t, p.nm);
-                    ok = bar_wait(b_empty, b_phase ^ 1, abort);
-                    if (!ok) break;
-                    b_phase ^= 1;
-                    if (rank == 0) bar_expect(b_full, 2 * p.kb * p.b_bytes);
-                    for (int kb = 0; kb < p.kb; ++kb)
-                        load_b(p, tile, kb, rank, held0 + kb * p.b_bytes, lead_b_full);
-                }
-                for (int kb = k.first; kb < k.end; kb += p.per_stage) {
-                    const bool two = p.per_stage == 2 && kb + 1 < k.end;
-                    if (!ready) ok = bar_wait(empty + 8 * stage, phase ^ 1, abort);
-                    if (!ok) break;
-                    const unsigned bar = lead_full + 8 * stage, at = stages0 + stage * stage_bytes;
-                    if (rank == 0) bar_expect(full + 8 * stage, two ? 4 * block_bytes : 2 * block_bytes);
-                    ++issued;
-                    if (++stage == p.stages) {
-                        stage = 0;
-                        phase ^= 1;
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                const GemmParams &p = launch.p[q];
+                const Range range = my_tiles(p, q ? launch.p[0].tiles : 0);
+                for (int t = range.first; t < range.end && ok; t += range.step) {
+                    const Tile tile = tile_of(p, t, rank);
+                    const KRange k = k_range(p, tile);
+                    if (p.stationary && column != quotient(t, p.nm)) {
+                        column = quotient(t, p.nm);
+                        ok = bar_wait(b_empty, b_phase ^ 1, abort);
+                        if (!ok) break;
+                        b_phase ^= 1;
+                        if (rank == 0) bar_expect(b_full, 2 * p.kb * p.b_bytes);
+                        for (int kb = 0; kb < p.kb; ++kb)
+                            load_b(p, tile, kb, rank, held0 + kb * p.b_bytes, lead_b_full);
                     }
-                    ready = bar_try(empty + 8 * stage, phase ^ 1);  // asked early: the answer takes a while
-                    load_a(p, tile, kb, at, bar);
-                    if (!p.stationary) load_b(p, tile, kb, rank, at + kABytes, bar);
-                    if (two) {
-                        load_a(p, tile, kb + 1, at + block_bytes, bar);
-                        if (!p.stationary) load_b(p, tile, kb + 1, rank, at + block_bytes + kABytes, bar);
+                    for (int kb = k.first; kb < k.end; kb += p.per_stage) {
+                        const bool two = p.per_stage == 2 && kb + 1 < k.end;
+                        if (!ready) ok = bar_wait(empty + 8 * stage, phase ^ 1, abort);
+                        if (!ok) break;
+                        const unsigned bar = lead_full + 8 * stage, at = stages0 + stage * stage_bytes;
+                        if (rank == 0) bar_expect(full + 8 * stage, two ? 4 * block_bytes : 2 * block_bytes);
+                        ++issued;
+                        if (++stage == p.stages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                        ready = bar_try(empty + 8 * stage, phase ^ 1);  // asked early: the answer takes a while
+                        load_a(p, tile, kb, at, bar);
+                        if (!p.stationary) load_b(p, tile, kb, rank, at + kABytes, bar);
+                        if (two) {
+                            load_a(p, tile, kb + 1, at + block_bytes, bar);
+                            if (!p.stationary) load_b(p, tile, kb + 1, rank, at + block_bytes + kABytes, bar);
+                        }
                     }
                 }
             }
@@ -762,69 +799,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
             }
         } else if (warp == kProductWarp && rank == 0 && elect_one()) {
-            const unsigned a_hi = (unsigned)(p.adesc >> 32), b_hi = (unsigned)(p.bdesc >> 32);
-            const unsigned a_lo = (unsigned)p.adesc, b_lo = (unsigned)p.bdesc;
             // Tiles left in the column of the first one (stationary B).
             int stage = 0, acc = 0, left = 0;
             unsigned phase = 0, acc_phase = 0, b_phase = 0;
             // Whether the next barriers were seen ready: asked before a block's
             // products are issued, so that the answer is there when they are.
             bool ok = true, full_ready = false, acc_ready = false;
-            for (int t = range.first; t < range.end; t += range.step) {
-                int nk = p.kb;
-                if (p.splits > 1) {
-                    const KRange k = k_range(p, tile_of(p, t, rank));
-                    nk = k.end - k.first;
-                }
-                if (p.stationary && left == 0) {
-                    left = p.nm.d;
-                    if (t == range.first)
-                        left -= t - quotient(t, p.nm) * p.nm.d;
-                    else
-                        mma_commit(b_empty);  // the last column's B is free
-                    ok = bar_wait(b_full, b_phase, abort);
-                    b_phase ^= 1;
-                    if (!ok) break;
-                }
-                --left;
-                if (!acc_ready) ok = bar_wait(acc_empty + 8 * acc, acc_phase ^ 1, abort);
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                const GemmParams &p = launch.p[q];
+                const Range range = my_tiles(p, q ? launch.p[0].tiles : 0);
+                const unsigned a_hi = (unsigned)(p.adesc >> 32), b_hi = (unsigned)(p.bdesc >> 32);
+                const unsigned a_lo = (unsigned)p.adesc, b_lo = (unsigned)p.bdesc;
                 if (!ok) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const unsigned d = tmem + acc * p.bn, this_full = acc_full + 8 * acc;
-                if (++acc == p.nacc) {
-                    acc = 0;
-                    acc_phase ^= 1;
-                }
-                bool more = false;
-                for (int kb = 0; kb < nk; kb += p.per_stage) {
-                    if (!full_ready) ok = bar_wait(full + 8 * stage, phase, abort);
+                for (int t = range.first; t < range.end; t += range.step) {
+                    int nk = p.kb;
+                    if (p.splits > 1) {
+                        const KRange k = k_range(p, tile_of(p, t, rank));
+                        nk = k.end - k.first;
+                    }
+                    if (p.stationary && left == 0) {
+                        left = p.nm.d;
+                        if (t == range.first)
+                            left -= t - quotient(t, p.nm) * p.nm.d;
+                        else
+                            mma_commit(b_empty);  // the last column's B is free
+                        ok = bar_wait(b_full, b_phase, abort);
+                        b_phase ^= 1;
+                        if (!ok) break;
+                    }
+                    --left;
+                    if (!acc_ready) ok = bar_wait(acc_empty + 8 * acc, acc_phase ^ 1, abort);
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const unsigned at = stages0 + stage * stage_bytes, done = empty + 8 * stage;
-                    const unsigned bt = p.stationary ? held0 + kb * p.b_bytes : at + kABytes;
-                    if (++stage == p.stages) {
-                        stage = 0;
-                        phase ^= 1;
+                    const unsigned d = tmem + acc * p.bn, this_full = acc_full + 8 * acc;
+                    if (++acc == p.nacc) {
+                        acc = 0;
+                        acc_phase ^= 1;
                     }
-                    full_ready = bar_try(full + 8 * stage, phase);
-                    if (kb + p.per_stage >= nk) acc_ready = bar_try(acc_empty + 8 * acc, acc_phase ^ 1);
-                    auto block = [&](unsigned a, unsigned b) {
-                        unsigned al = a_lo | (a >> 4), bl = b_lo | (b >> 4);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            mma(d, al, a_hi, bl, b_hi, p.idesc, more, p.fp8);
-                            more = true;
-                            al += p.a_step;
-                            bl += p.b_step;
+                    bool more = false;
+                    for (int kb = 0; kb < nk; kb += p.per_stage) {
+                        if (!full_ready) ok = bar_wait(full + 8 * stage, phase, abort);
+                        if (!ok) break;
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        const unsigned at = stages0 + stage * stage_bytes, done = empty + 8 * stage;
+                        const unsigned bt = p.stationary ? held0 + kb * p.b_bytes : at + kABytes;
+                        if (++stage == p.stages) {
+                            stage = 0;
+                            phase ^= 1;
                         }
-                    };
-                    block(at, bt);
-                    if (p.per_stage == 2 && kb + 1 < nk)
-                        block(at + block_bytes, bt + (p.stationary ? p.b_bytes : block_bytes));
-                    mma_commit(done);
+                        full_ready = bar_try(full + 8 * stage, phase);
+                        if (kb + p.per_stage >= nk) acc_ready = bar_try(acc_empty + 8 * acc, acc_phase ^ 1);
+                        auto block = [&](unsigned a, unsigned b) {
+                            unsigned al = a_lo | (a >> 4), bl = b_lo | (b >> 4);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                mma(d, al, a_hi, bl, b_hi, p.idesc, more, p.fp8);
+                                more = true;
+                                al += p.a_step;
+                                bl += p.b_step;
+                            }
+                        };
+                        block(at, bt);
+                        if (p.per_stage == 2 && kb + 1 < nk)
+                            block(at + block_bytes, bt + (p.stationary ? p.b_bytes : block_bytes));
+                        mma_commit(done);
+                    }
+                    if (!ok) break;
+                    mma_commit(this_full);
                 }
-                if (!ok) break;
-                mma_commit(this_full);
             }
             if (!ok) {
                 const unsigned drain = smem_u32(&bars->drain);
@@ -1116,8 +1159,8 @@ unsigned long long smem_desc(bool mn) {
            ((unsigned long long)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-template <int EPI, int ACT, bool NARROW>
-cudaError_t launch_as(const GemmParams &p, int grid, size_t smem, cudaStream_t s) {
+template <int EPI, int ACT, bool NARROW, int NP>
+cudaError_t launch_as(const GemmLaunch<NP> &l, int grid, size_t smem, cudaStream_t s) {
     // The kernel's shared-memory limit, raised once per device.
     static std::atomic<unsigned long long> raised{0};
     int dev = 0;
@@ -1125,27 +1168,27 @@ cudaError_t launch_as(const GemmParams &p, int grid, size_t smem, cudaStream_t s
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (dev > 63 || !(raised.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(k_gemm<EPI, ACT, NARROW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(k_gemm<EPI, ACT, NARROW, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSmemBytes);
         if (e != cudaSuccess) return e;
         raised.fetch_or(bit, std::memory_order_release);
     }
-    return launch_dependent(k_gemm<EPI, ACT, NARROW>, dim3((unsigned)grid), dim3(kThreads), smem, s, p);
+    return launch_dependent(k_gemm<EPI, ACT, NARROW, NP>, dim3((unsigned)grid), dim3(kThreads), smem, s, l);
 }
 template <int EPI, int ACT>
-cudaError_t launch_as(const GemmParams &p, int grid, size_t smem, cudaStream_t s) {
+cudaError_t launch_act(const GemmLaunch<1> &l, int grid, size_t smem, cudaStream_t s) {
     if constexpr (EPI == kEpiLinear)
-        if (p.narrow) return launch_as<EPI, ACT, true>(p, grid, smem, s);
-    return launch_as<EPI, ACT, false>(p, grid, smem, s);
+        if (l.p[0].narrow) return launch_as<EPI, ACT, true, 1>(l, grid, smem, s);
+    return launch_as<EPI, ACT, false, 1>(l, grid, smem, s);
 }
 template <int EPI>
-cudaError_t launch(const GemmParams &p, int act, int grid, size_t smem, cudaStream_t s) {
+cudaError_t launch(const GemmLaunch<1> &l, int act, int grid, size_t smem, cudaStream_t s) {
     switch (act) {
-        case PDR_ACT_RELU: return launch_as<EPI, PDR_ACT_RELU>(p, grid, smem, s);
-        case PDR_ACT_SILU: return launch_as<EPI, PDR_ACT_SILU>(p, grid, smem, s);
-        case PDR_ACT_GELU: return launch_as<EPI, PDR_ACT_GELU>(p, grid, smem, s);
-        case PDR_ACT_GELU_TANH: return launch_as<EPI, PDR_ACT_GELU_TANH>(p, grid, smem, s);
-        default: return launch_as<EPI, PDR_ACT_NONE>(p, grid, smem, s);
+        case PDR_ACT_RELU: return launch_act<EPI, PDR_ACT_RELU>(l, grid, smem, s);
+        case PDR_ACT_SILU: return launch_act<EPI, PDR_ACT_SILU>(l, grid, smem, s);
+        case PDR_ACT_GELU: return launch_act<EPI, PDR_ACT_GELU>(l, grid, smem, s);
+        case PDR_ACT_GELU_TANH: return launch_act<EPI, PDR_ACT_GELU_TANH>(l, grid, smem, s);
+        default: return launch_act<EPI, PDR_ACT_NONE>(l, grid, smem, s);
     }
 }
 
@@ -1195,11 +1238,19 @@ int gemm_splits(int M, int N, int nz, long long K) {
     return s < 1 ? 1 : (int)s;
 }
 
-cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
+namespace {
+int tile_columns(const GemmArgs &g) {
+    const int kelems = g.dtype == PDR_E4M3 ? kRowBytes : kRowBytes / 2, nz = g.mode == kBatchA ? 2 : 1;
+    if (g.splits > 1) return gemm_tile_columns(g.epi, 1 << 30, g.N, nz, 32);
+    return gemm_tile_columns(g.epi, g.M, g.N, nz, ceil_div(g.K[0], kelems) + ceil_div(g.K[1], kelems));
+}
+
+// Everything of a product but its shared memory.
+cudaError_t plan(const GemmArgs &g, int bcols, GemmParams &p) {
     const bool dual = g.mode == kDualB;
     const int bytes = g.dtype == PDR_E4M3 ? 1 : 2;
     const int kelems = kRowBytes / bytes;
-    GemmParams p = {};
+    p = {};
     p.mode = g.mode;
     p.a_mn = g.a_mn;
     p.b_mn = g.b_mn;
@@ -1210,8 +1261,7 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     p.kb0 = ceil_div(g.K[0], kelems);
     p.kb = p.kb0 + (g.mode == kTwoSources ? ceil_div(g.K[1], kelems) : 0);
     p.kelems = kelems;
-    p.bcols = g.splits > 1 ? gemm_tile_columns(g.epi, 1 << 30, g.N, p.nz, 32)
-                           : gemm_tile_columns(g.epi, g.M, g.N, p.nz, p.kb);
+    p.bcols = bcols;
     p.bn = dual ? 2 * p.bcols : p.bcols;
     p.nm = divisor(ceil_div(g.M, 2 * kBM));
     p.nn = divisor(ceil_div(g.N, p.bcols));
@@ -1220,10 +1270,6 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     p.tiles = (int)tiles;
     p.b_bytes = g.b_mn ? ceil_div(p.bn / 2, 64) * 8192 : p.bn / 2 * kRowBytes;
     p.nacc = p.bn >= 256 ? 2 : 4;
-    // Two or four groups share a tile, 64 columns a warp, and sets of groups take
-    // tiles in turn; a pair's only tile is shared by all that it has 32 columns for.
-    p.sharing = p.tiles <= kSMs / 2 ? p.bcols / kStore : p.bcols / kMaxCols;
-    p.sharing = p.sharing < 1 ? 1 : p.sharing > kGroups ? kGroups : p.sharing;
     p.fp8 = bytes == 1;
     // D fp32 | A and B: f16 0, bf16 1 (kind::f16) or e4m3 0 (kind::f8f6f4) | majors | N / 8 | M / 16
     const unsigned t = g.dtype == PDR_BF16 ? 1 : 0;
@@ -1264,14 +1310,23 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     p.in_dtype = g.in_dtype;
     p.ldi = g.ldi;
     p.colsum = g.colsum;
+    return cudaSuccess;
+}
+
+// Shared memory of a product, or of two with `tiles` in all and the same tile sizes.
+size_t plan_memory(GemmParams &p, int epi, int tiles, bool may_stay) {
+    // Two or four groups share a tile, 64 columns a warp, and sets of groups take
+    // tiles in turn; a pair's only tile is shared by all that it has 32 columns for.
+    p.sharing = tiles <= kSMs / 2 ? p.bcols / kStore : p.bcols / kMaxCols;
+    p.sharing = p.sharing < 1 ? 1 : p.sharing > kGroups ? kGroups : p.sharing;
     const size_t all_b = (size_t)p.kb * p.b_bytes;
-    const int pairs = p.tiles < kSMs / 2 ? p.tiles : kSMs / 2;
+    const int pairs = tiles < kSMs / 2 ? tiles : kSMs / 2;
     const size_t fixed = 1024 + 512 + kEpiWarps * 3 * kMaxCols * 4, buffers = kEpiWarps * kBufferBytes;
-    const bool both = g.epi == kEpiGatedBwd;  // dg and du have a buffer each
+    const bool both = epi == kEpiGatedBwd;  // dg and du have a buffer each
     size_t room = kSmemBytes - fixed - (both ? 2 : 1) * buffers;
     // B stays where it leaves room for three stages of A and a pair has several
     // tiles to use it for.
-    p.stationary = g.splits == 1 && all_b + 3 * kABytes <= room && p.tiles >= 2 * pairs;
+    p.stationary = may_stay && p.splits == 1 && all_b + 3 * kABytes <= room && p.tiles >= 2 * pairs;
     // A second buffer for each epilogue warp, where that takes no stage that is needed.
     p.nbuf = both || (p.stationary && all_b + 4 * kABytes + buffers <= room) ? 2 : 1;
     if (!both) room -= (p.nbuf - 1) * buffers;
@@ -1281,21 +1336,51 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
     // the memory's rate.
     const size_t left = room - (p.stationary ? all_b : 0);
     p.per_stage = p.stationary && p.kb > 1 && left >= 6 * kABytes ? 2 : 1;
-#ifdef X_PS
-    if (!p.stationary && p.kb > 1 && left >= X_PS * (kABytes + p.b_bytes)) p.per_stage = 2;
-#endif
     const size_t stage = p.per_stage * (kABytes + (p.stationary ? 0 : p.b_bytes));
     p.stages = (int)(left / stage);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
-    const size_t smem = fixed + p.nbuf * buffers + p.stages * stage + (p.stationary ? all_b : 0);
-    const int grid = 2 * pairs;
     static_assert(sizeof(Barriers) <= 512, "barriers fit their place");
+    return fixed + p.nbuf * buffers + p.stages * stage + (p.stationary ? all_b : 0);
+}
+
+int blocks_of(int tiles) { return 2 * (tiles < kSMs / 2 ? tiles : kSMs / 2); }
+}  // namespace
+
+cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s) {
+    GemmLaunch<1> l;
+    GemmParams &p = l.p[0];
+    const cudaError_t e = plan(g, tile_columns(g), p);
+    if (e != cudaSuccess) return e;
+    const size_t smem = plan_memory(p, g.epi, p.tiles, true);
+    const int grid = blocks_of(p.tiles);
     switch (g.epi) {
-        case kEpiGated: return launch<kEpiGated>(p, g.act, grid, smem, s);
-        case kEpiSlope: return launch<kEpiSlope>(p, g.act, grid, smem, s);
-        case kEpiGatedBwd: return launch<kEpiGatedBwd>(p, g.act, grid, smem, s);
-        default: return launch<kEpiLinear>(p, g.act, grid, smem, s);
+        case kEpiGated: return launch<kEpiGated>(l, g.act, grid, smem, s);
+        case kEpiSlope: return launch<kEpiSlope>(l, g.act, grid, smem, s);
+        case kEpiGatedBwd: return launch<kEpiGatedBwd>(l, g.act, grid, smem, s);
+        default: return launch<kEpiLinear>(l, g.act, grid, smem, s);
     }
+}
+
+cudaError_t launch_gemm2(const GemmArgs &g0, const GemmArgs &g1, cudaStream_t s) {
+    GemmLaunch<2> l;
+    const int c0 = tile_columns(g0), c1 = tile_columns(g1);
+    cudaError_t e = plan(g0, c0, l.p[0]);
+    if (e != cudaSuccess) return e;
+    // Apart where the first keeps its B in shared memory, or is narrow.
+    plan_memory(l.p[0], g0.epi, l.p[0].tiles, true);
+    if (l.p[0].stationary || g0.narrow || g1.narrow) {
+        e = launch_gemm(g0, s);
+        return e == cudaSuccess ? launch_gemm(g1, s) : e;
+    }
+    const int c = c0 > c1 ? c0 : c1;
+    if (c != c0) e = plan(g0, c, l.p[0]);
+    if (e == cudaSuccess) e = plan(g1, c, l.p[1]);
+    if (e != cudaSuccess) return e;
+    const long long tiles = (long long)l.p[0].tiles + l.p[1].tiles;
+    if (tiles > 1 << 30 || l.p[0].b_bytes != l.p[1].b_bytes) return cudaErrorInvalidValue;
+    const size_t smem = plan_memory(l.p[0], g0.epi, (int)tiles, false);
+    plan_memory(l.p[1], g1.epi, (int)tiles, false);
+    return launch_as<kEpiLinear, PDR_ACT_NONE, false, 2>(l, blocks_of((int)tiles), smem, s);
 }
 
 namespace {

@@ -180,6 +180,9 @@ int gemm_tile_columns(int epi, int M, int N, int nz, long long kb);
 // Tiles along k that fill the machine for a weight gradient, at most `most`.
 int gemm_splits(int M, int N, int nz, long long K);
 cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s);
+// Two products without an activation (kEpiLinear) whose B are laid out alike and have
+// the same N, in one launch where their tiles go together.
+cudaError_t launch_gemm2(const GemmArgs &g0, const GemmArgs &g1, cudaStream_t s);
 // Reads (and clears) the word that a bounded wait sets when it gives up.
 cudaError_t read_wait_error(int *bits, cudaStream_t s);
 

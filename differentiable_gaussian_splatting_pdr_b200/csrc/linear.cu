@@ -248,48 +248,35 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
     }
     if (e == cudaSuccess && colsum)
         e = launch_join_columns(colsum, L.sum_rows, N, grad_bias, bias_dtype, s);
-    if (e == cudaSuccess && grad_x) {
-        GemmArgs g;
-        g.dtype = dtype;
-        g.a[0] = oz;
-        g.b[0] = ow;
-        g.b_mn = true;
-        g.M = M;
-        g.N = K;
-        g.K[0] = N;
-        g.narrow = L.narrow;
-        g.out = L.pack_out ? ws + L.out : grad_x;
-        g.out_dtype = dtype;
-        g.ldo = L.ldo;
-        e = launch_gemm(g, s);
-        if (e == cudaSuccess && L.pack_out) e = launch_unpack(ws + L.out, M, K, L.ldo, 2, grad_x, s);
-    }
-    if (e == cudaSuccess && grad_weight) {
-        GemmArgs g;
-        g.dtype = dtype;
-        g.a[0] = oz;
-        g.b[0] = ox;
-        g.a_mn = g.b_mn = true;
-        g.M = N;
-        g.N = K;
-        g.K[0] = M;
-        g.splits = L.splits;
-        g.ldo = K;
-        const bool partial = L.splits > 1 || K % 8;
-        if (partial) {
-            g.out = ws + L.part;
-            g.out_dtype = PDR_F32;
-            g.ldo = L.ldp;
-            g.out_split = N * L.ldp;
-        } else {
-            g.out = grad_weight;
-            g.out_dtype = dtype;
-        }
-        e = launch_gemm(g, s);
-        if (e == cudaSuccess && partial)
-            e = launch_join(reinterpret_cast<float *>(ws + L.part), L.splits, N, K, L.ldp, grad_weight,
-                            nullptr, dtype, s);
-    }
+    GemmArgs gx, gw;  // dx = dz W, dW = dz^T x
+    gx.dtype = gw.dtype = dtype;
+    gx.a[0] = gw.a[0] = oz;
+    gx.b[0] = ow;
+    gw.b[0] = ox;
+    gx.b_mn = gw.a_mn = gw.b_mn = true;
+    gx.M = M;
+    gw.M = N;
+    gx.N = gw.N = K;
+    gx.K[0] = N;
+    gw.K[0] = M;
+    gx.narrow = L.narrow;
+    gx.out = L.pack_out ? ws + L.out : grad_x;
+    gx.out_dtype = dtype;
+    gx.ldo = L.ldo;
+    const bool partial = L.splits > 1 || K % 8;
+    gw.splits = L.splits;
+    gw.out = partial ? ws + L.part : grad_weight;
+    gw.out_dtype = partial ? (int)PDR_F32 : dtype;
+    gw.ldo = partial ? L.ldp : K;
+    gw.out_split = L.splits > 1 ? N * L.ldp : 0;
+    if (e == cudaSuccess && grad_x && grad_weight)
+        e = launch_gemm2(gx, gw, s);
+    else if (e == cudaSuccess && products)
+        e = launch_gemm(grad_x ? gx : gw, s);
+    if (e == cudaSuccess && grad_x && L.pack_out) e = launch_unpack(ws + L.out, M, K, L.ldo, 2, grad_x, s);
+    if (e == cudaSuccess && grad_weight && partial)
+        e = launch_join(reinterpret_cast<float *>(ws + L.part), L.splits, N, K, L.ldp, grad_weight, nullptr,
+                        dtype, s);
     return done(e);
 }
 
