@@ -969,16 +969,52 @@ __global__ void __launch_bounds__(256) k_unpack(const T *__restrict__ from, long
     }
 }
 
+// A block per `W` columns: thread row y of 256 / W adds rows y, y + 256 / W, ... (eight
+// loads under way at once), then the partial sums are added in order.
+template <int W>
+__device__ __forceinline__ void join_columns(const ColumnJob &j, unsigned block) {
+    constexpr int Y = 256 / W;
+    __shared__ float sums[Y][W + 1];
+    const int x = threadIdx.x % W, y = threadIdx.x / W;
+    const long long c = (long long)block * W + x;
+    float s = 0.0f;
+    if (c < j.cols)
+        for (long long r = y; r < j.rows; r += Y * 8) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = r + Y * k < j.rows ? __ldg(j.part + (r + Y * k) * j.cols + c) : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += v[k];
+        }
+    sums[y][x] = s;
+    __syncthreads();
+    if (y == 0 && c < j.cols) {
+        float v = 0.0f;
+        for (int k = 0; k < Y; ++k) v += sums[k][x];
+        img_store(j.to, (size_t)c, j.dtype, v);
+    }
+}
+__global__ void __launch_bounds__(256) k_join_columns(const ColumnJob j) {
+    grid_dep_wait();
+    join_columns<8>(j, blockIdx.x);
+}
+
 // Four neighbouring columns per thread.  Y rows of threads add a Y-th of the splits
 // each, in order, and their sums are added in order: 8 where there are too few columns to
 // fill the machine.
+// Blocks behind the first `blocks` add up column sums (ColumnJob), 8 columns by 32
+// rows of threads.
 template <int Y>
 __global__ void __launch_bounds__(256) k_join(const float *__restrict__ part, int splits, int rows,
                                               int cols, long long ld, void *to, void *to2,
-                                              int dtype) {
+                                              int dtype, unsigned blocks, const ColumnJob job) {
     constexpr int X = 256 / Y;
     __shared__ float4 sums[Y][X];
     grid_dep_wait();
+    if (blockIdx.x >= blocks) {
+        if (blockIdx.y == 0) join_columns<8>(job, blockIdx.x - blocks);
+        return;
+    }
     const long long n = rows * ld, stride = n * (to2 ? 2 : 1);
     part += blockIdx.y * n;
     if (blockIdx.y) to = to2;
@@ -1024,33 +1060,6 @@ __global__ void __launch_bounds__(256) k_join(const float *__restrict__ part, in
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (c + k < cols) img_store(to, at + k, dtype, v[k]);
-    }
-}
-
-// One block per 32 columns; thread row y adds rows y, y + 32, ..., then the 32
-// partial sums are added in order.
-__global__ void __launch_bounds__(1024) k_join_columns(const float *__restrict__ part,
-                                                       long long rows, long long cols, void *to,
-                                                       int dtype) {
-    __shared__ float sums[32][33];
-    grid_dep_wait();
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const long long c = (long long)blockIdx.x * 32 + x;
-    float s = 0.0f;
-    if (c < cols)
-        for (long long r = y; r < rows; r += 32 * 8) {
-            float v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = r + 32 * k < rows ? __ldg(part + (r + 32 * k) * cols + c) : 0.0f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) s += v[k];
-        }
-    sums[y][x] = s;
-    __syncthreads();
-    if (y == 0 && c < cols) {
-        float v = 0.0f;
-        for (int j = 0; j < 32; ++j) v += sums[j][x];
-        img_store(to, (size_t)c, dtype, v);
     }
 }
 
@@ -1412,18 +1421,17 @@ cudaError_t launch_unpack(const void *from, long long rows, long long cols, long
 }
 
 cudaError_t launch_join(const float *part, int splits, int rows, int cols, long long ld, void *to,
-                        void *to2, int dtype, cudaStream_t s) {
+                        void *to2, int dtype, const ColumnJob &columns, cudaStream_t s) {
     const long long vectors = rows * ld / 4;
     const bool few = vectors < 256 * kSMs;
-    const dim3 grid((unsigned)((vectors + (few ? 31 : 255)) / (few ? 32 : 256)), to2 ? 2 : 1);
+    const unsigned blocks = (unsigned)((vectors + (few ? 31 : 255)) / (few ? 32 : 256));
+    const dim3 grid(blocks + (unsigned)((columns.cols + 7) / 8), to2 ? 2 : 1);
     return launch_dependent(few ? k_join<8> : k_join<1>, grid, dim3(256), 0, s, part, splits, rows, cols, ld,
-                            to, to2, dtype);
+                            to, to2, dtype, blocks, columns);
 }
 
-cudaError_t launch_join_columns(const float *part, long long rows, long long cols, void *to,
-                                int dtype, cudaStream_t s) {
-    return launch_dependent(k_join_columns, dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, s,
-                            part, rows, cols, to, dtype);
+cudaError_t launch_join_columns(const ColumnJob &columns, cudaStream_t s) {
+    return launch_dependent(k_join_columns, dim3((unsigned)((columns.cols + 7) / 8)), dim3(256), 0, s, columns);
 }
 
 long long column_groups(long long M) {

@@ -204,14 +204,19 @@ cudaError_t launch_unpack(const void *from, long long rows, long long cols, long
 inline long long padded(long long cols, int bytes, int unit) {
     return (cols * bytes + unit - 1) / unit * unit / bytes;
 }
+// Column sums of part[rows][cols] to `to`, rounded once to `dtype`; no columns: none.
+struct ColumnJob {
+    const float *part = nullptr;
+    long long rows = 0, cols = 0;
+    void *to = nullptr;
+    int dtype = PDR_F32;
+};
+cudaError_t launch_join_columns(const ColumnJob &columns, cudaStream_t s);
 // to[r][c] = sum over the splits of part[split][r][c], rounded once to `dtype`;
 // partial rows are ld floats apart (a multiple of 4), results dense.  With a
-// second result the splits are part[split][2][rows][ld].
+// second result the splits are part[split][2][rows][ld].  And column sums beside it.
 cudaError_t launch_join(const float *part, int splits, int rows, int cols, long long ld, void *to,
-                        void *to2, int dtype, cudaStream_t s);
-// Column sums of part[rows][cols] (rows in order within fixed groups) to `dtype`.
-cudaError_t launch_join_columns(const float *part, long long rows, long long cols, void *to,
-                                int dtype, cudaStream_t s);
+                        void *to2, int dtype, const ColumnJob &columns, cudaStream_t s);
 // dz = dy in `dz_dtype` (rows of ldz; null: not wanted) and partial column sums
 // of dy, one row of `colsum` for each of column_groups(M) groups of rows (null: not wanted).
 long long column_groups(long long M);

@@ -246,8 +246,6 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
         e = launch_cast_columns(grad, grad_dtype, M, N, L.cast && products ? ws + L.dz : nullptr,
                                 dtype, L.ldz, colsum, s);
     }
-    if (e == cudaSuccess && colsum)
-        e = launch_join_columns(colsum, L.sum_rows, N, grad_bias, bias_dtype, s);
     GemmArgs gx, gw;  // dx = dz W, dW = dz^T x
     gx.dtype = gw.dtype = dtype;
     gx.a[0] = gw.a[0] = oz;
@@ -274,9 +272,13 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
     else if (e == cudaSuccess && products)
         e = launch_gemm(grad_x ? gx : gw, s);
     if (e == cudaSuccess && grad_x && L.pack_out) e = launch_unpack(ws + L.out, M, K, L.ldo, 2, grad_x, s);
+    ColumnJob db;
+    if (colsum) db = {colsum, L.sum_rows, N, grad_bias, bias_dtype};
     if (e == cudaSuccess && grad_weight && partial)
         e = launch_join(reinterpret_cast<float *>(ws + L.part), L.splits, N, K, L.ldp, grad_weight, nullptr,
-                        dtype, s);
+                        dtype, db, s);
+    else if (e == cudaSuccess && colsum)
+        e = launch_join_columns(db, s);
     return done(e);
 }
 

@@ -542,8 +542,7 @@ pdr_status pdr_rms_norm_bwd(const void *grad, const void *sum, int dtype, const 
     // One row of dw for each row of a block: at most 256 x 16 floats.
     err = launch_norm<true>(n, a, n.threads > n.T ? (size_t)(n.threads / n.T) * D * 4 : 0, s);
     if (err == cudaSuccess && grad_weight)
-        err = launch_join_columns(static_cast<const float *>(workspace), n.blocks, D, grad_weight,
-                                  weight_dtype, s);
+        err = launch_join_columns({static_cast<const float *>(workspace), n.blocks, D, grad_weight, weight_dtype}, s);
     return err == cudaSuccess ? PDR_OK : PDR_ERR_CUDA;
 }
 
