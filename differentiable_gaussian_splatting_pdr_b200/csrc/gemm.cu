@@ -66,6 +66,7 @@ struct __align__(64) GemmParams {
     int stationary;                   // B of a column of tiles stays in shared memory
     int per_stage;                    // k blocks of a stage
     int nbuf;                         // buffers of an epilogue warp (1 or 2)
+    int columns;                      // floats of an epilogue warp's bias and column scales
     int b_bytes, kelems;              // a block's B bytes, and k, of a k block
     unsigned idesc;
     unsigned long long adesc, bdesc;  // smem descriptors without the address
@@ -430,7 +431,7 @@ __device__ __forceinline__ void load_b(const GemmParams &p, const Tile &t, int k
 }
 
 // One warp's 32 rows of a tile, from column c0 to c1 (32 columns or 64).
-// `columns`: the warp's bias and column scales, [3][kMaxCols]; `have_n`: the
+// `columns`: the warp's bias and column scales, up to [3][kMaxCols]; `have_n`: the
 // column of tiles that they are of.  Here results leave by TMA, and rows of the
 // input are full 32-byte sectors (a multiple of 16 16-bit, or 8 fp32, wide).
 template <int EPI, int ACT>
@@ -657,8 +658,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     char *held = smem + p.stages * stage_bytes;  // B of all k, where it stays
     char *after = held + (p.stationary ? p.kb * p.b_bytes : 0);
     char *buffers = after;  // nbuf per epilogue warp, 1024-byte aligned
-    float *columns_all = reinterpret_cast<float *>(buffers + kEpiWarps * p.nbuf * kBufferBytes);  // [warp][3][kMaxCols]
-    Barriers *bars = reinterpret_cast<Barriers *>(columns_all + kEpiWarps * 3 * kMaxCols);
+    float *columns_all = reinterpret_cast<float *>(buffers + kEpiWarps * p.nbuf * kBufferBytes);  // [warp][columns]
+    Barriers *bars = reinterpret_cast<Barriers *>(columns_all + kEpiWarps * p.columns);
     const int warp = threadIdx.x >> 5;
     const int rank = blockIdx.x & 1;  // in the pair; block 0 leads
 
@@ -701,7 +702,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         const int ew = warp - kEpiWarp, group = ew >> 2, quarter = warp & 3;
         Staging staging = {buffers + ew * p.nbuf * kBufferBytes, p.nbuf, 0};
-        float *columns = columns_all + ew * 3 * kMaxCols;
+        float *columns = columns_all + ew * p.columns;
         // `sharing` groups divide a tile's columns, sets of them take tiles in turn.
         const int cols = p.bcols / p.sharing, cfirst = group % p.sharing * cols;
         const int sets = kGroups / p.sharing, set = group / p.sharing;
@@ -1330,7 +1331,9 @@ size_t plan_memory(GemmParams &p, int epi, int tiles, bool may_stay) {
     p.sharing = p.sharing < 1 ? 1 : p.sharing > kGroups ? kGroups : p.sharing;
     const size_t all_b = (size_t)p.kb * p.b_bytes;
     const int pairs = tiles < kSMs / 2 ? tiles : kSMs / 2;
-    const size_t fixed = 1024 + 512 + kEpiWarps * 3 * kMaxCols * 4, buffers = kEpiWarps * kBufferBytes;
+    p.columns = p.fp8 ? 3 * kMaxCols : p.bias ? kMaxCols : 0;
+    if (p.narrow) p.columns = 2 * kMaxCols;
+    const size_t fixed = 1024 + 512 + kEpiWarps * p.columns * 4, buffers = kEpiWarps * kBufferBytes;
     const bool both = epi == kEpiGatedBwd;  // dg and du have a buffer each
     size_t room = kSmemBytes - fixed - (both ? 2 : 1) * buffers;
     // B stays where it leaves room for three stages of A and a pair has several

@@ -29,6 +29,7 @@ _E4M3 = torch.float8_e4m3fn
 _HALF = (torch.float16, torch.bfloat16)
 _TYPE = {**_DTYPES, _E4M3: 3}
 _FLOAT = tuple(_DTYPES)
+_MAX_ROWS = 1 << 30  # as in include/pdr.h; sizes travel as C ints
 _OPERAND = (*_HALF, _E4M3)
 
 
@@ -108,7 +109,17 @@ def _check_rows(t, what: str, dtypes):
     if not shape or shape[-1] < 1:
         raise ValueError("%s must be [..., features] with at least one feature" % what)
     width = shape[-1]
-    return (shape[0] if len(shape) == 2 else t.numel() // width), width
+    rows = shape[0] if len(shape) == 2 else t.numel() // width
+    if rows > _MAX_ROWS or width > _MAX_ROWS:
+        raise ValueError("%s has more rows or features than 2^30" % what)
+    return rows, width
+
+
+def _check_weight(w, what: str, dtype, width: int, device):
+    _check(w, what, (dtype,), device=device)
+    if w.dim() != 2 or w.shape[1] != width or not 1 <= w.shape[0] <= _MAX_ROWS:
+        raise ValueError("%s must be [outputs, %d], got %s" % (what, width, list(w.shape)))
+    return w.shape[0]
 
 
 def _aligned(t, n: int = 16):
@@ -146,14 +157,12 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     x and weight: float16, bfloat16, or both float8_e4m3fn with x_scale (a value
     per row of x) and weight_scale [N].  bias [N] is float32 or 16 bits; residual
     [..., N] has out_dtype (float32, float16 or bfloat16; by default x's type, or
-    bfloat16 for 8-bit operands)."""
+    bfloat16 for 8-bit operands).  `out`, where given, is written and returned; it
+    may not overlap the inputs."""
     act = _act(activation)
     M, K = _check_rows(x, "x", _OPERAND)
     dev = x.device
-    _check(weight, "weight", (x.dtype,), device=dev)
-    if weight.dim() != 2 or weight.shape[1] != K or weight.shape[0] < 1:
-        raise ValueError("weight must be [N, %d], got %s" % (K, list(weight.shape)))
-    N = weight.shape[0]
+    N = _check_weight(weight, "weight", x.dtype, K, dev)
     if x_scale is not None or weight_scale is not None or x.dtype == _E4M3:
         _check_scales(x, (weight,), x_scale, (weight_scale,), M)
     if out_dtype is None:
@@ -187,10 +196,7 @@ def linear_bwd(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, bias: 
     act = _act(activation)
     M, K = _check_rows(x, "x", _HALF)
     dev = x.device
-    _check(weight, "weight", (x.dtype,), device=dev)
-    if weight.dim() != 2 or weight.shape[1] != K or weight.shape[0] < 1:
-        raise ValueError("weight must be [N, %d], got %s" % (K, list(weight.shape)))
-    N = weight.shape[0]
+    N = _check_weight(weight, "weight", x.dtype, K, dev)
     _check(grad, "grad", _FLOAT, torch.Size((*x.shape[:-1], N)), dev)
     if bias is not None:
         _check(bias, "bias", _FLOAT, (N,), dev)
@@ -231,11 +237,9 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
 
 def _check_gated(x, w_gate, w_up, dtypes):
     M, D = _check_rows(x, "x", dtypes)
-    _check(w_gate, "w_gate", (x.dtype,), device=x.device)
-    if w_gate.dim() != 2 or w_gate.shape[1] != D or w_gate.shape[0] < 1:
-        raise ValueError("w_gate must be [F, %d], got %s" % (D, list(w_gate.shape)))
+    F = _check_weight(w_gate, "w_gate", x.dtype, D, x.device)
     _check(w_up, "w_up", (x.dtype,), w_gate.shape, x.device)
-    return M, D, w_gate.shape[0]
+    return M, D, F
 
 
 def gated_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activation: str = "silu",
@@ -245,7 +249,8 @@ def gated_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activat
     """act(x Wg^T) * (x Wu^T): h [..., F] from x [..., D] and two weights [F, D].
 
     float16, bfloat16, or float8_e4m3fn with the scales (x's rows, [F], [F]).
-    out_dtype: x's type, or bfloat16 for 8-bit operands, unless given."""
+    out_dtype: x's type, or bfloat16 for 8-bit operands, unless given.  `out` as in
+    linear_fwd."""
     act = _act(activation)
     M, D, F = _check_gated(x, w_gate, w_up, _OPERAND)
     dev = x.device

@@ -357,6 +357,32 @@ def test_non_finite_values_stay_in_their_rows():
     assert torch.isnan(scale[7]) and torch.isinf(scale[130]) and torch.isfinite(scale[~hit]).all()
 
 
+def test_non_finite_weights_stay_in_their_columns():
+    rng = np.random.default_rng(34)
+    x, w, wu = rand(rng, (300, 72), F16), rand(rng, (70, 72), F16), rand(rng, (70, 72), F16)
+    bad = w.clone()
+    bad[5, 3], bad[64, 0] = float("nan"), float("inf")
+    hit = torch.zeros(70, dtype=torch.bool, device="cuda")
+    hit[[5, 64]] = True
+    for kind in ACTS:
+        for a, b in [(F.linear_fwd(x, bad, activation=kind), F.linear_fwd(x, w, activation=kind)),
+                     (F.gated_fwd(x, bad, wu, kind), F.gated_fwd(x, w, wu, kind)),
+                     (F.gated_fwd(x, wu, bad, kind), F.gated_fwd(x, wu, w, kind))]:
+            assert torch.equal(a[:, ~hit], b[:, ~hit]) and torch.isnan(a[:, 5]).all()
+
+
+def test_vectors_are_single_rows():
+    rng = np.random.default_rng(35)
+    x, w, wu, b, n = (rand(rng, s, BF16) for s in [(40,), (24, 40), (24, 40), (24,), (40,)])
+    assert torch.equal(F.linear_fwd(x, w, b), F.linear_fwd(x[None], w, b)[0])
+    assert torch.equal(F.gated_fwd(x, w, wu), F.gated_fwd(x[None], w, wu)[0])
+    assert torch.equal(F.rms_norm_fwd(x, n, x)[0], F.rms_norm_fwd(x[None], n, x[None])[0][0])
+    q, sc = F.quantize_rows(x)
+    assert q.shape == (40,) and sc.shape == ()
+    for a, e in zip(F.linear_bwd(b, x, w, b, "silu"), F.linear_bwd(b[None], x[None], w, b, "silu")):
+        assert torch.equal(a, e.view(a.shape))
+
+
 def test_repeated_calls_give_the_same_bits():
     rng = np.random.default_rng(13)
     x, w, wu, b, g = (rand(rng, s, BF16) for s in [(5000, 136), (96, 136), (96, 136), (96,), (5000, 96)])
