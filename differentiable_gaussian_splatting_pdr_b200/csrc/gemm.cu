@@ -944,7 +944,11 @@ __global__ void __launch_bounds__(256) k_pack(const PackJobs p) {
         pack_rows<unsigned>(j, block, blocks);
 }
 
-// And back.  Elements of 16 bits go in pairs that start at 4 bytes.
+// And back, a row per warp.  Rows of 16-bit elements: what a thread writes starts at 16
+// bytes; it lies the same distance behind a vector of the padded row for the whole
+// row, so that two aligned loads and a shift make it (linear 60000 x 128 -> 777 72 us, by
+// pairs of elements 99).  32-bit elements go one by one, a warp's together (60000 x 128 -> 333
+// 50 us; by shifted vectors 53).
 template <typename T>
 __global__ void __launch_bounds__(256) k_unpack(const T *__restrict__ from, long long rows, int cols,
                                                 int ld, T *__restrict__ to) {
@@ -953,20 +957,29 @@ __global__ void __launch_bounds__(256) k_unpack(const T *__restrict__ from, long
     for (long long r = (long long)blockIdx.x * 8 + warp; r < rows; r += (long long)gridDim.x * 8) {
         const T *row = from + r * ld;
         T *out = to + r * cols;
-        if constexpr (sizeof(T) == 2) {
-            const int odd = (int)((reinterpret_cast<uintptr_t>(out) >> 1) & 1);
-            for (int c = 2 * lane - odd; c < cols; c += 64) {
-                const unsigned a = c >= 0 ? __ldg(row + c) : 0, b = c + 1 < cols ? __ldg(row + c + 1) : 0;
-                if (c >= 0 && c + 1 < cols)
-                    *reinterpret_cast<unsigned *>(out + c) = a | b << 16;
-                else if (c >= 0)
-                    out[c] = (T)a;
-                else if (cols > 0)
-                    out[0] = (T)b;
-            }
-        } else {
+        if constexpr (sizeof(T) == 4) {
             for (int c = lane; c < cols; c += 32) out[c] = __ldg(row + c);
+            continue;
         }
+        int head = (int)((0 - (reinterpret_cast<uintptr_t>(out) >> 1)) & 7);  // before the first vector
+        if (head > cols) head = cols;
+        const int vectors = (cols - head) / 8, tail = head + 8 * vectors;
+        if (lane < head) out[lane] = __ldg(row + lane);
+        const uint4 *in = reinterpret_cast<const uint4 *>(row);
+        uint4 *whole = reinterpret_cast<uint4 *>(out + head);
+#pragma unroll 2
+        for (int v = lane; v < vectors; v += 32) {
+            const uint4 a = __ldg(in + v), b = __ldg(in + v + (head != 0));  // (b's first element is in the row)
+            unsigned w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = head & 4 ? w[i + 2] : w[i];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = head & 2 ? w[i + 1] : w[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = head & 1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+            whole[v] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (lane < cols - tail) out[tail + lane] = __ldg(row + tail + lane);
     }
 }
 
@@ -1212,6 +1225,7 @@ Divisor divisor(int d) {
 
 }  // namespace
 
+// (524288 x 256 to 6 fp32 columns with a residual: 50 us, through padded copies 143.)
 bool gemm_narrow(int N, int out_dtype, bool has_in) {
     const int row = N * dtype_bytes(out_dtype);
     return N <= kChunk && (row % 16 || (has_in && row % 32));
@@ -1326,7 +1340,8 @@ cudaError_t plan(const GemmArgs &g, int bcols, GemmParams &p) {
 // Shared memory of a product, or of two with `tiles` in all and the same tile sizes.
 size_t plan_memory(GemmParams &p, int epi, int tiles, bool may_stay) {
     // Two or four groups share a tile, 64 columns a warp, and sets of groups take
-    // tiles in turn; a pair's only tile is shared by all that it has 32 columns for.
+    // tiles in turn (gated: 63 us, with 32 columns a warp 66; in 8 bits 72 and 78); a pair's
+    // only tile is shared by all that it has 32 columns for.
     p.sharing = tiles <= kSMs / 2 ? p.bcols / kStore : p.bcols / kMaxCols;
     p.sharing = p.sharing < 1 ? 1 : p.sharing > kGroups ? kGroups : p.sharing;
     const size_t all_b = (size_t)p.kb * p.b_bytes;
@@ -1337,9 +1352,12 @@ size_t plan_memory(GemmParams &p, int epi, int tiles, bool may_stay) {
     const bool both = epi == kEpiGatedBwd;  // dg and du have a buffer each
     size_t room = kSmemBytes - fixed - (both ? 2 : 1) * buffers;
     // B stays where it leaves room for three stages of A and a pair has several
-    // tiles to use it for.
+    // tiles to use it for (65536 x 256 to 1024 columns with silu: 62 against 67 us, gated in
+    // 8 bits 72 against 76, to 8 columns 50 against 53).
     p.stationary = may_stay && p.splits == 1 && all_b + 3 * kABytes <= room && p.tiles >= 2 * pairs;
-    // A second buffer for each epilogue warp, where that takes no stage that is needed.
+    // A second buffer for each epilogue warp, where that takes no stage that is needed
+    // (524288 x 256 to 8 columns: 50 against 51 us; 65536 x 256 to 1024 with gelu and a
+    // residual 109 against 113).
     p.nbuf = both || (p.stationary && all_b + 4 * kABytes + buffers <= room) ? 2 : 1;
     if (!both) room -= (p.nbuf - 1) * buffers;
     // A stage of two k blocks, where there are as many and room for three stages,
@@ -1378,7 +1396,9 @@ cudaError_t launch_gemm2(const GemmArgs &g0, const GemmArgs &g1, cudaStream_t s)
     const int c0 = tile_columns(g0), c1 = tile_columns(g1);
     cudaError_t e = plan(g0, c0, l.p[0]);
     if (e != cudaSuccess) return e;
-    // Apart where the first keeps its B in shared memory, or is narrow.
+    // Together they took 26 us, one after the other 32 (dx and dW of 16384 x 256 to 1024;
+    // the gated backward pass 68 and 74).  Apart where the first keeps its B in shared
+    // memory, or is narrow.
     plan_memory(l.p[0], g0.epi, l.p[0].tiles, true);
     if (l.p[0].stationary || g0.narrow || g1.narrow) {
         e = launch_gemm(g0, s);
@@ -1426,6 +1446,8 @@ cudaError_t launch_unpack(const void *from, long long rows, long long cols, long
 cudaError_t launch_join(const float *part, int splits, int rows, int cols, long long ld, void *to,
                         void *to2, int dtype, const ColumnJob &columns, cudaStream_t s) {
     const long long vectors = rows * ld / 4;
+    // (Always Y = 8: gated backward with 1024 x 256 weights 75 against 68 us.  Always Y = 1:
+    // backward of 131072 x 256 to 8 columns 60 against 57, to 256 columns 172 against 170.)
     const bool few = vectors < 256 * kSMs;
     const unsigned blocks = (unsigned)((vectors + (few ? 31 : 255)) / (few ? 32 : 256));
     const dim3 grid(blocks + (unsigned)((columns.cols + 7) / 8), to2 ? 2 : 1);
