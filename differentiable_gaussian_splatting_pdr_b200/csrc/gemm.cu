@@ -60,6 +60,10 @@ struct __align__(64) GemmParams {
     int mode, a_mn, b_mn;
     int M, N, nz, splits, tiles;
     Divisor nm, nn;                   // tiles of 256 rows, of bcols columns
+    // Where B stays: `share` pairs walk down the first na rows of each column of tiles
+    // in turn (`main` tiles), the other pairs down the last nb rows, one column after another.
+    Divisor na, nb;
+    int share, main;
     int kb0, kb;                      // k blocks of the first source, of all
     int bn, bcols, stages, nacc;      // bcols: result columns of a tile
     int sharing;                      // epilogue groups that share a tile
@@ -367,15 +371,28 @@ struct KRange {
 __device__ __forceinline__ int quotient(int n, const Divisor &d) {
     return d.d == 1 ? n : (int)(__umulhi((unsigned)n, d.mul) >> d.shift);
 }
+// Whether B stays in shared memory (of two products in a launch neither does).
+template <int NP>
+__device__ __forceinline__ bool stays(const GemmParams &p) {
+    return NP == 1 && p.stationary;
+}
+template <int NP>
 __device__ __forceinline__ Tile tile_of(const GemmParams &p, int t, int rank) {
     Tile r;
-    // Down the columns of tiles, or along the rows: neighbouring pairs share A rows in L2.
-    const Divisor &inner = p.stationary ? p.nm : p.nn, &outer = p.stationary ? p.nn : p.nm;
-    const int q = quotient(t, inner), i = t - q * inner.d;
-    t = quotient(q, outer);
-    const int o = q - t * outer.d;
-    r.m = 2 * (p.stationary ? i : o) + rank;
-    r.n = p.stationary ? o : i;
+    if (stays<NP>(p)) {
+        const bool last = t >= p.main;
+        const Divisor &rows = last ? p.nb : p.na;
+        if (last) t -= p.main;
+        const int c = quotient(t, rows), z = quotient(c, p.nn);
+        r.m = 2 * (t - c * (int)rows.d + (last ? (int)(p.nm.d - p.nb.d) : 0)) + rank;
+        r.n = c - z * (int)p.nn.d;
+        t = z;
+    } else {  // along the rows: neighbouring pairs share A rows in L2
+        const int q = quotient(t, p.nn), z = quotient(q, p.nm);
+        r.n = t - q * (int)p.nn.d;
+        r.m = 2 * (q - z * (int)p.nm.d) + rank;
+        t = z;
+    }
     r.z = 0;
     r.split = t;
     if (p.nz == 2) {
@@ -389,15 +406,28 @@ __device__ __forceinline__ KRange k_range(const GemmParams &p, const Tile &t) {
     return {(int)((unsigned)(p.kb * t.split) / (unsigned)p.splits),  // kb * splits < 2^31
             (int)((unsigned)(p.kb * (t.split + 1)) / (unsigned)p.splits)};
 }
+// The column of tiles of a tile (stationary B).
+__device__ __forceinline__ int column_of(const GemmParams &p, int t) {
+    return t < p.main ? quotient(t, p.na) : quotient(t - p.main, p.nb);
+}
 // The tiles of a pair: a contiguous run of the columns, or every so many.
 struct Range {
     int first, end, step;
 };
 // (`before`: tiles of the product in front, after which the turn goes on.)
+template <int NP>
 __device__ __forceinline__ Range my_tiles(const GemmParams &p, int before) {
     const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
-    if (p.stationary)
-        return {(int)((long long)p.tiles * pair / pairs), (int)((long long)p.tiles * (pair + 1) / pairs), 1};
+    if (stays<NP>(p)) {
+        const int columns = p.nn.d * p.nz, sharing = columns * p.share;
+        if (pair < sharing) {
+            const int first = pair % columns * (int)p.na.d;
+            return {first + pair / columns, first + (int)p.na.d, p.share};
+        }
+        const long long rest = p.tiles - p.main;
+        return {p.main + (int)(rest * (pair - sharing) / (pairs - sharing)),
+                p.main + (int)(rest * (pair - sharing + 1) / (pairs - sharing)), 1};
+    }
     const int first = pair - before % pairs;
     return {first < 0 ? first + pairs : first, p.tiles, pairs};
 }
@@ -653,10 +683,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const GemmParams &p = launch.p[0];  // (both have the same tiles and shared memory)
     // Tiles first, at a 1024-byte boundary (the swizzle's period).
     char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    const int block_bytes = kABytes + (p.stationary ? 0 : p.b_bytes);  // of a k block
+    const int block_bytes = kABytes + (stays<NP>(p) ? 0 : p.b_bytes);  // of a k block
     const int stage_bytes = p.per_stage * block_bytes;
     char *held = smem + p.stages * stage_bytes;  // B of all k, where it stays
-    char *after = held + (p.stationary ? p.kb * p.b_bytes : 0);
+    char *after = held + (stays<NP>(p) ? p.kb * p.b_bytes : 0);
     char *buffers = after;  // nbuf per epilogue warp, 1024-byte aligned
     float *columns_all = reinterpret_cast<float *>(buffers + kEpiWarps * p.nbuf * kBufferBytes);  // [warp][columns]
     Barriers *bars = reinterpret_cast<Barriers *>(columns_all + kEpiWarps * p.columns);
@@ -713,9 +743,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
             const GemmParams &p = launch.p[q];
-            const Range range = my_tiles(p, q ? launch.p[0].tiles : 0);
+            const Range range = my_tiles<NP>(p, q ? launch.p[0].tiles : 0);
             int have_n = -1;
-            Tile tile = tile_of(p, range.first, rank);
+            Tile tile = tile_of<NP>(p, range.first, rank);
             for (int t = range.first; t < range.end && ok; t += range.step, ++it) {
                 if ((it & (sets - 1)) == set) {
                     const unsigned d = tmem + ((unsigned)(32 * quarter) << 16) + acc * p.bn;
@@ -729,8 +759,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                                      abort, release + 8 * acc);
                     if (!ok) break;
                 }
-                tile.m += 2;  // down the column, or looked up
-                if (!p.stationary || tile.m >= 2 * (int)p.nm.d) tile = tile_of(p, t + range.step, rank);
+                tile.m += 2 * range.step;  // down the column, or looked up
+                if (!stays<NP>(p) || t >= p.main) tile = tile_of<NP>(p, t + range.step, rank);
                 if (++acc == p.nacc) {
                     acc = 0;
                     acc_phase ^= 1;
@@ -749,12 +779,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
                 const GemmParams &p = launch.p[q];
-                const Range range = my_tiles(p, q ? launch.p[0].tiles : 0);
+                const Range range = my_tiles<NP>(p, q ? launch.p[0].tiles : 0);
                 for (int t = range.first; t < range.end && ok; t += range.step) {
-                    const Tile tile = tile_of(p, t, rank);
+                    const Tile tile = tile_of<NP>(p, t, rank);
                     const KRange k = k_range(p, tile);
-                    if (p.stationary && column != quotient(t, p.nm)) {
-                        column = quotient(t, p.nm);
+                    if (stays<NP>(p) && column != column_of(p, t)) {
+                        column = column_of(p, t);
                         ok = bar_wait(b_empty, b_phase ^ 1, abort);
                         if (!ok) break;
                         b_phase ^= 1;
@@ -775,10 +805,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                         ready = bar_try(empty + 8 * stage, phase ^ 1);  // asked early: the answer takes a while
                         load_a(p, tile, kb, at, bar);
-                        if (!p.stationary) load_b(p, tile, kb, rank, at + kABytes, bar);
+                        if (!stays<NP>(p)) load_b(p, tile, kb, rank, at + kABytes, bar);
                         if (two) {
                             load_a(p, tile, kb + 1, at + block_bytes, bar);
-                            if (!p.stationary) load_b(p, tile, kb + 1, rank, at + block_bytes + kABytes, bar);
+                            if (!stays<NP>(p)) load_b(p, tile, kb + 1, rank, at + block_bytes + kABytes, bar);
                         }
                     }
                 }
@@ -809,22 +839,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
                 const GemmParams &p = launch.p[q];
-                const Range range = my_tiles(p, q ? launch.p[0].tiles : 0);
+                const Range range = my_tiles<NP>(p, q ? launch.p[0].tiles : 0);
                 const unsigned a_hi = (unsigned)(p.adesc >> 32), b_hi = (unsigned)(p.bdesc >> 32);
                 const unsigned a_lo = (unsigned)p.adesc, b_lo = (unsigned)p.bdesc;
                 if (!ok) break;
                 for (int t = range.first; t < range.end; t += range.step) {
                     int nk = p.kb;
                     if (p.splits > 1) {
-                        const KRange k = k_range(p, tile_of(p, t, rank));
+                        const KRange k = k_range(p, tile_of<NP>(p, t, rank));
                         nk = k.end - k.first;
                     }
-                    if (p.stationary && left == 0) {
-                        left = p.nm.d;
-                        if (t == range.first)
-                            left -= t - quotient(t, p.nm) * p.nm.d;
-                        else
+                    if (stays<NP>(p) && left == 0) {
+                        left = t < p.main ? p.tiles : p.nb.d;
+                        if (t != range.first)
                             mma_commit(b_empty);  // the last column's B is free
+                        else if (t >= p.main)
+                            left -= t - p.main - column_of(p, t) * p.nb.d;
                         ok = bar_wait(b_full, b_phase, abort);
                         b_phase ^= 1;
                         if (!ok) break;
@@ -844,7 +874,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (!ok) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         const unsigned at = stages0 + stage * stage_bytes, done = empty + 8 * stage;
-                        const unsigned bt = p.stationary ? held0 + kb * p.b_bytes : at + kABytes;
+                        const unsigned bt = stays<NP>(p) ? held0 + kb * p.b_bytes : at + kABytes;
                         if (++stage == p.stages) {
                             stage = 0;
                             phase ^= 1;
@@ -863,7 +893,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         };
                         block(at, bt);
                         if (p.per_stage == 2 && kb + 1 < nk)
-                            block(at + block_bytes, bt + (p.stationary ? p.b_bytes : block_bytes));
+                            block(at + block_bytes, bt + (stays<NP>(p) ? p.b_bytes : block_bytes));
                         mma_commit(done);
                     }
                     if (!ok) break;
@@ -1235,14 +1265,15 @@ int gemm_tile_columns(int epi, int M, int N, int nz, long long kb) {
     const bool dual = epi == kEpiGated || epi == kEpiGatedBwd;
     // The width whose rounds of tiles over the pairs take least, in clocks as
     // measured: 560 + 4/3 per accumulator column and k block (the copies' way
-    // from L2 bounds them), 16 per column in the epilogue beside the next tile's
-    // products, and the first tile's start and the last one's end.
+    // from L2 bounds them), 300 + 16 per column in the epilogue beside the next tile's
+    // products, and the first tile's start and the last one's end.  (Without the 300, short k
+    // took narrow tiles: gated 49152 x 64 to 1024 62 against 42 us.)
     int best = 32;
     double least = -1;
     for (int c = dual ? 128 : 256; c >= 32; c /= 2) {
         const long long tiles = (long long)ceil_div(M, 2 * kBM) * ceil_div(N, c) * nz;
         const int bn = dual ? 2 * c : c;
-        const double products = kb * (560 + 4 * bn / 3), ends = 16.0 * bn;
+        const double products = kb * (560 + 4 * bn / 3), ends = 300 + 16.0 * bn;
         const double cost = (tiles + kSMs / 2 - 1) / (kSMs / 2) * (products > ends ? products : ends) +
                             3000 + ends;
         if (least < 0 || cost < least) {
@@ -1337,6 +1368,32 @@ cudaError_t plan(const GemmArgs &g, int bcols, GemmParams &p) {
     return cudaSuccess;
 }
 
+// Divides the columns of tiles among the pairs (stationary B): neighbouring rows of
+// tiles are under way at the same time, whole rows of the matrices together, which the
+// memory serves faster than as many places a column apart (65536 x 256 to 1024 columns: 39
+// against 43 us, with fp32 results and a residual 138 against 150, gated backward of
+// 49152 x 64 to 1024 175 against 203).
+void share_columns(GemmParams &p, int pairs) {
+    const int rows = p.nm.d, columns = p.nn.d * p.nz, left = pairs % columns;
+    p.share = pairs / columns;
+    int last = 0;  // rows for the pairs that are left over
+    if (left && p.share) {
+        last = (int)((long long)left * rows / pairs);
+        auto rounds = [&](int x) {
+            const int a = ceil_div(rows - x, p.share), b = ceil_div((long long)x * columns, left);
+            return a > b ? a : b;
+        };
+        if (rounds(last + 1) < rounds(last)) ++last;
+    }
+    if (!p.share || (left && !last)) {
+        p.share = 0;
+        last = rows;
+    }
+    p.main = (rows - last) * columns;
+    p.na = divisor(rows - last > 0 ? rows - last : 1);
+    p.nb = divisor(last > 0 ? last : 1);
+}
+
 // Shared memory of a product, or of two with `tiles` in all and the same tile sizes.
 size_t plan_memory(GemmParams &p, int epi, int tiles, bool may_stay) {
     // Two or four groups share a tile, 64 columns a warp, and sets of groups take
@@ -1355,6 +1412,7 @@ size_t plan_memory(GemmParams &p, int epi, int tiles, bool may_stay) {
     // tiles to use it for (65536 x 256 to 1024 columns with silu: 62 against 67 us, gated in
     // 8 bits 72 against 76, to 8 columns 50 against 53).
     p.stationary = may_stay && p.splits == 1 && all_b + 3 * kABytes <= room && p.tiles >= 2 * pairs;
+    if (p.stationary) share_columns(p, pairs);
     // A second buffer for each epilogue warp, where that takes no stage that is needed
     // (524288 x 256 to 8 columns: 50 against 51 us; 65536 x 256 to 1024 with gelu and a
     // residual 109 against 113).
