@@ -1107,54 +1107,101 @@ __global__ void __launch_bounds__(256) k_join(const float *__restrict__ part, in
     }
 }
 
-// Rows of a group whose column sums one block forms: about four blocks per SM, at
-// least 64 rows.
-long long group_rows(long long M) {
-    const long long r = (M + 4 * kSMs - 1) / (4 * kSMs);
-    return r < 64 ? 64 : r;
+// dy is taken in vectors of 16 bytes; a thread keeps its vector of the rows, and so its
+// columns.
+struct ColumnPlan {
+    int vectors;              // of a row (the last one may lie behind its end in part)
+    long long group;          // rows of a block
+    unsigned blocks, across;  // down the rows, and across 256 vectors each
+};
+ColumnPlan column_plan(long long M, int N, int bytes) {
+    const int E = 16 / bytes;
+    ColumnPlan p = {};
+    p.vectors = (N + E - 1) / E;
+    p.across = (unsigned)((p.vectors + 255) / 256);
+    // Four blocks an SM.
+    const int per = p.vectors < 256 ? 256 / p.vectors : 1;
+    long long blocks = 4 * kSMs / p.across;
+    if (blocks > M / per) blocks = M / per;
+    if (blocks < 1) blocks = 1;
+    p.group = (M + blocks - 1) / blocks;
+    p.blocks = M > 0 ? (unsigned)((M + p.group - 1) / p.group) : 0;
+    return p;
 }
 
-template <typename T>
-__device__ __forceinline__ float widen(T v, int dtype) {
-    if constexpr (sizeof(T) == 4)
-        return v;
-    else
-        return unpack2(v, dtype).x;
-}
-
-// A block takes a group of rows and 256 columns (all of them where there are fewer,
-// 256 / N rows at once); a thread keeps its column, four rows under way at once.
+// (Backward of 131072 x 256 to 256 columns, bf16 and a bias: 73 us, by single elements 162;
+// of 30000 x 256 to 777 columns, whose rows start anywhere, 63 and 101.)
 template <typename T>
 __global__ void __launch_bounds__(256) k_cast_columns(const T *__restrict__ dy, int dy_dtype,
-                                                      long long M, int N, void *__restrict__ dz,
-                                                      int dz_dtype, long long ldz, long long group,
-                                                      float *__restrict__ colsum) {
-    __shared__ float sums[256];
+                                                      long long M, int N, ColumnPlan p,
+                                                      void *__restrict__ dz, int dz_dtype,
+                                                      long long ldz, float *__restrict__ colsum) {
+    constexpr int E = 16 / sizeof(T);
+    __shared__ float sums[256][E + 1];
     grid_dep_wait();
-    const long long r0 = blockIdx.x * group, r1 = r0 + group < M ? r0 + group : M;
-    const int base = blockIdx.y * 256, width = N - base < 256 ? N - base : 256;
-    const int per = N < 256 ? 256 / N : 1;  // rows at once
-    const int sub = threadIdx.x / width, c = base + threadIdx.x % width;
-    float s = 0.0f;
+    const long long r0 = blockIdx.x * p.group, r1 = r0 + p.group < M ? r0 + p.group : M;
+    const int base = blockIdx.y * 256, width = p.vectors - base < 256 ? p.vectors - base : 256;
+    const int per = 256 / width;  // rows at once
+    const int sub = threadIdx.x / width, j = base + threadIdx.x % width;
+    const bool whole = N % E == 0;  // rows start at 16 bytes
+    float s[E] = {};
     if (sub < per)
         for (long long r = r0 + sub; r < r1; r += 4 * per) {
-            float v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                v[k] = r + k * per < r1 ? widen<T>(__ldg(dy + (r + k * per) * N + c), dy_dtype) : 0.0f;
+            uint4 raw[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                s += v[k];
-                if (dz && r + k * per < r1) img_store(dz, (size_t)((r + k * per) * ldz + c), dz_dtype, v[k]);
+                const T *row = dy + (r + k * per) * N;
+                if (r + k * per >= r1)
+                    raw[k] = make_uint4(0, 0, 0, 0);
+                else if (whole)
+                    raw[k] = __ldg(reinterpret_cast<const uint4 *>(row) + j);
+                else
+                    raw[k] = padded_vector(row, j, N);  // (zeros behind the row's end)
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const unsigned w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+                float v[E];
+                if constexpr (E == 4) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = unpack2(w[i], dy_dtype);
+                        v[2 * i] = f.x;
+                        v[2 * i + 1] = f.y;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < E; ++i) s[i] += v[i];
+                if (!dz || r + k * per >= r1) continue;
+                unsigned two[E / 2];
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) two[i] = pack2(v[2 * i], v[2 * i + 1], dz_dtype);
+                // (Padded rows hold whole vectors.)
+                unsigned short *to = static_cast<unsigned short *>(dz) + (r + k * per) * ldz + j * E;
+                if constexpr (E == 4)
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(two[0], two[1]);
+                else
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(two[0], two[1], two[2], two[3]);
             }
         }
     if (!colsum) return;
-    sums[threadIdx.x] = s;
-    __syncthreads();
-    if ((int)threadIdx.x < width) {
-        for (int j = 1; j < per; ++j) s += sums[threadIdx.x + j * width];
-        colsum[(long long)blockIdx.x * N + c] = s;
+    for (int half = 128; half >= 1; half /= 2) {  // the upper half of the rows to the lower, in turn
+        if (half >= per) continue;
+        if (sub >= half && sub < 2 * half && sub < per)
+#pragma unroll
+            for (int i = 0; i < E; ++i) sums[threadIdx.x][i] = s[i];
+        __syncthreads();
+        if (sub < half && sub + half < per)
+#pragma unroll
+            for (int i = 0; i < E; ++i) s[i] += sums[threadIdx.x + half * width][i];
     }
+    if (sub == 0)
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (j * E + i < N) colsum[(long long)blockIdx.x * N + j * E + i] = s[i];
 }
 
 // ---- host ----------------------------------------------------------------------
@@ -1455,10 +1502,9 @@ cudaError_t launch_gemm2(const GemmArgs &g0, const GemmArgs &g1, cudaStream_t s)
     cudaError_t e = plan(g0, c0, l.p[0]);
     if (e != cudaSuccess) return e;
     // Together they took 26 us, one after the other 32 (dx and dW of 16384 x 256 to 1024;
-    // the gated backward pass 68 and 74).  Apart where the first keeps its B in shared
-    // memory, or is narrow.
-    plan_memory(l.p[0], g0.epi, l.p[0].tiles, true);
-    if (l.p[0].stationary || g0.narrow || g1.narrow) {
+    // the gated backward pass 68 and 74), and 33 against 39 where the first alone would
+    // keep its B in shared memory (40722 x 440 to 8).  Apart where one is narrow.
+    if (g0.narrow || g1.narrow) {
         e = launch_gemm(g0, s);
         return e == cudaSuccess ? launch_gemm(g1, s) : e;
     }
@@ -1517,20 +1563,20 @@ cudaError_t launch_join_columns(const ColumnJob &columns, cudaStream_t s) {
     return launch_dependent(k_join_columns, dim3((unsigned)((columns.cols + 7) / 8)), dim3(256), 0, s, columns);
 }
 
-long long column_groups(long long M) {
-    const long long g = group_rows(M);
-    return (M + g - 1) / g;
+long long column_groups(long long M, int N, int dy_dtype) {
+    return column_plan(M, N, dtype_bytes(dy_dtype)).blocks;
 }
 
 cudaError_t launch_cast_columns(const void *dy, int dy_dtype, long long M, int N, void *dz,
                                 int dz_dtype, long long ldz, float *colsum, cudaStream_t s) {
-    const dim3 grid((unsigned)column_groups(M), (unsigned)((N + 255) / 256));
+    const ColumnPlan p = column_plan(M, N, dtype_bytes(dy_dtype));
+    const dim3 grid(p.blocks, p.across);
     if (dy_dtype == PDR_F32)
         return launch_dependent(k_cast_columns<float>, grid, dim3(256), 0, s, static_cast<const float *>(dy),
-                                dy_dtype, M, N, dz, dz_dtype, ldz, group_rows(M), colsum);
+                                dy_dtype, M, N, p, dz, dz_dtype, ldz, colsum);
     return launch_dependent(k_cast_columns<unsigned short>, grid, dim3(256), 0, s,
-                            static_cast<const unsigned short *>(dy), dy_dtype, M, N, dz, dz_dtype, ldz,
-                            group_rows(M), colsum);
+                            static_cast<const unsigned short *>(dy), dy_dtype, M, N, p, dz, dz_dtype,
+                            ldz, colsum);
 }
 
 cudaError_t read_wait_error(int *bits, cudaStream_t s) {

@@ -218,8 +218,8 @@ cudaError_t launch_join_columns(const ColumnJob &columns, cudaStream_t s);
 cudaError_t launch_join(const float *part, int splits, int rows, int cols, long long ld, void *to,
                         void *to2, int dtype, const ColumnJob &columns, cudaStream_t s);
 // dz = dy in `dz_dtype` (rows of ldz; null: not wanted) and partial column sums
-// of dy, one row of `colsum` for each of column_groups(M) groups of rows (null: not wanted).
-long long column_groups(long long M);
+// of dy, in column_groups(M, N, dy_dtype) rows of `colsum` (null: not wanted).
+long long column_groups(long long M, int N, int dy_dtype);
 cudaError_t launch_cast_columns(const void *dy, int dy_dtype, long long M, int N, void *dz,
                                 int dz_dtype, long long ldz, float *colsum, cudaStream_t s);
 

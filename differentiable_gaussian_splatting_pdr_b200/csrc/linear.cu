@@ -82,7 +82,7 @@ LinearLayout bwd_layout(int M, int N, int K, int dtype, int grad_dtype, int act)
     L.ldo = L.narrow ? K : padded(K, 2, 16);
     L.pack_out = L.ldo != K;
     if (L.pack_out) L.out = L.take((size_t)M * L.ldo * 2);
-    L.sum_rows = act != PDR_ACT_NONE ? 4 * (((long long)M + 127) / 128) : column_groups(M);
+    L.sum_rows = act != PDR_ACT_NONE ? 4 * (((long long)M + 127) / 128) : column_groups(M, N, grad_dtype);
     L.colsum = L.take((size_t)L.sum_rows * N * 4);
     // dW through fp32 partial results, also where only its rows ask for it
     L.splits = gemm_splits(N, K, 1, M);
