@@ -3,8 +3,8 @@
 // norm (include/pdr.h).
 //
 // One pass over the data: a row's elements stay in the registers of the T
-// threads that share it (16 per thread; T a power of two, so that a shuffle
-// tree, across warps through shared memory, forms its sums).  The forward
+// threads that share it (16 per thread; T a power of two or whole warps, so that a
+// shuffle tree, across warps through shared memory, forms its sums).  The forward
 // normalises the unrounded fp32 sum x + r.  The backward, with
 //   n = s rstd,  p = dy w:   dx = rstd (p - n mean(p n)) + ds,  dw = sum dy n,
 // forms rstd again from the row it reads anyway (nothing is saved), and keeps
@@ -21,10 +21,10 @@ namespace pdr {
 namespace {
 
 constexpr int kPer = 16;              // row elements per thread
-// Blocks of 256 threads per SM (a thread's share of an fp32 row takes twice the
-// registers): 16384 x 333 in fp32 took 15.0 us with two against 18.7 with three, 65536 x 512 in
-// bf16 to 8 bits 41.0 with three against 44.9 with four.
-constexpr int kFwdPerSm = 3, kFwdPerSm32 = 2, kBwdPerSm = 2;
+// Threads per SM (a thread's share of an fp32 row takes twice the registers): 16384 x 333 in
+// fp32 took 15.0 us with 512 against 18.7 with 768, 65536 x 512 in bf16 to 8 bits 41.0
+// with 768 against 44.9 with 1024.
+constexpr int kFwdThreads = 768, kFwdThreads32 = 512, kBwdThreads = 512;
 constexpr float kE4M3Max = 448.0f;    // largest finite e4m3 value
 constexpr float kMinScale = 1.17549435082228751e-38f;  // 2^-126
 
@@ -230,9 +230,11 @@ __device__ __forceinline__ void store_row(void *p, long long row, bool on, const
 }
 
 // Two sums, or a sum and a maximum, over the T threads of a row, for all of them;
-// the whole block calls it.  `red`: one pair per warp.
+// the whole block calls it.  `red`: one pair per warp, of two such places in turn (a place is
+// written again behind the next call's barrier).
 template <bool MAX>
-__device__ __forceinline__ float2 row_reduce(float a, float b, int T, float2 *red) {
+__device__ __forceinline__ float2 row_reduce(float a, float b, int T, float2 *&red,
+                                             int &red_step) {
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1)
         if (d < T) {
@@ -241,8 +243,7 @@ __device__ __forceinline__ float2 row_reduce(float a, float b, int T, float2 *re
             b = MAX ? max_nan(b, ob) : b + ob;
         }
     if (T > 32) {
-        const int warp = threadIdx.x >> 5, first = (threadIdx.x & ~(T - 1)) >> 5;
-        __syncthreads();
+        const int warp = threadIdx.x >> 5, first = T == 64 ? warp & ~1 : 0;  // (wider rows: one a block)
         if ((threadIdx.x & 31) == 0) red[warp] = make_float2(a, b);
         __syncthreads();
         a = red[first].x;
@@ -251,98 +252,109 @@ __device__ __forceinline__ float2 row_reduce(float a, float b, int T, float2 *re
             a += red[first + i].x;
             b = MAX ? max_nan(b, red[first + i].y) : b + red[first + i].y;
         }
+        red += red_step;
+        red_step = -red_step;
     }
     return make_float2(a, b);
 }
-
-// Blocks have 256 threads for rows of at most 4096 elements, 512 or 1024 for wider
-// ones.  The next row is fetched ahead where registers allow it: not for blocks of
-// 1024 threads, nor (`room`) for the two fp32 rows of the backward (60000 x 512:
-// 82 us without, 89 with spilled registers).
-template <int THREADS, bool room>
-constexpr bool kAhead = THREADS < 1024 && room;
 
 template <int E, bool SHIFT>
 __device__ __forceinline__ Row<E, SHIFT> make_row(long long row, long long M, int D, int T) {
     Row<E, SHIFT> q;
     q.D = D;
     q.T = T;
-    q.t = threadIdx.x & (T - 1);
+    q.t = threadIdx.x % T;
     q.shift = SHIFT ? (int)(row * D & (E - 1)) : 0;
     q.total = M * D;
     return q;
 }
 
-template <int E, bool SHIFT, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : E == 4 ? kFwdPerSm32 : kFwdPerSm)
-    k_rms_norm(const NormArgs a) {
-    __shared__ float2 red[32];
-    grid_dep_wait();
+// The rows of a block, AHEAD of them under way: a row's registers are fetched anew as
+// soon as its elements are unpacked (a copy from register to register would wait for
+// the loads).  AHEAD = 0: fetched when they are needed.
+template <int E, bool SHIFT, bool ADD, int AHEAD>
+__device__ __forceinline__ void norm_rows(const NormArgs &a, const Row<E, SHIFT> &q, long long row,
+                                          const float (&w)[kPer], float2 *red) {
+    constexpr int S = AHEAD > 0 ? AHEAD : 1;
     const int T = a.T, per_block = blockDim.x / T;
     const long long step = (long long)gridDim.x * per_block;
-    long long row = (long long)blockIdx.x * per_block + threadIdx.x / T;
-    const Row<E, SHIFT> q = make_row<E, SHIFT>(row, a.M, a.D, T);
-    float w[kPer];
-    if (a.w) load_weight(a.w, a.w_dtype, q, w);
-    Raw<E> x, r, next_x, next_r;
-    if constexpr (kAhead<THREADS, true>) {  // (nothing of rows behind the last)
-        fetch(x, a.x, row, row < a.M, q);
-        if (a.r) fetch(r, a.r, row, row < a.M, q);
-    }
-    for (long long base = (long long)blockIdx.x * per_block; base < a.M; base += step, row += step) {
-        const bool on = row < a.M;
-        if constexpr (kAhead<THREADS, true>) {
-            fetch(next_x, a.x, row + step, row + step < a.M, q);
-            if (a.r) fetch(next_r, a.r, row + step, row + step < a.M, q);
-        } else {
-            fetch(x, a.x, row, on, q);
-            if (a.r) fetch(r, a.r, row, on, q);
-        }
-        float v[kPer];
-        unpack<E>(x, a.dtype, v);
-        if (a.r) {
-            float f[kPer];
-            unpack<E>(r, a.dtype, f);
+    int red_step = 32;
+    Raw<E> x[S], r[ADD ? S : 1];
+    auto fetch_row = [&](int k, long long at) {
+        fetch(x[k], a.x, at, at < a.M, q);
+        if constexpr (ADD) fetch(r[k], a.r, at, at < a.M, q);
+    };
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) v[j] += f[j];
-            if (a.s) store_row(a.s, row, on, q, a.dtype, v);
-        }
-        keep_row(v, q);
-        // y = v w rstd: the sum of v^2 and the largest |v w| in one reduction.
-        float ss = 0.0f, m = 0.0f;
-        if (a.w) {
+    for (int k = 0; k < AHEAD; ++k) fetch_row(k, row + k * step);
+    for (long long base = (long long)blockIdx.x * per_block; base < a.M;) {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                ss = fmaf(v[j], v[j], ss);
-                v[j] *= w[j];
+        for (int k = 0; k < S; ++k, base += step, row += step) {
+            if (k && base >= a.M) break;
+            const bool on = row < a.M;
+            if constexpr (AHEAD == 0) fetch_row(k, row);
+            float v[kPer];
+            unpack<E>(x[k], a.dtype, v);
+            if constexpr (ADD) {
+                float f[kPer];
+                unpack<E>(r[k], a.dtype, f);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) v[j] += f[j];
             }
-        }
-        if (a.scale) {
+            if constexpr (AHEAD > 0) fetch_row(k, row + AHEAD * step);
+            if (ADD && a.s) store_row(a.s, row, on, q, a.dtype, v);
+            keep_row(v, q);
+            // y = v w rstd: the sum of v^2 and the largest |v w| in one reduction.
+            float ss = 0.0f, m = 0.0f;
+            if (a.w) {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) m = max_nan(m, fabsf(v[j]));
-        }
-        const float2 both = row_reduce<true>(ss, m, T, red);
-        float k = a.w ? rsqrtf(fmaf(both.x, a.inv_d, a.eps)) : 1.0f;
-        if (a.scale) {
-            const float scale = max_nan(both.y * k * (1.0f / kE4M3Max), kMinScale);
-            k *= rcp(scale);
-            if (q.t == 0 && on) a.scale[row] = scale;
-        }
+                for (int j = 0; j < kPer; ++j) {
+                    ss = fmaf(v[j], v[j], ss);
+                    v[j] *= w[j];
+                }
+            }
+            if (a.scale) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) v[j] *= k;
-        store_row(a.y, row, on, q, a.y_dtype, v);
-        if constexpr (kAhead<THREADS, true>) {
-            x = next_x;
-            r = next_r;
+                for (int j = 0; j < kPer; ++j) m = max_nan(m, fabsf(v[j]));
+            }
+            const float2 both = row_reduce<true>(ss, m, T, red, red_step);
+            float k1 = a.w ? rsqrtf(fmaf(both.x, a.inv_d, a.eps)) : 1.0f;
+            if (a.scale) {
+                const float scale = max_nan(both.y * k1 * (1.0f / kE4M3Max), kMinScale);
+                k1 *= rcp(scale);
+                if (q.t == 0 && on) a.scale[row] = scale;
+            }
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) v[j] *= k1;
+            store_row(a.y, row, on, q, a.y_dtype, v);
         }
     }
 }
 
 template <int E, bool SHIFT, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : kBwdPerSm)
+__global__ void __launch_bounds__(THREADS, 1) k_rms_norm(const NormArgs a) {
+    __shared__ float2 red[2 * 32];
+    grid_dep_wait();
+    const long long row = (long long)blockIdx.x * (blockDim.x / a.T) + threadIdx.x / a.T;
+    const Row<E, SHIFT> q = make_row<E, SHIFT>(row, a.M, a.D, a.T);
+    float w[kPer];
+    if (a.w) load_weight(a.w, a.w_dtype, q, w);
+    // Two 16-bit rows, or one fp32 row (16384 x 333: 12.4 us, two 13.7) or one and what is
+    // added (65536 x 512 to 8 bits: 40.9 us, two of both 44.1 with spilled registers).  Blocks of 1024 threads have none
+    // to spare.
+    constexpr int some = THREADS < 1024;
+    if (a.r)
+        norm_rows<E, SHIFT, true, some>(a, q, row, w, red);
+    else
+        norm_rows<E, SHIFT, false, some * (E == 8 ? 2 : 1)>(a, q, row, w, red);
+}
+
+template <int E, bool SHIFT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1)
     k_rms_norm_bwd(const NormBwdArgs a) {
     extern __shared__ float part[];  // [rows of a block][D] when there are several
-    __shared__ float2 red[32];
+    __shared__ float2 reds[2][32];
+    float2 *red = reds[0];
+    int red_step = 32;
     grid_dep_wait();
     const int T = a.T, per_block = blockDim.x / T;
     const long long step = (long long)gridDim.x * per_block;
@@ -352,24 +364,32 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : kBwdPerSm)
     load_weight(a.w, a.w_dtype, q, w);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) dw[j] = 0.0f;
+    // The next row is fetched ahead: to other registers (`ahead`), or fp32 rows, which have
+    // none to spare, to the same ones when they are unpacked (25620 x 776 62 us, in time for
+    // their use 69).  Blocks of 1024 threads have registers for neither.
+    constexpr bool ahead = THREADS < 1024 && E == 8, again = THREADS < 1024 && E == 4;
     Raw<E> s, dy, ds, next_s, next_dy;
-    if constexpr (kAhead<THREADS, E == 8>) {
+    if constexpr (ahead || again) {
         fetch(s, a.s, row, row < a.M, q);
         fetch(dy, a.dy, row, row < a.M, q);
     }
     for (long long base = (long long)blockIdx.x * per_block; base < a.M; base += step, row += step) {
         const bool on = row < a.M;
-        if constexpr (kAhead<THREADS, E == 8>) {
+        if constexpr (ahead) {
             if (a.ds) fetch(ds, a.ds, row, on, q);  // needed last
             fetch(next_s, a.s, row + step, row + step < a.M, q);
             fetch(next_dy, a.dy, row + step, row + step < a.M, q);
-        } else {
+        } else if constexpr (!again) {
             fetch(s, a.s, row, on, q);
             fetch(dy, a.dy, row, on, q);
         }
         float v[kPer], g[kPer];
         unpack<E>(s, a.dtype, v);
         unpack<E>(dy, a.dtype, g);
+        if constexpr (again) {
+            fetch(s, a.s, row + step, row + step < a.M, q);
+            fetch(dy, a.dy, row + step, row + step < a.M, q);
+        }
         keep_row(v, q);
         keep_row(g, q);
         // With p = dy w: sum v^2 and sum p v in one reduction; n = v rstd.
@@ -379,7 +399,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : kBwdPerSm)
             ss = fmaf(v[j], v[j], ss);
             pv = fmaf(g[j] * w[j], v[j], pv);
         }
-        const float2 sums = row_reduce<false>(ss, pv, T, red);
+        const float2 sums = row_reduce<false>(ss, pv, T, red, red_step);
         const float rstd = rsqrtf(fmaf(sums.x, a.inv_d, a.eps));
         const float dot = rstd * rstd * sums.y * a.inv_d;  // mean(p n) / |v|_rms
 #pragma unroll
@@ -388,13 +408,13 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : kBwdPerSm)
             g[j] = rstd * fmaf(-v[j], dot, g[j] * w[j]);
         }
         if (a.ds) {
-            if constexpr (!kAhead<THREADS, E == 8>) fetch(ds, a.ds, row, on, q);
+            if constexpr (!ahead) fetch(ds, a.ds, row, on, q);
             unpack<E>(ds, a.dtype, v);
 #pragma unroll
             for (int j = 0; j < kPer; ++j) g[j] += v[j];
         }
         if (a.dx) store_row(a.dx, row, on, q, a.dtype, g);
-        if constexpr (kAhead<THREADS, E == 8>) {
+        if constexpr (ahead) {
             s = next_s;
             dy = next_dy;
         }
@@ -421,20 +441,25 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 1 : kBwdPerSm)
 bool half_type(int t) { return t == PDR_F16 || t == PDR_BF16; }
 bool float_type(int t) { return t == PDR_F32 || half_type(t); }
 
-// Threads per row, block size and blocks for M rows of D elements.
+// Threads per row, block size and blocks for M rows of D elements.  Rows of more than
+// 1024 elements have a block each, as many blocks as `per_sm` threads an SM make
+// (with powers of two for T and blocks of 256, 512 or 1024 threads 73416 x 1152 to 8 bits took
+// 104 us against 76, 17708 x 4170 189 against 112, the backward of 30114 x 2304 144 against 109).
 struct NormShape {
     bool shift;
     int T, threads, blocks;
 };
-NormShape norm_shape(long long M, int D, int bytes, int per_sm) {  // per_sm: blocks of 256 threads
+NormShape norm_shape(long long M, int D, int bytes, int per_sm) {
     NormShape n;
     const int E = 16 / bytes;
     n.shift = D % E != 0;
     n.T = 1;
-    while (n.T * kPer < D + (n.shift ? E - 1 : 0)) n.T *= 2;
-    n.threads = n.T > 256 ? n.T : 256;
+    const int share = (D + (n.shift ? E - 1 : 0) + kPer - 1) / kPer;
+    while (n.T < share && n.T < 64) n.T *= 2;
+    if (share > 64) n.T = (share + 31) / 32 * 32;
+    n.threads = n.T > 64 ? n.T : 256;
     const long long per_block = n.threads / n.T, need = (M + per_block - 1) / per_block;
-    long long most = n.threads > 256 ? kSMs : kSMs * per_sm;
+    long long most = kSMs * (per_sm > n.threads ? per_sm / n.threads : 1);
     if (n.shift && need > most && per_block < 8)  // a thread's rows 8 apart
         most = most * per_block / 8 * 8 / per_block;
     n.blocks = (int)(need < most ? need : most);
@@ -451,17 +476,19 @@ auto norm_kernel() {
 template <bool BWD, typename Args>
 cudaError_t launch_norm(const NormShape &n, const Args &a, size_t smem, cudaStream_t s) {
     using Kernel = void (*)(Args);
-    static const Kernel kernels[2][2][3] = {
-        {{norm_kernel<BWD, 8, false, 256>(), norm_kernel<BWD, 8, false, 512>(), norm_kernel<BWD, 8, false, 1024>()},
-         {norm_kernel<BWD, 8, true, 256>(), norm_kernel<BWD, 8, true, 512>(), norm_kernel<BWD, 8, true, 1024>()}},
-        {{norm_kernel<BWD, 4, false, 256>(), norm_kernel<BWD, 4, false, 512>(), norm_kernel<BWD, 4, false, 1024>()},
-         {norm_kernel<BWD, 4, true, 256>(), norm_kernel<BWD, 4, true, 512>(), norm_kernel<BWD, 4, true, 1024>()}}};
-    return launch_dependent(kernels[a.dtype == PDR_F32][n.shift][n.threads / 512], dim3((unsigned)n.blocks),
+    constexpr int most = BWD ? kBwdThreads : kFwdThreads, most32 = BWD ? kBwdThreads : kFwdThreads32;
+    static const Kernel kernels[2][2][2] = {
+        {{norm_kernel<BWD, 8, false, most>(), norm_kernel<BWD, 8, false, 1024>()},
+         {norm_kernel<BWD, 8, true, most>(), norm_kernel<BWD, 8, true, 1024>()}},
+        {{norm_kernel<BWD, 4, false, most32>(), norm_kernel<BWD, 4, false, 1024>()},
+         {norm_kernel<BWD, 4, true, most32>(), norm_kernel<BWD, 4, true, 1024>()}}};
+    const bool f32 = a.dtype == PDR_F32;
+    return launch_dependent(kernels[f32][n.shift][n.threads > (f32 ? most32 : most)], dim3((unsigned)n.blocks),
                             dim3((unsigned)n.threads), smem, s, a);
 }
 
 pdr_status run_fwd(NormArgs a, cudaStream_t s) {
-    const NormShape n = norm_shape(a.M, a.D, dtype_bytes(a.dtype), a.dtype == PDR_F32 ? kFwdPerSm32 : kFwdPerSm);
+    const NormShape n = norm_shape(a.M, a.D, dtype_bytes(a.dtype), a.dtype == PDR_F32 ? kFwdThreads32 : kFwdThreads);
     a.T = n.T;
     return launch_norm<false>(n, a, 0, s) == cudaSuccess ? PDR_OK : PDR_ERR_CUDA;
 }
@@ -508,7 +535,7 @@ pdr_status pdr_quantize_rows(const void *x, int dtype, int M, int D, void *y, fl
 size_t pdr_rms_norm_bwd_workspace_bytes(int M, int D) {
     if (!norm_sizes(M, D) || !norm_in_limits(M, D)) return 0;
     // (for the type that takes more blocks)
-    const int a = norm_shape(M, D, 2, kBwdPerSm).blocks, b = norm_shape(M, D, 4, kBwdPerSm).blocks;
+    const int a = norm_shape(M, D, 2, kBwdThreads).blocks, b = norm_shape(M, D, 4, kBwdThreads).blocks;
     return align256((size_t)(a > b ? a : b) * D * 4);
 }
 
@@ -535,7 +562,7 @@ pdr_status pdr_rms_norm_bwd(const void *grad, const void *sum, int dtype, const 
         return err == cudaSuccess ? PDR_OK : PDR_ERR_CUDA;
     }
     if (!grad_x && !grad_weight) return PDR_OK;
-    const NormShape n = norm_shape(M, D, dtype_bytes(dtype), kBwdPerSm);
+    const NormShape n = norm_shape(M, D, dtype_bytes(dtype), kBwdThreads);
     const NormBwdArgs a = {grad, sum, weight, grad_sum, grad_x,
                            grad_weight ? static_cast<float *>(workspace) : nullptr,
                            dtype, weight_dtype, eps, 1.0f / D, M, D, n.T};
