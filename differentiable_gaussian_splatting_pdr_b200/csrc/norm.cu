@@ -494,7 +494,11 @@ pdr_status run_fwd(NormArgs a, cudaStream_t s) {
 }
 
 bool norm_sizes(int M, int D) { return M >= 0 && D >= 1; }
-bool norm_in_limits(int M, int D) { return M <= PDR_MAX_ROWS && D <= PDR_MAX_NORM_FEATURES; }
+// (The vectors of a shifted row take up to E - 1 elements more, and 1024 threads 16 each.)
+bool norm_in_limits(int M, int D, int bytes) {
+    const int E = 16 / bytes;
+    return M <= PDR_MAX_ROWS && D <= PDR_MAX_NORM_FEATURES - (D % E ? E - 1 : 0);
+}
 
 }  // namespace
 }  // namespace pdr
@@ -509,7 +513,7 @@ pdr_status pdr_rms_norm_fwd(const void *x, const void *residual, int dtype, cons
     if (!norm_sizes(M, D) || !float_type(dtype) || !(weight_dtype == dtype || weight_dtype == PDR_F32) ||
         !(y_dtype == dtype || y_dtype == PDR_E4M3) || !(eps >= 0.0f))
         return PDR_ERR_INVALID_ARG;
-    if (!norm_in_limits(M, D)) return PDR_ERR_TOO_LARGE;
+    if (!norm_in_limits(M, D, dtype_bytes(dtype))) return PDR_ERR_TOO_LARGE;
     if (!weight || (M > 0 && (!x || !y)) || (M > 0 && (y_dtype == PDR_E4M3) != (y_scale != nullptr)) ||
         (!residual && sum))
         return PDR_ERR_INVALID_ARG;
@@ -524,7 +528,7 @@ pdr_status pdr_rms_norm_fwd(const void *x, const void *residual, int dtype, cons
 pdr_status pdr_quantize_rows(const void *x, int dtype, int M, int D, void *y, float *y_scale,
                              void *stream) {
     if (!norm_sizes(M, D) || !float_type(dtype)) return PDR_ERR_INVALID_ARG;
-    if (!norm_in_limits(M, D)) return PDR_ERR_TOO_LARGE;
+    if (!norm_in_limits(M, D, dtype_bytes(dtype))) return PDR_ERR_TOO_LARGE;
     if (M > 0 && (!x || !y || !y_scale)) return PDR_ERR_INVALID_ARG;
     if (!aligned_to(x, 16) || !aligned_to(y, 16) || !aligned_to(y_scale, 4)) return PDR_ERR_INVALID_ARG;
     if (M == 0) return PDR_OK;
@@ -533,7 +537,7 @@ pdr_status pdr_quantize_rows(const void *x, int dtype, int M, int D, void *y, fl
 }
 
 size_t pdr_rms_norm_bwd_workspace_bytes(int M, int D) {
-    if (!norm_sizes(M, D) || !norm_in_limits(M, D)) return 0;
+    if (!norm_sizes(M, D) || !norm_in_limits(M, D, 4)) return 0;
     // (for the type that takes more blocks)
     const int a = norm_shape(M, D, 2, kBwdThreads).blocks, b = norm_shape(M, D, 4, kBwdThreads).blocks;
     return align256((size_t)(a > b ? a : b) * D * 4);
@@ -546,7 +550,7 @@ pdr_status pdr_rms_norm_bwd(const void *grad, const void *sum, int dtype, const 
     if (!norm_sizes(M, D) || !float_type(dtype) || !(weight_dtype == dtype || weight_dtype == PDR_F32) ||
         !(eps >= 0.0f))
         return PDR_ERR_INVALID_ARG;
-    if (!norm_in_limits(M, D)) return PDR_ERR_TOO_LARGE;
+    if (!norm_in_limits(M, D, dtype_bytes(dtype))) return PDR_ERR_TOO_LARGE;
     if (!weight || (M > 0 && (!grad || !sum))) return PDR_ERR_INVALID_ARG;
     const int we = dtype_bytes(weight_dtype);
     if (!aligned_to(grad, 16) || !aligned_to(sum, 16) || !aligned_to(grad_sum, 16) ||

@@ -322,7 +322,9 @@ typedef enum {
 
 #define PDR_MAX_ROWS (1 << 30)
 #define PDR_MAX_FEATURES 65536       /* N, K, D and F of the products */
-#define PDR_MAX_NORM_FEATURES 16384  /* D of rms_norm and quantize_rows */
+/* D of rms_norm and quantize_rows; for rows that are no multiple of 16 bytes 7 (of
+ * 16-bit types) or 3 (PDR_F32) less */
+#define PDR_MAX_NORM_FEATURES 16384
 
 /* x [M][K], weight [N][K] of `dtype`; bias [N] of bias_dtype (PDR_F32, PDR_F16
  * or PDR_BF16) or NULL; residual [M][N] of y_dtype or NULL; y [M][N] of y_dtype

@@ -161,3 +161,18 @@ def test_package_exports():
     for name in ["linear", "linear_fwd", "linear_bwd", "gated", "gated_fwd", "gated_bwd", "rms_norm",
                  "rms_norm_fwd", "rms_norm_bwd", "quantize_rows", "adapter", "AdapterWeights", "check_wait_error"]:
         assert getattr(pkg, name) is getattr(F, name)
+
+
+@no_gpu
+def test_norm_refuses_the_widest_rows_that_start_inside_a_vector(lib):
+    """1024 threads hold 16384 elements, of which a row that is no multiple of 16
+    bytes cannot use the last ones."""
+    def fwd(D, t, yt, sc):
+        return lib.pdr_rms_norm_fwd(P, None, t, P, t, 1e-6, 4, D, None, P, yt, sc, None)
+
+    for t, first in ((BF16, 16378), (F32, 16382)):
+        for D in range(first, 16384):
+            if D % (4 if t == F32 else 8) == 0:
+                continue
+            assert fwd(D, t, t, None) == LARGE and lib.pdr_quantize_rows(P, t, 4, D, P, P, None) == LARGE
+            assert lib.pdr_rms_norm_bwd(P, P, t, P, t, None, 1e-6, 4, D, P, P, P, 1 << 40, None) == LARGE
