@@ -789,3 +789,48 @@ def test_given_workspaces_hold_nothing_between_calls():
                                  *(t.data_ptr() for t in d), ws.data_ptr(), ws.numel(), stream) == 0
         for a, e in zip(d, want):
             assert torch.equal(a, e)
+
+
+# Rows shared by one to 32 warps, and more rows than the machine has blocks for.
+WIDE_SHAPES = [(2500, 1032), (2500, 1152), (2401, 1409), (1300, 2304), (700, 4170), (500, 6464), (333, 8191), (300, 12296),
+               (160, 12289), (300, 16377)]
+
+
+@pytest.mark.parametrize("M,D", WIDE_SHAPES)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rms_norm_of_wide_rows(M, D, dtype):
+    test_rms_norm(M, D, dtype, dtype, M % 2 == 0)
+    test_rms_norm_gradients(M, D, dtype, dtype, M % 2 == 1)
+
+
+@pytest.mark.parametrize("D", [16381, 16384])
+def test_rms_norm_of_the_widest_fp32_rows(D):
+    test_rms_norm(160, D, F32, F32, True)
+    test_rms_norm_gradients(160, D, F32, F32, True)
+
+
+@pytest.mark.parametrize("M,N", [(40000, 600), (12000, 1800), (40000, 130), (9000, 4000), (70000, 256)])
+def test_linear_of_many_rows_of_tiles(M, N):
+    """Columns of tiles that divide the machine evenly, or leave pairs over."""
+    rng = np.random.default_rng(N)
+    x, w, b = rand(rng, (M, 72), BF16), rand(rng, (N, 72), BF16, 0.2), rand(rng, (N,), F32)
+    X, W, B = f64(x), f64(w), f64(b)
+    want = O.linear(X, W, B)
+    close(F.linear_fwd(x, w, b, out_dtype=F32), want, z_error(X, W, B) + STEP * np.abs(want), F32, "y")
+
+
+@pytest.mark.parametrize("M,N", [(20000, 700), (9000, 2056)])
+def test_gated_of_many_rows_of_tiles(M, N):
+    rng = np.random.default_rng(N)
+    x, g, u = rand(rng, (M, 64), BF16), rand(rng, (N, 64), BF16, 0.2), rand(rng, (N, 64), BF16, 0.2)
+    X, G, Up = f64(x), f64(g), f64(u)
+    eg, eu = z_error(X, G, None) + 4 * STEP * np.abs(X @ G.T), z_error(X, Up, None) + 4 * STEP * np.abs(X @ Up.T)
+    a, z = O.act(X @ G.T, "silu")[0], X @ Up.T
+    h = F.gated_fwd(x, g, u, out_dtype=F32)
+    close(h, a * z, value_error(X @ G.T, eg, "silu") * (np.abs(z) + eu) + np.abs(a) * eu + STEP * np.abs(a * z), F32, "h")
+
+
+@pytest.mark.parametrize("N", [1, 6, 8, 45, 256, 300, 777, 2050])
+@pytest.mark.parametrize("grad_dtype", [F32, BF16])
+def test_bias_sums_of_any_width(N, grad_dtype):
+    check_linear_bwd(5003, 40, N, BF16, grad_dtype, "none")
