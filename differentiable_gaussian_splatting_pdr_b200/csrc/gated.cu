@@ -10,8 +10,10 @@
 //   dg = dh u act'(g),   du = dh act(g),
 // rounded to x's type as operands of the three products that follow:
 //   dx = dg Wg + du Wu          one product, k running over both sources;
-//   dWg = dg^T x, dWu = du^T x  one launch, k split over the machine, fp32
+//   dWg = dg^T x, dWu = du^T x  in the same launch, k split over the machine, fp32
 //                               partial results added in order.
+// 65536 x 256 to 1024 in bf16: 61 us (74 under the power cap that a long run meets; 1120 and
+// 929 TFLOP/s); the backward of 16384 rows 69 us.
 #include "gemm.cuh"
 
 namespace pdr {

@@ -15,7 +15,9 @@
 //            into one of the accumulators there (2 of 256 columns, 4 of fewer);
 //   warps 4..19 take finished accumulators to registers and run the
 //            epilogue, while the next tile's products run.
-// What the four epilogues compute is in gemm.cuh (GemmEpi).
+// What the four epilogues compute is in gemm.cuh (GemmEpi).  524288 x 256 to 8 columns: 50 us,
+// 6.1 TB/s; 4096 x 4096 x 4096 in bf16: 106 us, 1300 TFLOP/s, bound by the operands' way
+// from L2.
 #include <stdint.h>
 
 #include <atomic>

@@ -11,10 +11,10 @@
 //       forward: at widths up to about 1000 forming z again costs less time
 //       than writing and reading it, and no memory);
 //   db  sums of dy act'(z) in fp32 before any rounding: per 32-row group in
-//       the epilogue (or per 512 rows of dy), then over the groups in order;
+//       the epilogue (or per block that reads dy), then over the groups in order;
 //   dx  = dz W     (W read with its k as rows: an MN-major operand);
 //   dW  = dz^T x   (both operands MN-major), k split over the machine, fp32
-//       partial results added in order: bitwise reproducible.
+//       partial results added in order: bitwise reproducible.  In one launch with dx.
 // dz is rounded to x's type: it is an operand of 16-bit products, whose
 // results are rounded to that type too.
 #include "gemm.cuh"
