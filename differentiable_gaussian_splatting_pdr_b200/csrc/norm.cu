@@ -328,8 +328,12 @@ __device__ __forceinline__ void norm_rows(const NormArgs &a, const Row<E, SHIFT>
             float k1 = a.w ? rsqrtf(fmaf(both.x, a.inv_d, a.eps)) : 1.0f;
             if (a.scale) {
                 const float scale = max_nan(both.y * k1 * (1.0f / kE4M3Max), kMinScale);
-                k1 *= rcp(scale);
                 if (q.t == 0 && on) a.scale[row] = scale;
+                // One factor after the other: |v k1| <= 448 scale, while rstd / scale of a row of
+                // zeros (1000 x 2^126) is beyond fp32, and 0 times that no zero.
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) v[j] *= k1;
+                k1 = rcp(scale);
             }
 #pragma unroll
             for (int j = 0; j < kPer; ++j) v[j] *= k1;

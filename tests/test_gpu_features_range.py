@@ -1,0 +1,155 @@
+"""linear, gated and rms_norm at the ends of their values' range, and over several
+tiles a pair of SMs: against the formulas in fp64 on the GPU, element by element.
+
+Tolerances, derived before the first run; u(t) is half a step of type t, relative to
+the value (fp32 2^-24, fp16 2^-11, bf16 2^-8, e4m3 2^-4).
+  sums      n additions, each off by at most a whole fp32 step: (n + 4) 2^-23 sum |a||b|.
+  acts      |slope|, |curvature| <= 1.13; the evaluation adds 2^-18 |value| + 1.5e-7 |z| to the
+            value and 2^-18 (1 + |z|) to the slope (the tails have tests of their own).
+  dz, dg, du are rounded to x's type: u(t) of their size.  fp16 has half a step of 2^-25 below
+            its normal range; the power of two that is taken out before brings the largest value
+            that can occur, B, to 2^14 at least, so that this is 2^-39 B.  B is
+            max |dy| for dz, and max |dh| D max |x| max |w| for dg and du.
+  outputs   rounded once: u(t) of the value (fp16: 2^-25 at least).
+"""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from differentiable_gaussian_splatting_pdr_b200 import build as pdr_build  # noqa: E402
+from differentiable_gaussian_splatting_pdr_b200 import features as F  # noqa: E402
+
+BF16, F16, F32, E4M3 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
+U = {F32: 2.0 ** -24, F16: 2.0 ** -11, BF16: 2.0 ** -8}
+TINY = {F32: 2.0 ** -150, F16: 2.0 ** -25, BF16: 2.0 ** -134}
+STEP, EVAL = 2.0 ** -23, 2.0 ** -18
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    pdr_build.build()
+    yield
+    torch.cuda.synchronize()
+    F.check_wait_error()
+
+
+def generator(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def rand(gen, shape, dtype, scale=1.0):
+    return (scale * torch.randn(shape, generator=gen, device="cuda", dtype=torch.float64)).to(dtype)
+
+
+def f64(t):
+    return None if t is None else t.detach().double()
+
+
+def close(got, want, tol, dtype, what=""):
+    got = f64(got)
+    assert got.shape == want.shape, what
+    assert torch.isfinite(want).all()
+    limit = tol * (1 + U[dtype]) + U[dtype] * want.abs() + TINY[dtype]
+    bad = ~((got - want).abs() <= limit)
+    assert not bad.any(), (what, int(bad.sum()), bad.nonzero()[:3].tolist(), float((got - want)[bad].abs().max()),
+                           float(limit[bad].min()))
+
+
+def act(z, kind):
+    """(value, slope) in fp64; the tail of the normal distribution without cancellation."""
+    if kind == "none":
+        return z, torch.ones_like(z)
+    if kind == "relu":
+        return z.clamp_min(0), (z > 0).double()
+    if kind == "silu":
+        t = torch.special.expit(z)
+        return z * t, t * (1 + z * torch.special.expit(-z))
+    if kind == "gelu":
+        p = 0.5 * torch.special.erfc(-z / math.sqrt(2.0))
+        return z * p, p + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    c = math.sqrt(2 / math.pi)
+    t = torch.special.expit(2 * c * (z + 0.044715 * z ** 3))
+    return z * t, t + 2 * z * t * (1 - t) * c * (1 + 3 * 0.044715 * z * z)
+
+
+def z_error(x, w, b):
+    return (x.shape[-1] + 6) * STEP * (x.abs() @ w.abs().t() + (0 if b is None else b.abs()))
+
+
+def value_error(z, dz, kind):
+    return dz if kind == "none" else 1.13 * dz + EVAL * act(z, kind)[0].abs() + 1.5e-7 * z.abs()
+
+
+def slope_error(z, dz, kind):
+    if kind == "none":
+        return torch.zeros_like(z)
+    if kind == "relu":
+        return (z.abs() <= dz).double()
+    return 1.13 * dz + EVAL * (1 + z.abs())
+
+
+# ---- rows of zeros and rows near the smallest numbers -----------------------------
+
+
+@pytest.mark.parametrize("dtype,wt", [(F32, F32), (BF16, BF16), (F16, F16), (F16, F32)])
+@pytest.mark.parametrize("D", [1, 8, 64, 333, 512, 4096, 12296])
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_rms_norm_to_8_bits_of_zero_rows(D, dtype, wt, with_residual):
+    gen = generator(D)
+    M = 21
+    zero = [0, 7, 8, M - 1]
+    x, w = rand(gen, (M, D), dtype, 2.0), 1 + 0.1 * rand(gen, (D,), wt).abs()
+    x[zero] = 0
+    r = None
+    if with_residual:
+        r = rand(gen, (M, D), dtype)
+        x[8] = -r[8]  # a sum of zero
+        r[[0, 7, M - 1]] = 0
+    q, s, scale = F.rms_norm_fwd(x, w, r, out_dtype=E4M3)
+    q = q.float()
+    assert torch.isfinite(q).all() and torch.isfinite(scale).all()
+    assert not q[zero].any() and (scale[zero] == 2.0 ** -126).all()
+    rest = [m for m in range(M) if m not in zero]
+    y = F.rms_norm_fwd(x, w, r)[0]
+    # the 8-bit rows are those of the norm in the rows' own type
+    assert ((q * scale[:, None] - y.float()).abs()[rest] <= (2.0 ** -4 + 2 * U[dtype] + 1e-5) * y[rest].float().abs()
+            + 2.0 ** -9 * scale[rest, None]).all()
+    q, _, scale = F.rms_norm_fwd(rand(gen, (M, D), dtype, 0.01), torch.zeros_like(w), r, out_dtype=E4M3)
+    assert not q.float().any() and (scale == 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-34, 1e-36, 1e-37, 1e-38])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [64, 333])
+def test_rms_norm_to_8_bits_of_tiny_rows(D, dtype, size):
+    """1 / scale alone is near the largest number here; rstd is 1000."""
+    gen = generator(D)
+    x, w = rand(gen, (10, D), dtype, size), 1 + 0.1 * rand(gen, (D,), F32)
+    q, _, scale = F.rms_norm_fwd(x, w, out_dtype=E4M3)
+    X, W = f64(x), f64(w)
+    want = X / (X.square().mean(-1, keepdim=True) + 1e-6).sqrt() * W
+    ws = (want.abs().amax(-1) / 448).clamp_min(2.0 ** -126)
+    # products of tiny numbers are off by half of the smallest one, 2^-150, times rstd
+    assert ((f64(scale) - ws).abs() <= 32 * STEP * ws + 1000 * 2.0 ** -149).all()
+    err = (f64(q.float()) * f64(scale)[:, None] - want).abs()
+    assert (err <= (2.0 ** -4 + 1e-5) * want.abs() + 2.0 ** -10 * 1.001 * f64(scale)[:, None] + 1000 * 2.0 ** -149).all()
+
+
+def test_adapter_in_8_bits_with_a_row_of_zeros():
+    """A padded token: its parameters are those that the formulas give for zeros, the others stay."""
+    gen = generator(3)
+    B, N, D, Fw, P = 2, 40, 64, 96, 8
+    w = F.AdapterWeights(1 + 0.1 * rand(gen, (D,), BF16), rand(gen, (Fw, D), BF16, D ** -0.5), rand(gen, (Fw, D), BF16, D ** -0.5),
+                         rand(gen, (D, Fw), BF16, 0.3 * Fw ** -0.5), 1 + 0.1 * rand(gen, (D,), BF16),
+                         rand(gen, (P, D), BF16, 0.2 * D ** -0.5), rand(gen, (P,), F32, 0.1)).quantized()
+    f, base = rand(gen, (B, N, D), BF16), rand(gen, (B, N, P), F32)
+    whole = F.adapter(f, w, base)
+    f[:, 30:] = 0
+    y = F.adapter(f, w, base)
+    assert torch.equal(y[:, :30], whole[:, :30])
+    assert torch.equal(y[:, 30:], (w.head_bias + base)[:, 30:])
