@@ -412,7 +412,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             pv = fmaf(g[j] * w[j], v[j], pv);
         }
         const float2 sums = row_reduce<false>(ss, pv, T, red, red_step);
-        const float rstd = rsqrtf(fmaf(sums.x, a.inv_d, a.eps));
+        // (Behind the last row the norm is eps alone; with eps = 0 infinity times 0 would reach dw.)
+        const float rstd = on ? rsqrtf(fmaf(sums.x, a.inv_d, a.eps)) : 0.0f;
         const float dot = rstd * rstd * sums.y * a.inv_d;  // mean(p n) / |v|_rms
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {

@@ -153,3 +153,24 @@ def test_adapter_in_8_bits_with_a_row_of_zeros():
     y = F.adapter(f, w, base)
     assert torch.equal(y[:, :30], whole[:, :30])
     assert torch.equal(y[:, 30:], (w.head_bias + base)[:, 30:])
+
+
+@pytest.mark.parametrize("dtype,wt", [(F32, F32), (BF16, BF16), (F16, F32)])
+@pytest.mark.parametrize("M", [1, 5, 33, 601])
+@pytest.mark.parametrize("D", [1, 8, 64, 333, 512, 777, 1024, 4170])
+def test_rms_norm_gradients_without_eps(M, D, dtype, wt):
+    """eps = 0: threads behind the last row have a norm of zero there and add nothing."""
+    gen = generator(M + D)
+    s, w, g = rand(gen, (M, D), dtype, 2.0), rand(gen, (D,), wt), rand(gen, (M, D), dtype)
+    s = torch.where(s == 0, torch.ones_like(s), s)
+    gs = rand(gen, (M, D), dtype) if M % 2 else None
+    dx, dw = F.rms_norm_bwd(g, s, w, gs, eps=0.0)
+    S, W, G = f64(s), f64(w), f64(g)
+    m = S.square().mean(-1, keepdim=True).sqrt()
+    p = G * W
+    wx = p / m - S * (p * S).mean(-1, keepdim=True) / m ** 3 + (0 if gs is None else f64(gs))
+    size = p.abs() / m + S.abs() * (p * S).abs().mean(-1, keepdim=True) / m ** 3
+    close(dx, wx, (D + 40) * STEP * size + STEP * wx.abs(), dtype, "dx")
+    close(dw, (G * S / m).sum(0), (D / 2 + M + 40) * STEP * ((G * S).abs() / m).sum(0), wt, "dw")
+    y = F.rms_norm_fwd(s, w, eps=0.0)[0]
+    close(y, S / m * W, (D / 2 + 16) * STEP * (S / m * W).abs(), dtype, "y")
