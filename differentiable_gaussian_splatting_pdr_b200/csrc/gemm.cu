@@ -87,6 +87,7 @@ struct __align__(64) GemmParams {
     int in_dtype;
     long long ldi;
     float *colsum;
+    Bound bound;
 };
 
 // One product, or two that run one behind the other in the same launch: tiles of the
@@ -469,7 +470,7 @@ __device__ __forceinline__ void load_b(const GemmParams &p, const Tile &t, int k
 template <int EPI, int ACT>
 __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t, unsigned acc,
                                               unsigned ready, unsigned phase, int c0, int c1,
-                                              int quarter, float *columns, int &have_n,
+                                              int quarter, float *columns, int &have_n, float factor,
                                               Staging &staging, int *abort, unsigned release) {
     constexpr bool kTwo = EPI == kEpiGated || EPI == kEpiGatedBwd;  // g and u
     constexpr int C = EPI == kEpiGated ? 32 : 16;                   // columns at once
@@ -528,6 +529,15 @@ __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t
         if (has_in) {
             unpack_row(p.in_dtype, raw, x);
             if (c + C < c1) fetch(c + C);
+        }
+        if (p.bound.part) {  // (a slope's or gated result has its input as a factor)
+            if constexpr (EPI == kEpiLinear) {
+#pragma unroll
+                for (int i = 0; i < C; ++i) v[i] *= factor;
+            } else {
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) x[i] *= factor;
+            }
         }
         const float4 *column = reinterpret_cast<const float4 *>(columns + c - c0);
         if (p.fp8) {
@@ -605,8 +615,8 @@ __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t
 #pragma unroll
                 for (int i = 0; i < C; ++i) v[i] = on ? v[i] : 0.0f;  // rows outside count nothing
                 const float s = column_sums(v);
-                if (lane < kChunk && c + lane < c1)
-                    p.colsum[((long long)t.m * 4 + quarter) * p.N + n0 + c + lane] = s;
+                if (lane < kChunk && c + lane < c1)  // (1 / factor: a power of two)
+                    p.colsum[((long long)t.m * 4 + quarter) * p.N + n0 + c + lane] = p.bound.part ? s / factor : s;
             }
     }
     if (!any && lane == 0) bar_arrive_at(release);
@@ -619,7 +629,7 @@ __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t
 template <int ACT>
 __device__ __forceinline__ bool epilogue_narrow(const GemmParams &p, const Tile &t, unsigned acc,
                                                 unsigned ready, unsigned phase, int quarter,
-                                                float *columns, int &have_n, float *buffer,
+                                                float *columns, int &have_n, float factor, float *buffer,
                                                 int *abort, unsigned release) {
     const int lane = threadIdx.x & 31, N = p.N;
     const int row0 = t.m * kBM + 32 * quarter, rows = max(0, min(32, p.M - row0));
@@ -659,6 +669,9 @@ __device__ __forceinline__ bool epilogue_narrow(const GemmParams &p, const Tile 
     if (p.fp8) {
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) v[i] *= scale_m * columns[kMaxCols + i];
+    } else if (p.bound.part) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) v[i] *= factor;
     }
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) v[i] += columns[i];
@@ -739,6 +752,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int cols = p.bcols / p.sharing, cfirst = group % p.sharing * cols;
         const int sets = kGroups / p.sharing, set = group / p.sharing;
         const unsigned release = at_rank(acc_empty, 0);
+        const float factor = EPI != kEpiGated && p.bound.part ? bound_factor(p.bound, EPI == kEpiLinear) : 1.0f;
         int acc = 0, it = 0;
         unsigned acc_phase = 0;
         bool ok = true;
@@ -753,12 +767,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const unsigned d = tmem + ((unsigned)(32 * quarter) << 16) + acc * p.bn;
                     if constexpr (NARROW)
                         ok = epilogue_narrow<ACT>(p, tile, d, acc_full + 8 * acc, acc_phase, quarter,
-                                                  columns, have_n, reinterpret_cast<float *>(staging.base), abort,
-                                                  release + 8 * acc);
+                                                  columns, have_n, factor, reinterpret_cast<float *>(staging.base),
+                                                  abort, release + 8 * acc);
                     else
                         ok = epilogue_tile<EPI, ACT>(p, tile, d, acc_full + 8 * acc, acc_phase, cfirst,
-                                                     cfirst + cols, quarter, columns, have_n, staging,
-                                                     abort, release + 8 * acc);
+                                                     cfirst + cols, quarter, columns, have_n, factor,
+                                                     staging, abort, release + 8 * acc);
                     if (!ok) break;
                 }
                 tile.m += 2 * range.step;  // down the column, or looked up
@@ -1109,6 +1123,76 @@ __global__ void __launch_bounds__(256) k_join(const float *__restrict__ part, in
     }
 }
 
+// The largest finite |v| of a job's arrays (blockIdx.y), a partial maximum per block of
+// the kBoundParts across.  Maxima drop NaN by themselves; a thread that met an infinity
+// looks again, element by element.  (16384 x 1024 in fp16: 8 us with the launch.)
+struct BoundJobs {
+    BoundJob job[3];
+};
+__device__ __forceinline__ unsigned larger2(unsigned m, unsigned w, int dtype) {
+    w &= 0x7fff7fffu;
+    if (dtype == PDR_F16) {
+        const __half2 h = __hmax2(*reinterpret_cast<const __half2 *>(&m), *reinterpret_cast<const __half2 *>(&w));
+        return *reinterpret_cast<const unsigned *>(&h);
+    }
+    const __nv_bfloat162 h =
+        __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&m), *reinterpret_cast<const __nv_bfloat162 *>(&w));
+    return *reinterpret_cast<const unsigned *>(&h);
+}
+__device__ __forceinline__ float larger(float m, float v) {
+    const float a = fabsf(v);
+    return a <= 3.402823466e38f ? fmaxf(m, a) : m;
+}
+constexpr int kLargestThreads = 256;
+__global__ void __launch_bounds__(kLargestThreads)
+    k_largest(const __grid_constant__ BoundJobs jobs, float *__restrict__ part) {
+    __shared__ float warps[kLargestThreads / 32];
+    grid_dep_wait();
+    const BoundJob &j = jobs.job[blockIdx.y];
+    const int E = j.dtype == PDR_F32 ? 4 : 8;
+    const long long vectors = j.n / E, step = (long long)kBoundParts * kLargestThreads;
+    const long long first = (long long)blockIdx.x * kLargestThreads + threadIdx.x;
+    float m = 0.0f;
+    for (int a = 0; a < (j.p2 ? 2 : 1); ++a) {
+        const uint4 *p = static_cast<const uint4 *>(a ? j.p2 : j.p);
+        float f = 0.0f;
+        unsigned h = 0;
+        for (long long i = first; i < vectors; i += 8 * step) {
+            uint4 u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = i + k * step < vectors ? __ldg(p + i + k * step) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const unsigned w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (E == 4)
+                        f = fmaxf(f, fabsf(__uint_as_float(w[i])));
+                    else
+                        h = larger2(h, w[i], j.dtype);
+            }
+        }
+        if (E == 8) {
+            const float2 two = unpack2(h, j.dtype);
+            f = fmaxf(two.x, two.y);
+        }
+        if (f > 3.402823466e38f) {
+            f = 0.0f;
+            for (long long i = first; i < vectors; i += step)
+                for (int k = 0; k < E; ++k) f = larger(f, img_load(p, (size_t)(i * E + k), j.dtype));
+        }
+        m = fmaxf(m, f);
+        if (first < j.n - vectors * E) m = larger(m, img_load(p, (size_t)(vectors * E + first), j.dtype));
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int i = 1; i < kLargestThreads / 32; ++i) m = fmaxf(m, warps[i]);
+    part[blockIdx.y * kBoundParts + blockIdx.x] = m;
+}
+
 // dy is taken in vectors of 16 bytes; a thread keeps its vector of the rows, and so its
 // columns.
 struct ColumnPlan {
@@ -1137,7 +1221,8 @@ template <typename T>
 __global__ void __launch_bounds__(256) k_cast_columns(const T *__restrict__ dy, int dy_dtype,
                                                       long long M, int N, ColumnPlan p,
                                                       void *__restrict__ dz, int dz_dtype,
-                                                      long long ldz, float *__restrict__ colsum) {
+                                                      long long ldz, float *__restrict__ colsum,
+                                                      const Bound bound) {
     constexpr int E = 16 / sizeof(T);
     __shared__ float sums[256][E + 1];
     grid_dep_wait();
@@ -1146,6 +1231,7 @@ __global__ void __launch_bounds__(256) k_cast_columns(const T *__restrict__ dy, 
     const int per = 256 / width;  // rows at once
     const int sub = threadIdx.x / width, j = base + threadIdx.x % width;
     const bool whole = N % E == 0;  // rows start at 16 bytes
+    const float factor = bound.part ? bound_factor(bound, false) : 1.0f;
     float s[E] = {};
     if (sub < per)
         for (long long r = r0 + sub; r < r1; r += 4 * per) {
@@ -1180,7 +1266,7 @@ __global__ void __launch_bounds__(256) k_cast_columns(const T *__restrict__ dy, 
                 if (!dz || r + k * per >= r1) continue;
                 unsigned two[E / 2];
 #pragma unroll
-                for (int i = 0; i < E / 2; ++i) two[i] = pack2(v[2 * i], v[2 * i + 1], dz_dtype);
+                for (int i = 0; i < E / 2; ++i) two[i] = pack2(v[2 * i] * factor, v[2 * i + 1] * factor, dz_dtype);
                 // (Padded rows hold whole vectors.)
                 unsigned short *to = static_cast<unsigned short *>(dz) + (r + k * per) * ldz + j * E;
                 if constexpr (E == 4)
@@ -1414,6 +1500,7 @@ cudaError_t plan(const GemmArgs &g, int bcols, GemmParams &p) {
     p.in_dtype = g.in_dtype;
     p.ldi = g.ldi;
     p.colsum = g.colsum;
+    p.bound = g.bound;
     return cudaSuccess;
 }
 
@@ -1570,15 +1657,22 @@ long long column_groups(long long M, int N, int dy_dtype) {
 }
 
 cudaError_t launch_cast_columns(const void *dy, int dy_dtype, long long M, int N, void *dz,
-                                int dz_dtype, long long ldz, float *colsum, cudaStream_t s) {
+                                int dz_dtype, long long ldz, float *colsum, const Bound &bound,
+                                cudaStream_t s) {
     const ColumnPlan p = column_plan(M, N, dtype_bytes(dy_dtype));
     const dim3 grid(p.blocks, p.across);
     if (dy_dtype == PDR_F32)
         return launch_dependent(k_cast_columns<float>, grid, dim3(256), 0, s, static_cast<const float *>(dy),
-                                dy_dtype, M, N, p, dz, dz_dtype, ldz, colsum);
+                                dy_dtype, M, N, p, dz, dz_dtype, ldz, colsum, bound);
     return launch_dependent(k_cast_columns<unsigned short>, grid, dim3(256), 0, s,
                             static_cast<const unsigned short *>(dy), dy_dtype, M, N, p, dz, dz_dtype,
-                            ldz, colsum);
+                            ldz, colsum, bound);
+}
+
+cudaError_t launch_largest(const BoundJob *jobs, int n, float *part, cudaStream_t s) {
+    BoundJobs j = {};
+    for (int i = 0; i < n; ++i) j.job[i] = jobs[i];
+    return launch_dependent(k_largest, dim3(kBoundParts, (unsigned)n), dim3(kLargestThreads), 0, s, j, part);
 }
 
 cudaError_t read_wait_error(int *bits, cudaStream_t s) {

@@ -123,6 +123,36 @@ __device__ __forceinline__ void store8(bool on, void *p, const unsigned *w) {
         : "memory");
 }
 
+// ---- fp16's range --------------------------------------------------------------
+
+// The largest values of up to three arrays, as kBoundParts partial maxima each
+// (launch_largest), and what their product is taken times: a bound of what a product's
+// fp16 factor can hold.  part null: none.
+constexpr int kBoundParts = 256;  // two vectors a lane
+struct Bound {
+    const float *part = nullptr;
+    int groups = 0;
+    float times = 1.0f;
+};
+
+// 2^k with bound 2^k in [2^14, 2^15): a factor of at most 1.13 bounds (a slope's) stays
+// below fp16's largest number then, and 2^-28 of the bound is still a normal one.
+// `inverse`: 2^-k.  (Both are normal fp32 numbers: k in [-113, 126].)  The whole warp calls it.
+__device__ __forceinline__ float bound_factor(const Bound &r, bool inverse) {
+    float b = r.times;
+    for (int g = 0; g < r.groups; ++g) {
+        const float4 *p = reinterpret_cast<const float4 *>(r.part + g * kBoundParts) + (threadIdx.x & 31);
+        const float4 v = __ldg(p), u = __ldg(p + 32);
+        float m = fmaxf(fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)), fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)));
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        b *= m;
+    }
+    int e = (int)(__float_as_uint(b) >> 23);  // its exponent + 127
+    e = e < 15 ? 15 : e > 254 ? 254 : e;
+    return __uint_as_float((unsigned)(inverse ? e - 14 : 268 - e) << 23);
+}
+
 // ---- host plan -------------------------------------------------------------
 
 // One operand of a product as it lies in memory: `rows` x `cols`, rows of `ld`
@@ -169,6 +199,9 @@ struct GemmArgs {
     int in_dtype = PDR_F32;
     long long ldi = 0;
     float *colsum = nullptr;        // kEpiSlope: [4 * ceil(M / 128)][N] partial column sums
+    // Takes the bound's factor into the results (kEpiSlope, whose column sums stay without
+    // it, and kEpiGatedBwd), or out of them (kEpiLinear).
+    Bound bound;
 };
 
 // Whether a linear result of N columns (with an input of its type) is so narrow that
@@ -217,11 +250,21 @@ cudaError_t launch_join_columns(const ColumnJob &columns, cudaStream_t s);
 // second result the splits are part[split][2][rows][ld].  And column sums beside it.
 cudaError_t launch_join(const float *part, int splits, int rows, int cols, long long ld, void *to,
                         void *to2, int dtype, const ColumnJob &columns, cudaStream_t s);
-// dz = dy in `dz_dtype` (rows of ldz; null: not wanted) and partial column sums
-// of dy, in column_groups(M, N, dy_dtype) rows of `colsum` (null: not wanted).
+// dz = dy in `dz_dtype` times the bound's factor (rows of ldz; null: not wanted) and
+// partial column sums of dy, in column_groups(M, N, dy_dtype) rows of `colsum` (null: not
+// wanted).
 long long column_groups(long long M, int N, int dy_dtype);
 cudaError_t launch_cast_columns(const void *dy, int dy_dtype, long long M, int N, void *dz,
-                                int dz_dtype, long long ldz, float *colsum, cudaStream_t s);
+                                int dz_dtype, long long ldz, float *colsum, const Bound &bound,
+                                cudaStream_t s);
+// kBoundParts partial maxima of |v| over the finite values of each job's arrays (16-byte
+// aligned; the second may be null).
+struct BoundJob {
+    const void *p, *p2;
+    long long n;
+    int dtype;
+};
+cudaError_t launch_largest(const BoundJob *jobs, int n, float *part, cudaStream_t s);
 
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 inline bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

@@ -16,7 +16,12 @@
 //   dW  = dz^T x   (both operands MN-major), k split over the machine, fp32
 //       partial results added in order: bitwise reproducible.  In one launch with dx.
 // dz is rounded to x's type: it is an operand of 16-bit products, whose
-// results are rounded to that type too.
+// results are rounded to that type too.  Gradients of a loss that is a mean are far below
+// fp16's range (1e-6 for the parameters of a 512 x 512 frame), others may lie above it, and
+// dW's sums inside it all the same: an fp16 dz of another type's dy, or of a slope, is
+// taken times a power of two that brings the largest |dy| to 2^14 (one more pass over dy:
+// k_largest), and dx and dW are formed without it from the fp32 sums.  (16384 x 256 to 1024
+// with silu 78 us, without the factor 69; 65536 x 256 to 8 from fp32 dy 36 and 32.)
 #include "gemm.cuh"
 
 namespace pdr {
@@ -26,9 +31,9 @@ namespace {
 // that are no multiple of 16 bytes; of the residual or of dy, of 32), padded
 // results that are copied out at the end, dz, and partial sums.
 struct LinearLayout {
-    size_t x, w, in, out, dz, colsum, part, total;
+    size_t x, w, in, out, dz, colsum, part, bound, total;
     long long ldk, ldi, ldo, ldz, ldp, sum_rows;
-    bool pack_x, pack_in, pack_out, narrow, cast;
+    bool pack_x, pack_in, pack_out, narrow, cast, scaled;
     int splits;
     size_t take(size_t bytes) {
         const size_t at = total;
@@ -78,6 +83,8 @@ LinearLayout bwd_layout(int M, int N, int K, int dtype, int grad_dtype, int act)
     L.cast = act != PDR_ACT_NONE || grad_dtype != dtype || N % 8 != 0;
     L.ldz = L.cast ? padded(N, 2, 32) : N;
     if (L.cast) L.dz = L.take((size_t)M * L.ldz * 2);
+    L.scaled = dtype == PDR_F16 && (act != PDR_ACT_NONE || grad_dtype != dtype);
+    if (L.scaled) L.bound = L.take(kBoundParts * 4);
     L.narrow = gemm_narrow(K, dtype, false);  // dx
     L.ldo = L.narrow ? K : padded(K, 2, 16);
     L.pack_out = L.ldo != K;
@@ -220,6 +227,13 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
     if (L.pack_in) jobs[n++] = {grad, ws + L.in, M, N, L.ldi, dtype_bytes(grad_dtype)};
     if (launch_pack(jobs, n, s) != cudaSuccess) return PDR_ERR_CUDA;
     float *colsum = grad_bias ? reinterpret_cast<float *>(ws + L.colsum) : nullptr;
+    Bound bound;
+    if (L.scaled && (act || products)) {
+        const BoundJob job = {grad, nullptr, (long long)M * N, grad_dtype};
+        float *parts = reinterpret_cast<float *>(ws + L.bound);
+        if (launch_largest(&job, 1, parts, s) != cudaSuccess) return PDR_ERR_CUDA;
+        bound = {parts, 1, 1.0f};
+    }
     const Operand ox = {x, M, K, L.ldk}, ow = {weight, N, K, L.ldk};
     Operand oz = {L.cast ? ws + L.dz : grad, M, N, L.ldz};
     if (act) {
@@ -241,13 +255,15 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
         g.out_dtype = dtype;
         g.ldo = L.ldz;
         g.colsum = colsum;
+        g.bound = bound;
         e = launch_gemm(g, s);
     } else if ((L.cast && products) || colsum) {
         e = launch_cast_columns(grad, grad_dtype, M, N, L.cast && products ? ws + L.dz : nullptr,
-                                dtype, L.ldz, colsum, s);
+                                dtype, L.ldz, colsum, bound, s);
     }
     GemmArgs gx, gw;  // dx = dz W, dW = dz^T x
     gx.dtype = gw.dtype = dtype;
+    gx.bound = gw.bound = bound;
     gx.a[0] = gw.a[0] = oz;
     gx.b[0] = ow;
     gw.b[0] = ox;

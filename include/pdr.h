@@ -342,7 +342,11 @@ pdr_status pdr_linear_fwd(const void *x, const void *weight, int dtype, const fl
  * of `dtype` (16 bits), grad_bias [N] of bias_dtype; each may be NULL (not
  * wanted).  dL/dresidual is grad itself.  The pre-activation is formed again
  * from x, weight and bias where the activation needs it (nothing is saved by
- * the forward); grad_bias sums unrounded fp32 values. */
+ * the forward); grad_bias sums unrounded fp32 values.  dL/dz is rounded to
+ * `dtype` as an operand of grad_x's and grad_weight's products; in PDR_F16 (of
+ * another type's grad, or with an activation) it is taken times a power of two
+ * that fits the largest finite |grad|, which those results are freed of in fp32:
+ * gradients of any size keep fp16's 11 bits down to 2^-28 of the largest one. */
 size_t pdr_linear_bwd_workspace_bytes(int M, int N, int K, int dtype, int grad_dtype,
                                       int activation);
 pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const void *weight,

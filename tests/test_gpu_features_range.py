@@ -174,3 +174,67 @@ def test_rms_norm_gradients_without_eps(M, D, dtype, wt):
     close(dw, (G * S / m).sum(0), (D / 2 + M + 40) * STEP * ((G * S).abs() / m).sum(0), wt, "dw")
     y = F.rms_norm_fwd(s, w, eps=0.0)[0]
     close(y, S / m * W, (D / 2 + 16) * STEP * (S / m * W).abs(), dtype, "y")
+
+
+# ---- small and large gradients ------------------------------------------------------
+
+
+def check_linear_bwd(M, K, N, dtype, gdt, kind, gs=1.0, xs=1.0, ws=None, bias_dtype=F32, seed=0):
+    gen = generator(seed + M + K + N)
+    x, w, g = rand(gen, (M, K), dtype, xs), rand(gen, (N, K), dtype, K ** -0.5 if ws is None else ws), rand(gen, (M, N), gdt, gs)
+    b = rand(gen, (N,), bias_dtype)
+    X, W, B, G = f64(x), f64(w), f64(b), f64(g)
+    dx, dw, db = F.linear_bwd(g, x, w, b, kind)
+    z = X @ W.t() + B
+    slope = act(z, kind)[1]
+    dz = G * slope
+    e = G.abs() * slope_error(z, z_error(X, W, B), kind) + 2 * STEP * dz.abs()
+    er = e + U[dtype] * (dz.abs() + e) + (2.0 ** -39 * G.abs().max() if dtype == F16 else 0)
+    if kind == "none" and gdt == dtype:
+        er = torch.zeros_like(dz)
+    a = dz.abs() + er
+    close(dx, dz @ W, er @ W.abs() + (N + 4) * STEP * (a @ W.abs()), dtype, "dx")
+    close(dw, dz.t() @ X, er.t() @ X.abs() + (M + 100) * STEP * (a.t() @ X.abs()), dtype, "dw")
+    close(db, dz.sum(0), e.sum(0) + (M + 100) * STEP * (dz.abs() + e).sum(0), bias_dtype, "db")
+    return dx, dw, db
+
+
+@pytest.mark.parametrize("gdt,size", [(F32, 1e-6), (F32, 1e-8), (F32, 1e-12), (F32, 1e-25), (BF16, 1e-7), (F32, 1.0), (F32, 3e6), (BF16, 3e6)])
+@pytest.mark.parametrize("M,K,N", [(150, 64, 8), (150, 72, 6), (200, 77, 45), (130, 64, 40)])
+def test_linear_fp16_gradients_of_any_size(M, K, N, gdt, size):
+    """Gradients of a mean over pixels are far below fp16's smallest normal number; they keep their bits
+    on the way to dx and dW.  x and W are such that dx and dW lie in fp16's range where that is possible."""
+    scale = max(2.0 ** -13, min(100.0, 1e-2 / size))
+    dx, dw, db = check_linear_bwd(M, K, N, F16, gdt, "none", size, xs=scale, ws=scale)
+    assert db.abs().max() > 0
+    if 1e-8 <= size:
+        assert dx.abs().max() > 0 and dw.abs().max() > 0
+
+
+@pytest.mark.parametrize("kind", ["relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("gdt,size", [(F32, 1e-7), (BF16, 1e-7), (F16, 2e-6), (F32, 3e6), (F16, 1.2e4)])
+@pytest.mark.parametrize("M,K,N", [(200, 64, 40), (150, 77, 45)])
+def test_linear_fp16_gradients_of_any_size_with_an_activation(M, K, N, gdt, size, kind):
+    xs = 30.0 if size < 1 else 2.0 ** -13
+    check_linear_bwd(M, K, N, F16, gdt, kind, size, xs=xs, ws=K ** -0.5 / xs if size < 1 else 2.0 ** -13)
+
+
+@pytest.mark.parametrize("kind", ["none", "gelu"])
+def test_linear_fp16_gradients_of_zeros_and_infinities(kind):
+    gen = generator(9)
+    x, w, b = rand(gen, (300, 64), F16), rand(gen, (40, 64), F16, 0.1), rand(gen, (40,), F32)
+    dx, dw, db = F.linear_bwd(torch.zeros(300, 40, device="cuda"), x, w, b, kind)
+    assert not dx.any() and not dw.any() and not db.any()
+    g = rand(gen, (300, 40), F32, 1e-3)
+    clean = g.clone()
+    clean[[7, 150]] = 0
+    g[7, 3], g[150, 39] = float("inf"), float("nan")
+    hit = torch.zeros(300, dtype=torch.bool, device="cuda")
+    hit[[7, 150]] = True
+    got, want = F.linear_bwd(g, x, w, b, kind), F.linear_bwd(clean, x, w, b, kind)
+    # (a factor that differs by a power of two moves roundings 2^-39 of the largest value below)
+    assert ((got[0] - want[0])[~hit].abs().double() <= U[F16] * want[0][~hit].abs().double() + TINY[F16] * 2).all()
+    assert not torch.isfinite(got[0][hit]).any()
+    cols = torch.ones(40, dtype=torch.bool, device="cuda")
+    cols[[3, 39]] = False
+    assert torch.isfinite(got[1][cols]).all() and not torch.isfinite(got[1][~cols]).any()
