@@ -12,6 +12,10 @@
 //   dx = dg Wg + du Wu          one product, k running over both sources;
 //   dWg = dg^T x, dWu = du^T x  in the same launch, k split over the machine, fp32
 //                               partial results added in order.
+// In fp16 dg and du are taken times a power of two that fits their bound, as dz in
+// linear.cu: |dg| and |du| are at most 1.13 max |dh| D max |x| max |w| (k_largest over the
+// four).  The bound is loose by some 2^7, and 2^-28 of it still a normal number.
+// (16384 x 256 to 1024: 85 us, without the factor 76.)
 // 65536 x 256 to 1024 in bf16: 61 us (74 under the power cap that a long run meets; 1120 and
 // 929 TFLOP/s); the backward of 16384 rows 69 us.
 #include "gemm.cuh"
@@ -22,9 +26,9 @@ namespace {
 // The workspace: padded copies of what TMA or 32-byte loads cannot address,
 // padded results that are copied out at the end, dg and du, and partial sums.
 struct GatedLayout {
-    size_t x, wg, wu, in, out, dg, du, part, total;
+    size_t x, wg, wu, in, out, dg, du, part, bound, total;
     long long ldk, ldi, ldo, ldf, ldp;
-    bool pack_x, pack_in, pack_out;
+    bool pack_x, pack_in, pack_out, scaled;
     int splits;
     size_t take(size_t bytes) {
         const size_t at = total;
@@ -68,6 +72,8 @@ GatedLayout bwd_layout(int M, int D, int F, int dtype) {
     if (L.pack_in) L.in = L.take((size_t)M * L.ldi * 2);
     L.dg = L.take((size_t)M * L.ldf * 2);
     L.du = L.take((size_t)M * L.ldf * 2);
+    L.scaled = dtype == PDR_F16;
+    if (L.scaled) L.bound = L.take(3 * kBoundParts * 4);
     L.ldo = padded(D, 2, 16);
     L.pack_out = L.ldo != D;
     if (L.pack_out) L.out = L.take((size_t)M * L.ldo * 2);
@@ -191,6 +197,15 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
     }
     if (!grad_x && !grad_gate) return PDR_OK;
     char *ws = static_cast<char *>(workspace);
+    Bound bound;
+    if (L.scaled) {
+        const BoundJob jobs[3] = {{grad, nullptr, (long long)M * F, dtype},
+                                  {x, nullptr, (long long)M * D, dtype},
+                                  {w_gate, w_up, (long long)F * D, dtype}};
+        float *parts = reinterpret_cast<float *>(ws + L.bound);
+        if (launch_largest(jobs, 3, parts, s) != cudaSuccess) return PDR_ERR_CUDA;
+        bound = {parts, 3, (float)D};
+    }
     if (pack_rows(L, x, w_gate, w_up, &grad, M, D, F, 2, ws, s) != cudaSuccess) return PDR_ERR_CUDA;
     const Operand ox = {x, M, D, L.ldk}, og = {w_gate, F, D, L.ldk}, ou = {w_up, F, D, L.ldk};
     const Operand odg = {ws + L.dg, M, F, L.ldf}, odu = {ws + L.du, M, F, L.ldf};
@@ -213,12 +228,14 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
         g.out2 = ws + L.du;
         g.out_dtype = dtype;
         g.ldo = L.ldf;
+        g.bound = bound;
         e = launch_gemm(g, s);
     }
     GemmArgs gx, gw;  // dx = dg Wg + du Wu; dWg = dg^T x and dWu = du^T x
     gx.mode = kTwoSources;
     gw.mode = kBatchA;
     gx.dtype = gw.dtype = dtype;
+    gx.bound = gw.bound = bound;
     gx.a[0] = gw.a[0] = odg;
     gx.a[1] = gw.a[1] = odu;
     gx.b[0] = og;

@@ -149,7 +149,7 @@ __device__ __forceinline__ float bound_factor(const Bound &r, bool inverse) {
         b *= m;
     }
     int e = (int)(__float_as_uint(b) >> 23);  // its exponent + 127
-    e = e < 15 ? 15 : e > 254 ? 254 : e;
+    e = b == 0.0f ? 141 : e < 15 ? 15 : e > 254 ? 254 : e;  // (nothing to fit: 1)
     return __uint_as_float((unsigned)(inverse ? e - 14 : 268 - e) << 23);
 }
 

@@ -363,7 +363,10 @@ pdr_status pdr_gated_fwd(const void *x, const void *w_gate, const void *w_up, in
                          size_t workspace_bytes, void *stream);
 
 /* From grad = dL/dh [M][F]: grad_x [M][D], grad_gate and grad_up [F][D], all of
- * `dtype` (16 bits); grad_x, or both weight gradients, may be NULL. */
+ * `dtype` (16 bits); grad_x, or both weight gradients, may be NULL.  The gradients
+ * of the two products are rounded to `dtype` as operands of the next ones; in
+ * PDR_F16 with a power of two as in pdr_linear_bwd, fitted to the largest finite
+ * values of grad, x and the weights. */
 size_t pdr_gated_bwd_workspace_bytes(int M, int D, int F, int dtype);
 pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, const void *w_up,
                          int dtype, int activation, int M, int D, int F, void *grad_x,

@@ -238,3 +238,49 @@ def test_linear_fp16_gradients_of_zeros_and_infinities(kind):
     cols = torch.ones(40, dtype=torch.bool, device="cuda")
     cols[[3, 39]] = False
     assert torch.isfinite(got[1][cols]).all() and not torch.isfinite(got[1][~cols]).any()
+
+
+def check_gated_bwd(M, D, Fw, dtype, kind, gs=1.0, xs=1.0, wgs=None, wus=None, seed=0):
+    gen = generator(seed + M + D + Fw)
+    x = rand(gen, (M, D), dtype, xs)
+    wg, wu = (rand(gen, (Fw, D), dtype, D ** -0.5 if s is None else s) for s in (wgs, wus))
+    dh = rand(gen, (M, Fw), dtype, gs)
+    X, G, Up, H = f64(x), f64(wg), f64(wu), f64(dh)
+    g, u = X @ G.t(), X @ Up.t()
+    a, s = act(g, kind)
+    eg, eu = z_error(X, G, None), z_error(X, Up, None)
+    ea, es = value_error(g, eg, kind), slope_error(g, eg, kind)
+    dx, dg, du = F.gated_bwd(dh, x, wg, wu, kind)
+    DG, DU = H * u * s, H * a
+    eG = H.abs() * (es * (u.abs() + eu) + s.abs() * eu) + 3 * STEP * DG.abs()
+    eU = H.abs() * ea + 2 * STEP * DU.abs()
+    low = 2.0 ** -39 * H.abs().max() * D * X.abs().max() * max(G.abs().max(), Up.abs().max()) if dtype == F16 else 0
+    eG, eU = eG + U[dtype] * (DG.abs() + eG) + low, eU + U[dtype] * (DU.abs() + eU) + low
+    aG, aU = DG.abs() + eG, DU.abs() + eU
+    close(dx, DG @ G + DU @ Up, eG @ G.abs() + eU @ Up.abs() + (2 * Fw + 4) * STEP * (aG @ G.abs() + aU @ Up.abs()), dtype, "dx")
+    close(dg, DG.t() @ X, eG.t() @ X.abs() + (M + 100) * STEP * (aG.t() @ X.abs()), dtype, "dwg")
+    close(du, DU.t() @ X, eU.t() @ X.abs() + (M + 100) * STEP * (aU.t() @ X.abs()), dtype, "dwu")
+    return dx, dg, du
+
+
+@pytest.mark.parametrize("kind", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("M,D,Fw", [(150, 64, 40), (120, 72, 32), (200, 77, 45)])
+def test_gated_fp16_gradients_of_any_size(M, D, Fw, kind):
+    # dh of 32 of fp16's smallest steps, whose products with slopes lie below them
+    dx, dg, du = check_gated_bwd(M, D, Fw, F16, kind, 2e-6, xs=16.0, wgs=D ** -0.5 / 16, wus=D ** -0.5 / 16)
+    assert dg.abs().max() > 0
+    # dg beyond fp16's largest number on the way to a dx and dW inside its range
+    check_gated_bwd(M, D, Fw, F16, kind, 1.2e4, xs=2.0 ** -7, wgs=1e-3, wus=100.0)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("kind", ["none", "silu"])
+def test_gated_gradients_of_zeros(dtype, kind):
+    """Features, weights or gradients that are all zero: every gradient is zero, or what the others give."""
+    gen = generator(10)
+    x, wg, wu, dh = rand(gen, (150, 64), dtype), rand(gen, (40, 64), dtype, 0.1), rand(gen, (40, 64), dtype, 0.1), rand(gen, (150, 40), dtype, 1e3)
+    z = torch.zeros_like
+    for args in [(dh, z(x), wg, wu), (dh, x, z(wg), z(wu)), (z(dh), x, wg, wu)]:
+        assert not any(t.any() for t in F.gated_bwd(*args, kind))
+    dx, dg, du = F.gated_bwd(dh, x, z(wg), wu, kind)
+    assert torch.isfinite(dg).all() and not du.any() and (not dx.any() if kind == "silu" else True) and dg.any()
