@@ -40,20 +40,25 @@ __device__ __forceinline__ float rcp(float x) {
 // elements in one f32x2 instruction took 65.4.
 __device__ __forceinline__ float logistic(float v) { return rcp(1.0f + ex2(-kLog2e * v)); }
 
-// Phi(z) = erfc(-z / sqrt 2) / 2, and e^{-z^2/2}.  Abramowitz and Stegun, Handbook
-// of Mathematical Functions, 7.1.26: erfc(x) = (a1 t + ... + a5 t^5) e^{-x^2},
-// t = 1 / (1 + p x), |error| <= 1.5e-7 for x >= 0 -- below the rounding of every
-// type that an activation is stored in here, and small in the negative tail,
-// where 1 + erf would cancel.
+// Phi(z) = erfc(-z / sqrt 2) / 2, and e^{-z^2/2}.  For x >= 0 the form of Abramowitz and
+// Stegun, Handbook of Mathematical Functions, 7.1.26, erfc(x) = (c1 t + ... + c8 t^8)
+// e^{-x^2}, t = 1 / (1 + p x), with p = 0.43 and eight terms (half of them below) whose largest
+// relative error for 0 <= x <= 9.5 is least: 8.4e-8, 4e-7 as evaluated.  Relative, so
+// that the negative tail, where 1 + erf would cancel, keeps its bits in fp32 results too: an
+// activation there is good to 2^-21 + z^2 2^-23 (the exponent's rounding), down to 2^-126.
+// (The handbook's five terms bound the absolute error by 1.5e-7: 1.5e-2 of the value at
+// z = -6.  65536 rows of 256 to 1024, gated by gelu: 83 us, with five 79.)
 __device__ __forceinline__ float normal_cdf(float z, float &gauss) {
-    const float x = fabsf(z) * 0.70710678118654752f;
-    gauss = ex2(-kLog2e * x * x);
-    const float t = rcp(fmaf(0.3275911f, x, 1.0f));
-    float p = fmaf(1.061405429f, t, -1.453152027f);
-    p = fmaf(p, t, 1.421413741f);
-    p = fmaf(p, t, -0.284496736f);
-    p = fmaf(p, t, 0.254829592f);
-    const float half = 0.5f * p * t * gauss;  // erfc(|z| / sqrt 2) / 2
+    gauss = ex2(-0.5f * kLog2e * z * z);
+    const float t = rcp(fmaf(0.304055929f, fabsf(z), 1.0f));  // 0.43 / sqrt 2
+    float p = fmaf(0.0368627422f, t, -0.155225113f);
+    p = fmaf(p, t, 0.191922709f);
+    p = fmaf(p, t, -0.0429310761f);
+    p = fmaf(p, t, 0.123460680f);
+    p = fmaf(p, t, 0.102463067f);
+    p = fmaf(p, t, 0.122189872f);
+    p = fmaf(p, t, 0.121257156f);
+    const float half = p * t * gauss;  // erfc(|z| / sqrt 2) / 2
     return z < 0.0f ? half : 1.0f - half;
 }
 

@@ -284,3 +284,40 @@ def test_gated_gradients_of_zeros(dtype, kind):
         assert not any(t.any() for t in F.gated_bwd(*args, kind))
     dx, dg, du = F.gated_bwd(dh, x, z(wg), wu, kind)
     assert torch.isfinite(dg).all() and not du.any() and (not dx.any() if kind == "silu" else True) and dg.any()
+
+
+# ---- tails of the activations -----------------------------------------------------
+
+
+def tail(z, kind):
+    """Relative error that an activation may have: the exponent's argument is rounded."""
+    a = {"silu": z.abs(), "gelu": z * z / 2, "gelu_tanh": 1.6 * z.abs() * (1 + 0.0448 * z * z)}[kind]
+    return (16 + 4 * a) * STEP
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_activations_relative_to_their_value(kind, dtype):
+    """fp32 results of z from -12 to 6 (one input, weight 1: z is exact): small values keep their bits.
+    Factors below 2^-126 become 0, which moves the value by at most |z| 2^-126."""
+    z = torch.linspace(-12, 6, 4001, device="cuda").to(dtype)[:, None].contiguous()
+    z = torch.cat([z, (z[:2000] * 2.0 ** -10).contiguous()])
+    one = torch.ones(1, 1, device="cuda", dtype=dtype)
+    Z = f64(z)
+    want = act(Z, kind)[0]
+    for got in (F.linear_fwd(z, one, activation=kind, out_dtype=F32),
+                F.gated_fwd(torch.cat([z, torch.ones_like(z)], 1), torch.tensor([[1.0, 0.0]], device="cuda").to(dtype),
+                            torch.tensor([[0.0, 1.0]], device="cuda").to(dtype), kind, out_dtype=F32)):
+        err = (f64(got) - want).abs()
+        assert (err <= tail(Z, kind) * want.abs() + (1 + Z.abs()) * 2.0 ** -126).all(), (kind, float((err / want.abs().clamp_min(1e-300)).max()))
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu", "gelu_tanh"])
+def test_slopes_relative_to_their_terms(kind):
+    z = torch.linspace(-9, 6, 3001, device="cuda").to(BF16)[:, None].contiguous()
+    one = torch.ones(1, 1, device="cuda", dtype=BF16)
+    Z = f64(z)
+    dx = F.linear_bwd(torch.ones(3001, 1, device="cuda", dtype=BF16), z, one, None, kind, need=(True, False, False))[0]
+    value, slope = act(Z, kind)
+    terms = (value / Z.where(Z != 0, torch.ones_like(Z))).abs() + (slope - value / Z.where(Z != 0, torch.ones_like(Z))).abs()
+    assert ((f64(dx) - slope).abs() <= 2.01 * U[BF16] * slope.abs() + 2 * tail(Z, kind) * terms + STEP * terms).all()
