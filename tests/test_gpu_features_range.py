@@ -321,3 +321,39 @@ def test_slopes_relative_to_their_terms(kind):
     value, slope = act(Z, kind)
     terms = (value / Z.where(Z != 0, torch.ones_like(Z))).abs() + (slope - value / Z.where(Z != 0, torch.ones_like(Z))).abs()
     assert ((f64(dx) - slope).abs() <= 2.01 * U[BF16] * slope.abs() + 2 * tail(Z, kind) * terms + STEP * terms).all()
+
+
+# ---- several tiles a pair of SMs ---------------------------------------------------
+
+# B kept in shared memory (short k), and streamed.
+MANY = [(20000, 64, 700), (20000, 1000, 700), (40000, 72, 600)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("M,D,Fw", MANY)
+def test_gated_gradients_over_many_tiles(M, D, Fw, dtype):
+    check_gated_bwd(M, D, Fw, dtype, "silu")
+
+
+@pytest.mark.parametrize("dtype,gdt,kind", [(BF16, BF16, "gelu"), (F16, F32, "silu"), (BF16, F32, "none")])
+@pytest.mark.parametrize("M,K,N", MANY)
+def test_linear_gradients_over_many_tiles(M, K, N, dtype, gdt, kind):
+    check_linear_bwd(M, K, N, dtype, gdt, kind)
+
+
+@pytest.mark.parametrize("M,K,N", [(20000, 384, 700), (20000, 2048, 700), (30000, 100, 333)])
+def test_8_bits_over_many_tiles(M, K, N):
+    gen = generator(M + K + N)
+    x, xs = F.quantize_rows(rand(gen, (M, K), BF16))
+    (wg, gs), (wu, us) = (F.quantize_rows(rand(gen, (N, K), F32, K ** -0.5)) for _ in range(2))
+    b, r = rand(gen, (N,), F32), rand(gen, (M, N), F32)
+    X, G, Up = (f64(q.float()) * f64(s)[:, None] for q, s in [(x, xs), (wg, gs), (wu, us)])
+    g, u = X @ G.t(), X @ Up.t()
+    eg, eu = z_error(X, G, None) + 4 * STEP * g.abs(), z_error(X, Up, None) + 4 * STEP * u.abs()
+    z, ez = g + f64(b), z_error(X, G, f64(b)) + 4 * STEP * g.abs()
+    y = F.linear_fwd(x, wg, b, r, "gelu", F32, xs, gs)
+    want = act(z, "gelu")[0] + f64(r)
+    close(y, want, value_error(z, ez, "gelu") + STEP * (want.abs() + f64(r).abs()), F32, "y")
+    a = act(g, "silu")[0]
+    h = F.gated_fwd(x, wg, wu, x_scale=xs, gate_scale=gs, up_scale=us)
+    close(h, a * u, value_error(g, eg, "silu") * (u.abs() + eu) + a.abs() * eu + STEP * (a * u).abs(), BF16, "h")
