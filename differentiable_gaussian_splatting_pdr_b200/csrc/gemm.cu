@@ -70,7 +70,7 @@ struct __align__(64) GemmParams {
     int bn, bcols, stages, nacc;      // bcols: result columns of a tile
     int sharing;                      // epilogue groups that share a tile
     int stationary;                   // B of a column of tiles stays in shared memory
-    int per_stage;                    // k blocks of a stage
+    int per_stage;                    // k blocks of a stage (2: where B stays only)
     int nbuf;                         // buffers of an epilogue warp (1 or 2)
     int columns;                      // floats of an epilogue warp's bias and column scales
     int b_bytes, kelems;              // a block's B bytes, and k, of a k block
@@ -809,7 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             load_b(p, tile, kb, rank, held0 + kb * p.b_bytes, lead_b_full);
                     }
                     for (int kb = k.first; kb < k.end; kb += p.per_stage) {
-                        const bool two = p.per_stage == 2 && kb + 1 < k.end;
+                        const bool two = stays<NP>(p) && p.per_stage == 2 && kb + 1 < k.end;
                         if (!ready) ok = bar_wait(empty + 8 * stage, phase ^ 1, abort);
                         if (!ok) break;
                         const unsigned bar = lead_full + 8 * stage, at = stages0 + stage * stage_bytes;
@@ -822,10 +822,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         ready = bar_try(empty + 8 * stage, phase ^ 1);  // asked early: the answer takes a while
                         load_a(p, tile, kb, at, bar);
                         if (!stays<NP>(p)) load_b(p, tile, kb, rank, at + kABytes, bar);
-                        if (two) {
-                            load_a(p, tile, kb + 1, at + block_bytes, bar);
-                            if (!stays<NP>(p)) load_b(p, tile, kb + 1, rank, at + block_bytes + kABytes, bar);
-                        }
+                        if (two) load_a(p, tile, kb + 1, at + kABytes, bar);
                     }
                 }
             }
@@ -908,8 +905,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             }
                         };
                         block(at, bt);
-                        if (p.per_stage == 2 && kb + 1 < nk)
-                            block(at + block_bytes, bt + (stays<NP>(p) ? p.b_bytes : block_bytes));
+                        if (stays<NP>(p) && p.per_stage == 2 && kb + 1 < nk)
+                            block(at + kABytes, bt + p.b_bytes);
                         mma_commit(done);
                     }
                     if (!ok) break;
@@ -1376,7 +1373,11 @@ cudaError_t launch(const GemmLaunch<1> &l, int act, int grid, size_t smem, cudaS
         case PDR_ACT_SILU: return launch_act<EPI, PDR_ACT_SILU>(l, grid, smem, s);
         case PDR_ACT_GELU: return launch_act<EPI, PDR_ACT_GELU>(l, grid, smem, s);
         case PDR_ACT_GELU_TANH: return launch_act<EPI, PDR_ACT_GELU_TANH>(l, grid, smem, s);
-        default: return launch_act<EPI, PDR_ACT_NONE>(l, grid, smem, s);
+        default:
+            if constexpr (EPI == kEpiSlope)
+                return cudaErrorInvalidValue;  // (no activation, no slope: its callers read dy itself)
+            else
+                return launch_act<EPI, PDR_ACT_NONE>(l, grid, smem, s);
     }
 }
 
