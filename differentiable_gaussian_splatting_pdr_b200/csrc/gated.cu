@@ -41,8 +41,6 @@ bool sizes_ok(int M, int D, int F) { return M >= 0 && D >= 1 && F >= 1; }
 bool in_limits(int M, int D, int F) {
     return M <= PDR_MAX_ROWS && D <= PDR_MAX_FEATURES && F <= PDR_MAX_FEATURES;
 }
-bool half_type(int t) { return t == PDR_F16 || t == PDR_BF16; }
-bool act_ok(int act) { return act >= PDR_ACT_NONE && act <= PDR_ACT_GELU_TANH; }
 GatedLayout x_layout(int M, int D, int F, int dtype) {
     GatedLayout L = {};
     const int e = dtype_bytes(dtype);
@@ -104,8 +102,6 @@ cudaError_t pack_rows(const GatedLayout &L, const void *&x, const void *&wg, con
     return launch_pack(jobs, n, s);
 }
 
-pdr_status done(cudaError_t e) { return e == cudaSuccess ? PDR_OK : PDR_ERR_CUDA; }
-
 }  // namespace
 }  // namespace pdr
 
@@ -115,7 +111,7 @@ extern "C" {
 
 size_t pdr_gated_workspace_bytes(int M, int D, int F, int dtype, int h_dtype) {
     if (!sizes_ok(M, D, F) || !in_limits(M, D, F) || !(half_type(dtype) || dtype == PDR_E4M3) ||
-        !(half_type(h_dtype) || h_dtype == PDR_F32))
+        !float_type(h_dtype))
         return 0;
     return fwd_layout(M, D, F, dtype, h_dtype).total;
 }
@@ -125,7 +121,7 @@ pdr_status pdr_gated_fwd(const void *x, const void *w_gate, const void *w_up, in
                          int activation, int M, int D, int F, void *h, int h_dtype, void *workspace,
                          size_t workspace_bytes, void *stream) {
     const bool fp8 = dtype == PDR_E4M3;
-    if (!sizes_ok(M, D, F) || !(half_type(dtype) || fp8) || !(half_type(h_dtype) || h_dtype == PDR_F32) ||
+    if (!sizes_ok(M, D, F) || !(half_type(dtype) || fp8) || !float_type(h_dtype) ||
         !act_ok(activation))
         return PDR_ERR_INVALID_ARG;
     if (!in_limits(M, D, F)) return PDR_ERR_TOO_LARGE;

@@ -1397,7 +1397,8 @@ bool gemm_narrow(int N, int out_dtype, bool has_in) {
     return N <= kChunk && (row % 16 || (has_in && row % 32));
 }
 
-int gemm_tile_columns(int epi, int M, int N, int nz, long long kb) {
+// Columns of a tile of a result of M x N (x nz products) over kb k blocks.
+static int gemm_tile_columns(int epi, int M, int N, int nz, long long kb) {
     const bool dual = epi == kEpiGated || epi == kEpiGatedBwd;
     // The width whose rounds of tiles over the pairs take least, in clocks as
     // measured: 560 + 4/3 per accumulator column and k block (the copies' way

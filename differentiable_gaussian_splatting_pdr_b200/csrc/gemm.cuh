@@ -212,9 +212,6 @@ struct GemmArgs {
 // Whether a linear result of N columns (with an input of its type) is so narrow that
 // rows which TMA could not store, or the input's sectors, are taken as they are.
 bool gemm_narrow(int N, int out_dtype, bool has_in);
-// Columns of a tile that launch_gemm picks for a result of M x N (x nz products) over
-// kb k blocks.
-int gemm_tile_columns(int epi, int M, int N, int nz, long long kb);
 // Tiles along k that fill the machine for a weight gradient, at most `most`.
 int gemm_splits(int M, int N, int nz, long long K);
 cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s);
@@ -271,6 +268,11 @@ struct BoundJob {
 };
 cudaError_t launch_largest(const BoundJob *jobs, int n, float *part, cudaStream_t s);
 
+// What the entry points check and return.
+inline bool half_type(int t) { return t == PDR_F16 || t == PDR_BF16; }
+inline bool float_type(int t) { return t == PDR_F32 || half_type(t); }
+inline bool act_ok(int act) { return act >= PDR_ACT_NONE && act <= PDR_ACT_GELU_TANH; }
+inline pdr_status done(cudaError_t e) { return e == cudaSuccess ? PDR_OK : PDR_ERR_CUDA; }
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 inline bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 

@@ -98,12 +98,6 @@ LinearLayout bwd_layout(int M, int N, int K, int dtype, int grad_dtype, int act)
     return L;
 }
 
-bool act_ok(int act) { return act >= PDR_ACT_NONE && act <= PDR_ACT_GELU_TANH; }
-bool half_type(int t) { return t == PDR_F16 || t == PDR_BF16; }
-bool float_type(int t) { return t == PDR_F32 || half_type(t); }
-
-pdr_status done(cudaError_t e) { return e == cudaSuccess ? PDR_OK : PDR_ERR_CUDA; }
-
 }  // namespace
 }  // namespace pdr
 

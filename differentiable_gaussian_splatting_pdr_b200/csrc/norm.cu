@@ -451,9 +451,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-bool half_type(int t) { return t == PDR_F16 || t == PDR_BF16; }
-bool float_type(int t) { return t == PDR_F32 || half_type(t); }
-
 // Threads per row, block size and blocks for M rows of D elements.  Rows of more than
 // 1024 elements have a block each, as many blocks as `per_sm` threads an SM make
 // (with powers of two for T and blocks of 256, 512 or 1024 threads 73416 x 1152 to 8 bits took
@@ -503,7 +500,7 @@ cudaError_t launch_norm(const NormShape &n, const Args &a, size_t smem, cudaStre
 pdr_status run_fwd(NormArgs a, cudaStream_t s) {
     const NormShape n = norm_shape(a.M, a.D, dtype_bytes(a.dtype), a.dtype == PDR_F32 ? kFwdThreads32 : kFwdThreads);
     a.T = n.T;
-    return launch_norm<false>(n, a, 0, s) == cudaSuccess ? PDR_OK : PDR_ERR_CUDA;
+    return done(launch_norm<false>(n, a, 0, s));
 }
 
 bool norm_sizes(int M, int D) { return M >= 0 && D >= 1; }
@@ -576,7 +573,7 @@ pdr_status pdr_rms_norm_bwd(const void *grad, const void *sum, int dtype, const 
     cudaError_t err = cudaSuccess;
     if (M == 0) {
         if (grad_weight) err = cudaMemsetAsync(grad_weight, 0, (size_t)D * we, s);
-        return err == cudaSuccess ? PDR_OK : PDR_ERR_CUDA;
+        return done(err);
     }
     if (!grad_x && !grad_weight) return PDR_OK;
     const NormShape n = norm_shape(M, D, dtype_bytes(dtype), kBwdThreads);
@@ -587,7 +584,7 @@ pdr_status pdr_rms_norm_bwd(const void *grad, const void *sum, int dtype, const 
     err = launch_norm<true>(n, a, n.threads > n.T ? (size_t)(n.threads / n.T) * D * 4 : 0, s);
     if (err == cudaSuccess && grad_weight)
         err = launch_join_columns({static_cast<const float *>(workspace), n.blocks, D, grad_weight, weight_dtype}, s);
-    return err == cudaSuccess ? PDR_OK : PDR_ERR_CUDA;
+    return done(err);
 }
 
 }  // extern "C"
