@@ -58,6 +58,7 @@ SIGNATURES = {
     "pdr_rms_norm_bwd_workspace_bytes": (_sz, [_i] * 2),
     "pdr_rms_norm_bwd": (_i, [_vp, _vp, _i, _vp, _i, _vp, ctypes.c_float, _i, _i] + [_vp] * 3 + [_sz, _vp]),
     "pdr_check_wait_error": (_i, [_vp]),
+    "pdr_set_wait_limit": (_i, [_i]),
 }
 
 _lib = None

@@ -43,9 +43,11 @@ constexpr int kChunk = 16;            // columns an epilogue warp computes at on
 constexpr int kStore = 2 * kChunk;    // columns that it stores at once
 constexpr int kMaxCols = 64;          // most columns of a tile that an epilogue warp has
 constexpr int kBufferBytes = 32 * kStore * 2;  // per epilogue warp: 32 rows of 16 floats or 32 halves
-// Tries of a bounded wait: each try sleeps in hardware for up to some
-// microseconds, so a wait gives up after seconds, far beyond any product.
-constexpr int kWaitTries = 1 << 22;
+// Tries of a bounded wait.  A try that fails sleeps in hardware for 4.0 us (measured), so a
+// wait gives up after 4 seconds, far beyond any product; what is under way when one did
+// is waited for up to a quarter of a second each.
+constexpr int kWaitTries = 1 << 20, kDrainTries = 1 << 16;
+std::atomic<int> g_wait_tries{kWaitTries};
 
 __device__ int g_wait_error;  // set when a bounded wait gave up
 
@@ -88,6 +90,7 @@ struct __align__(64) GemmParams {
     long long ldi;
     float *colsum;
     Bound bound;
+    int tries;                        // of a wait
 };
 
 // One product, or two that run one behind the other in the same launch: tiles of the
@@ -102,7 +105,9 @@ struct Barriers {
     unsigned long long full[kMaxStages], empty[kMaxStages], acc_full[kMaxAcc], acc_empty[kMaxAcc];
     unsigned long long b_full, b_empty, drain;
     unsigned tmem;
-    int abort;
+    int abort;                        // a wait of the pair gave up
+    // In the first block: stages, and columns of stationary B, whose copies each block started.
+    int stages_sent[2], columns_sent[2];
 };
 
 __device__ __forceinline__ unsigned smem_u32(const void *p) {
@@ -154,16 +159,31 @@ __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
         : "memory");
     return ok != 0;
 }
-// Waits for a phase of a barrier, at most kWaitTries tries; false (and the
-// block's abort flag and the library's error word set) if it gave up.
-__device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity, int *abort) {
-    for (int i = 0; i < kWaitTries; ++i) {
+// An int of a block of the pair (its cluster address).
+__device__ __forceinline__ void store_at(unsigned addr, int v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Waits for a phase of a barrier, at most `tries` tries; false (and the abort flags of
+// both blocks and the library's error word set) if it gave up.  Nothing that waited in vain goes
+// on to use what it waited for: the roles leave their loops, and the pair ends together.
+__device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity, int *abort, int tries) {
+    for (int i = 0; i < tries; ++i) {
         if (bar_try(bar, parity)) return true;
         if ((i & 63) == 63 && *(volatile int *)abort) return false;
     }
-    *(volatile int *)abort = 1;
+    store_at(at_rank(smem_u32(abort), 0), 1);
+    store_at(at_rank(smem_u32(abort), 1), 1);
     atomicExch(&g_wait_error, 1);
     return false;
+}
+// Waits for what is under way, after a wait gave up.
+__device__ __forceinline__ void bar_drain(unsigned bar, unsigned parity) {
+    for (int i = 0; i < kDrainTries && !bar_try(bar, parity); ++i) {
+    }
+}
+// A phase's bytes that never come count as come.
+__device__ __forceinline__ void bar_complete(unsigned bar, unsigned bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 // The copy reports to a barrier of the first block (`bar`: its cluster address).
 __device__ __forceinline__ void tma_load(unsigned dst, const CUtensorMap *map, int x, int y,
@@ -508,7 +528,7 @@ __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t
             __syncwarp();
         }
     }
-    if (!__all_sync(0xffffffffu, bar_wait(ready, phase, abort))) return false;
+    if (!__all_sync(0xffffffffu, bar_wait(ready, phase, abort, p.tries))) return false;
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     for (int c = c0; c < c1 && any; c += C) {
         float v[C], u[kTwo ? C : 1];
@@ -657,7 +677,7 @@ __device__ __forceinline__ bool epilogue_narrow(const GemmParams &p, const Tile 
         }
         __syncwarp();
     }
-    if (!__all_sync(0xffffffffu, bar_wait(ready, phase, abort))) return false;
+    if (!__all_sync(0xffffffffu, bar_wait(ready, phase, abort, p.tries))) return false;
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     float v[kChunk];
     tmem_load(acc, v);
@@ -689,6 +709,34 @@ __device__ __forceinline__ bool epilogue_narrow(const GemmParams &p, const Tile 
     }
     __syncwarp();
     return true;
+}
+
+// After a wait gave up: the copies that the two blocks started end, whose bytes the first
+// block's barriers count.  A stage's n-th use is the (n / stages)-th phase of its barrier, and
+// one use of a stage is under way at most: the next is started behind the products
+// that read it, which waited for both blocks' copies.  So are the columns of stationary B.  Where one
+// block alone started a use, the other's share is put right first: the first block announces
+// the bytes of the second's copies, or counts those that it announced in vain.
+__device__ __forceinline__ void drain_phase(unsigned bar, int n, const int (&sent)[2], unsigned bytes,
+                                            unsigned parity) {
+    if (n >= sent[0])
+        bar_expect(bar, bytes);
+    else if (n >= sent[1])
+        bar_complete(bar, bytes);
+    bar_drain(bar, parity);
+}
+template <int NP>
+__device__ __forceinline__ void drain_copies(const GemmParams &p, const Barriers &bars, unsigned full,
+                                             unsigned b_full, unsigned block_bytes) {
+    const int sent[2] = {*(volatile const int *)&bars.stages_sent[0], *(volatile const int *)&bars.stages_sent[1]};
+    const int last = max(sent[0], sent[1]), uses = (p.kb + p.per_stage - 1) / p.per_stage;  // (of a tile, where B stays)
+    for (int n = max(0, last - p.stages); n < last; ++n) {
+        const bool two = stays<NP>(p) && p.per_stage == 2 && 2 * (n % uses) + 1 < p.kb;
+        drain_phase(full + 8 * (n % p.stages), n, sent, two ? 2 * block_bytes : block_bytes, n / p.stages & 1);
+    }
+    const int columns[2] = {*(volatile const int *)&bars.columns_sent[0], *(volatile const int *)&bars.columns_sent[1]};
+    const int most = max(columns[0], columns[1]);
+    if (most > 0) drain_phase(b_full, most - 1, columns, p.kb * p.b_bytes, (most - 1) & 1);
 }
 
 template <int EPI, int ACT, bool NARROW, int NP>
@@ -789,7 +837,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const unsigned stages0 = smem_u32(smem), held0 = smem_u32(held);
         if (warp == kCopyWarp && elect_one()) {
             const unsigned lead_full = at_rank(full, 0), lead_b_full = at_rank(b_full, 0);
-            int stage = 0, issued = 0, column = -1;
+            int stage = 0, issued = 0, column = -1, columns = 0;
             unsigned phase = 0, b_phase = 0;
             bool ok = true, ready = true;  // the first stages are empty
 #pragma unroll
@@ -801,16 +849,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const KRange k = k_range(p, tile);
                     if (stays<NP>(p) && column != column_of(p, t)) {
                         column = column_of(p, t);
-                        ok = bar_wait(b_empty, b_phase ^ 1, abort);
+                        ok = bar_wait(b_empty, b_phase ^ 1, abort, p.tries);
                         if (!ok) break;
                         b_phase ^= 1;
+                        ++columns;
                         if (rank == 0) bar_expect(b_full, 2 * p.kb * p.b_bytes);
                         for (int kb = 0; kb < p.kb; ++kb)
                             load_b(p, tile, kb, rank, held0 + kb * p.b_bytes, lead_b_full);
                     }
                     for (int kb = k.first; kb < k.end; kb += p.per_stage) {
                         const bool two = stays<NP>(p) && p.per_stage == 2 && kb + 1 < k.end;
-                        if (!ready) ok = bar_wait(empty + 8 * stage, phase ^ 1, abort);
+                        if (!ready) ok = bar_wait(empty + 8 * stage, phase ^ 1, abort, p.tries);
                         if (!ok) break;
                         const unsigned bar = lead_full + 8 * stage, at = stages0 + stage * stage_bytes;
                         if (rank == 0) bar_expect(full + 8 * stage, two ? 4 * block_bytes : 2 * block_bytes);
@@ -826,22 +875,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!ok && rank == 0) {
-                // The pair's copies in flight end before its blocks do (waits bounded).
-                const int n = issued < p.stages ? issued : p.stages;
-                for (int i = 0; i < n; ++i) {
-                    if (stage == 0) {
-                        stage = p.stages;
-                        phase ^= 1;
-                    }
-                    --stage;
-                    for (int j = 0; j < kWaitTries && !bar_try(full + 8 * stage, phase); ++j) {
-                    }
-                }
-                if (column >= 0)
-                    for (int j = 0; j < kWaitTries && !bar_try(b_full, b_phase ^ 1); ++j) {
-                    }
-            }
+            store_at(at_rank(smem_u32(&bars->stages_sent[rank]), 0), issued);
+            store_at(at_rank(smem_u32(&bars->columns_sent[rank]), 0), columns);
         } else if (warp == kProductWarp && rank == 0 && elect_one()) {
             // Tiles left in the column of the first one (stationary B).
             int stage = 0, acc = 0, left = 0;
@@ -868,12 +903,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             mma_commit(b_empty);  // the last column's B is free
                         else if (t >= p.main)
                             left -= t - p.main - column_of(p, t) * p.nb.d;
-                        ok = bar_wait(b_full, b_phase, abort);
+                        ok = bar_wait(b_full, b_phase, abort, p.tries);
                         b_phase ^= 1;
                         if (!ok) break;
                     }
                     --left;
-                    if (!acc_ready) ok = bar_wait(acc_empty + 8 * acc, acc_phase ^ 1, abort);
+                    if (!acc_ready) ok = bar_wait(acc_empty + 8 * acc, acc_phase ^ 1, abort, p.tries);
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const unsigned d = tmem + acc * p.bn, this_full = acc_full + 8 * acc;
@@ -883,7 +918,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     bool more = false;
                     for (int kb = 0; kb < nk; kb += p.per_stage) {
-                        if (!full_ready) ok = bar_wait(full + 8 * stage, phase, abort);
+                        if (!full_ready) ok = bar_wait(full + 8 * stage, phase, abort, p.tries);
                         if (!ok) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         const unsigned at = stages0 + stage * stage_bytes, done = empty + 8 * stage;
@@ -913,18 +948,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     mma_commit(this_full);
                 }
             }
-            if (!ok) {
-                const unsigned drain = smem_u32(&bars->drain);
-                mma_commit(drain);  // products in flight end before their memory is freed
-                for (int j = 0; j < kWaitTries && !bar_try(drain, 0); ++j) {
-                }
-            }
         }
     }
     // Neither block leaves, or gives up its memory, before both are done.
     __syncwarp();
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     cluster_sync();
+    if (*(volatile int *)abort) {  // (in both blocks or in neither)
+        // A wait gave up.  No copy or product is started any more; those under way end first.
+        if (warp == kProductWarp && elect_one()) {
+            const unsigned drain = smem_u32(&bars->drain);
+            if (rank == 0) mma_commit(drain);  // (of the thread that issued the products)
+            bar_drain(drain, 0);
+        } else if (warp == kCopyWarp && rank == 0 && elect_one()) {
+            drain_copies<NP>(p, *bars, full, b_full, block_bytes);
+        }
+        __syncwarp();
+        cluster_sync();
+    }
     if (warp == kProductWarp) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
@@ -1503,6 +1544,7 @@ cudaError_t plan(const GemmArgs &g, int bcols, GemmParams &p) {
     p.ldi = g.ldi;
     p.colsum = g.colsum;
     p.bound = g.bound;
+    p.tries = g_wait_tries.load(std::memory_order_relaxed);
     return cudaSuccess;
 }
 
@@ -1675,6 +1717,10 @@ cudaError_t launch_largest(const BoundJob *jobs, int n, float *part, cudaStream_
     BoundJobs j = {};
     for (int i = 0; i < n; ++i) j.job[i] = jobs[i];
     return launch_dependent(k_largest, dim3(kBoundParts, (unsigned)n), dim3(kLargestThreads), 0, s, j, part);
+}
+
+void set_wait_tries(int tries) {
+    g_wait_tries.store(tries < 0 ? kWaitTries : tries, std::memory_order_relaxed);
 }
 
 cudaError_t read_wait_error(int *bits, cudaStream_t s) {

@@ -218,6 +218,8 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s);
 // Two products without an activation (kEpiLinear) whose B are laid out alike and have
 // the same N, in one launch where their tiles go together.
 cudaError_t launch_gemm2(const GemmArgs &g0, const GemmArgs &g1, cudaStream_t s);
+// Tries of a wait in the launches to come (about 4 us each); negative: the default.
+void set_wait_tries(int tries);
 // Reads (and clears) the word that a bounded wait sets when it gives up.
 cudaError_t read_wait_error(int *bits, cudaStream_t s);
 

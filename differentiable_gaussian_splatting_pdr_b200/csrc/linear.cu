@@ -292,6 +292,11 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
     return done(e);
 }
 
+pdr_status pdr_set_wait_limit(int tries) {
+    set_wait_tries(tries);
+    return PDR_OK;
+}
+
 pdr_status pdr_check_wait_error(void *stream) {
     int bits = 0;
     if (read_wait_error(&bits, static_cast<cudaStream_t>(stream)) != cudaSuccess) return PDR_ERR_CUDA;

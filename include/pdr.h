@@ -404,6 +404,12 @@ pdr_status pdr_rms_norm_bwd(const void *grad, const void *sum, int dtype, const 
  * since the last call, and clears it. */
 pdr_status pdr_check_wait_error(void *stream);
 
+/* For tests of a caller's error handling: how often a wait of the products'
+ * kernels launched from now on is tried before it gives up (about 4 us a try; 0:
+ * at once; negative: the default, 4 seconds).  The kernels wait for what they have under
+ * way, leave the arrays around their results alone and return, whatever the limit. */
+pdr_status pdr_set_wait_limit(int tries);
+
 #ifdef __cplusplus
 }
 #endif
