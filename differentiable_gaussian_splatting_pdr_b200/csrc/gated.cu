@@ -135,6 +135,7 @@ pdr_status pdr_gated_fwd(const void *x, const void *w_gate, const void *w_up, in
     const GatedLayout L = fwd_layout(M, D, F, dtype, h_dtype);
     if (L.total && (!workspace || !aligned_to(workspace, 256))) return PDR_ERR_INVALID_ARG;
     if (workspace_bytes < L.total) return PDR_ERR_WORKSPACE_TOO_SMALL;
+    if (wait_error_pending()) return PDR_ERR_DEVICE_TIMEOUT;
     if (M == 0) return PDR_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (pack_rows(L, x, w_gate, w_up, nullptr, M, D, F, dtype_bytes(dtype), static_cast<char *>(workspace),
@@ -184,6 +185,7 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
     const GatedLayout L = bwd_layout(M, D, F, dtype);
     if (L.total && (!workspace || !aligned_to(workspace, 256))) return PDR_ERR_INVALID_ARG;
     if (workspace_bytes < L.total) return PDR_ERR_WORKSPACE_TOO_SMALL;
+    if (wait_error_pending()) return PDR_ERR_DEVICE_TIMEOUT;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     if (M == 0) {

@@ -19,6 +19,7 @@
 // 6.1 TB/s; 4096 x 4096 x 4096 in bf16: 106 us, 1300 TFLOP/s, bound by the operands' way
 // from L2.
 #include <stdint.h>
+#include <string.h>
 
 #include <atomic>
 
@@ -49,7 +50,10 @@ constexpr int kBufferBytes = 32 * kStore * 2;  // per epilogue warp: 32 rows of 
 constexpr int kWaitTries = 1 << 20, kDrainTries = 1 << 16;
 std::atomic<int> g_wait_tries{kWaitTries};
 
-__device__ int g_wait_error;  // set when a bounded wait gave up
+// A word per device that is set when a bounded wait gave up, in host memory that the
+// kernels write: entry points read it without waiting for the device.
+constexpr int kDevices = 64;
+std::atomic<int *> g_wait_words{nullptr};
 
 // Quotients by a divisor that is fixed for a launch, for dividends below 2^31:
 // with l = ceil(log2 d) and mul = floor(2^(31 + l) / d) + 1, n / d = (n mul) >> (31 + l).
@@ -91,6 +95,7 @@ struct __align__(64) GemmParams {
     float *colsum;
     Bound bound;
     int tries;                        // of a wait
+    int *wait_word;                   // set when one gave up
 };
 
 // One product, or two that run one behind the other in the same launch: tiles of the
@@ -163,17 +168,18 @@ __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
 __device__ __forceinline__ void store_at(unsigned addr, int v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-// Waits for a phase of a barrier, at most `tries` tries; false (and the abort flags of
+// Waits for a phase of a barrier, at most p.tries tries; false (and the abort flags of
 // both blocks and the library's error word set) if it gave up.  Nothing that waited in vain goes
 // on to use what it waited for: the roles leave their loops, and the pair ends together.
-__device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity, int *abort, int tries) {
-    for (int i = 0; i < tries; ++i) {
+__device__ __forceinline__ bool bar_wait(unsigned bar, unsigned parity, int *abort, const GemmParams &p) {
+    for (int i = 0; i < p.tries; ++i) {
         if (bar_try(bar, parity)) return true;
         if ((i & 63) == 63 && *(volatile int *)abort) return false;
     }
     store_at(at_rank(smem_u32(abort), 0), 1);
     store_at(at_rank(smem_u32(abort), 1), 1);
-    atomicExch(&g_wait_error, 1);
+    *(volatile int *)p.wait_word = 1;
+    __threadfence_system();
     return false;
 }
 // Waits for what is under way, after a wait gave up.
@@ -528,7 +534,7 @@ __device__ __forceinline__ bool epilogue_tile(const GemmParams &p, const Tile &t
             __syncwarp();
         }
     }
-    if (!__all_sync(0xffffffffu, bar_wait(ready, phase, abort, p.tries))) return false;
+    if (!__all_sync(0xffffffffu, bar_wait(ready, phase, abort, p))) return false;
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     for (int c = c0; c < c1 && any; c += C) {
         float v[C], u[kTwo ? C : 1];
@@ -677,7 +683,7 @@ __device__ __forceinline__ bool epilogue_narrow(const GemmParams &p, const Tile 
         }
         __syncwarp();
     }
-    if (!__all_sync(0xffffffffu, bar_wait(ready, phase, abort, p.tries))) return false;
+    if (!__all_sync(0xffffffffu, bar_wait(ready, phase, abort, p))) return false;
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     float v[kChunk];
     tmem_load(acc, v);
@@ -849,7 +855,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const KRange k = k_range(p, tile);
                     if (stays<NP>(p) && column != column_of(p, t)) {
                         column = column_of(p, t);
-                        ok = bar_wait(b_empty, b_phase ^ 1, abort, p.tries);
+                        ok = bar_wait(b_empty, b_phase ^ 1, abort, p);
                         if (!ok) break;
                         b_phase ^= 1;
                         ++columns;
@@ -859,7 +865,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     for (int kb = k.first; kb < k.end; kb += p.per_stage) {
                         const bool two = stays<NP>(p) && p.per_stage == 2 && kb + 1 < k.end;
-                        if (!ready) ok = bar_wait(empty + 8 * stage, phase ^ 1, abort, p.tries);
+                        if (!ready) ok = bar_wait(empty + 8 * stage, phase ^ 1, abort, p);
                         if (!ok) break;
                         const unsigned bar = lead_full + 8 * stage, at = stages0 + stage * stage_bytes;
                         if (rank == 0) bar_expect(full + 8 * stage, two ? 4 * block_bytes : 2 * block_bytes);
@@ -903,12 +909,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             mma_commit(b_empty);  // the last column's B is free
                         else if (t >= p.main)
                             left -= t - p.main - column_of(p, t) * p.nb.d;
-                        ok = bar_wait(b_full, b_phase, abort, p.tries);
+                        ok = bar_wait(b_full, b_phase, abort, p);
                         b_phase ^= 1;
                         if (!ok) break;
                     }
                     --left;
-                    if (!acc_ready) ok = bar_wait(acc_empty + 8 * acc, acc_phase ^ 1, abort, p.tries);
+                    if (!acc_ready) ok = bar_wait(acc_empty + 8 * acc, acc_phase ^ 1, abort, p);
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const unsigned d = tmem + acc * p.bn, this_full = acc_full + 8 * acc;
@@ -918,7 +924,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     bool more = false;
                     for (int kb = 0; kb < nk; kb += p.per_stage) {
-                        if (!full_ready) ok = bar_wait(full + 8 * stage, phase, abort, p.tries);
+                        if (!full_ready) ok = bar_wait(full + 8 * stage, phase, abort, p);
                         if (!ok) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         const unsigned at = stages0 + stage * stage_bytes, done = empty + 8 * stage;
@@ -1472,6 +1478,28 @@ int gemm_splits(int M, int N, int nz, long long K) {
 }
 
 namespace {
+// The current device's word, null where there is no memory for it.
+int *wait_word() {
+    int *words = g_wait_words.load(std::memory_order_acquire);
+    if (!words) {  // (relaxed: the first launch may be in a stream that is being captured)
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
+        void *p = nullptr;
+        const cudaError_t e = cudaHostAlloc(&p, kDevices * sizeof(int), cudaHostAllocPortable | cudaHostAllocMapped);
+        if (e == cudaSuccess) {
+            memset(p, 0, kDevices * sizeof(int));
+            if (g_wait_words.compare_exchange_strong(words, static_cast<int *>(p)))
+                words = static_cast<int *>(p);
+            else
+                cudaFreeHost(p);  // another thread was first: its words
+        }
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e != cudaSuccess) return nullptr;
+    }
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess ? words + dev % kDevices : nullptr;
+}
+
 int tile_columns(const GemmArgs &g) {
     const int kelems = g.dtype == PDR_E4M3 ? kRowBytes : kRowBytes / 2, nz = g.mode == kBatchA ? 2 : 1;
     if (g.splits > 1) return gemm_tile_columns(g.epi, 1 << 30, g.N, nz, 32);
@@ -1545,7 +1573,8 @@ cudaError_t plan(const GemmArgs &g, int bcols, GemmParams &p) {
     p.colsum = g.colsum;
     p.bound = g.bound;
     p.tries = g_wait_tries.load(std::memory_order_relaxed);
-    return cudaSuccess;
+    p.wait_word = wait_word();
+    return p.wait_word ? cudaSuccess : cudaErrorMemoryAllocation;
 }
 
 // Divides the columns of tiles among the pairs (stationary B): neighbouring rows of
@@ -1723,14 +1752,18 @@ void set_wait_tries(int tries) {
     g_wait_tries.store(tries < 0 ? kWaitTries : tries, std::memory_order_relaxed);
 }
 
+bool wait_error_pending() {
+    const int *words = g_wait_words.load(std::memory_order_acquire);
+    int dev = 0;
+    if (!words || cudaGetDevice(&dev) != cudaSuccess) return false;
+    return *(volatile const int *)(words + dev % kDevices) != 0;
+}
+
 cudaError_t read_wait_error(int *bits, cudaStream_t s) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(bits, g_wait_error, sizeof(int), 0,
-                                              cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess || *bits == 0) return e;
-    const int zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_wait_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-    return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
+    const cudaError_t e = cudaStreamSynchronize(s);
+    *bits = wait_error_pending();
+    if (*bits) *(volatile int *)wait_word() = 0;
+    return e;
 }
 
 }  // namespace pdr

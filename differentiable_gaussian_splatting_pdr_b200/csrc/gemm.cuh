@@ -220,6 +220,8 @@ cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t s);
 cudaError_t launch_gemm2(const GemmArgs &g0, const GemmArgs &g1, cudaStream_t s);
 // Tries of a wait in the launches to come (about 4 us each); negative: the default.
 void set_wait_tries(int tries);
+// Whether a wait on the current device gave up since read_wait_error last reported one.
+bool wait_error_pending();
 // Reads (and clears) the word that a bounded wait sets when it gives up.
 cudaError_t read_wait_error(int *bits, cudaStream_t s);
 

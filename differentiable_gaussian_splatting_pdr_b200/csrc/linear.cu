@@ -132,6 +132,7 @@ pdr_status pdr_linear_fwd(const void *x, const void *weight, int dtype, const fl
     const LinearLayout L = fwd_layout(M, N, K, dtype, y_dtype, residual != nullptr);
     if (L.total && (!workspace || !aligned_to(workspace, 256))) return PDR_ERR_INVALID_ARG;
     if (workspace_bytes < L.total) return PDR_ERR_WORKSPACE_TOO_SMALL;
+    if (wait_error_pending()) return PDR_ERR_DEVICE_TIMEOUT;
     if (M == 0) return PDR_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     GemmArgs g;
@@ -198,6 +199,7 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
     const LinearLayout L = bwd_layout(M, N, K, dtype, grad_dtype, activation);
     if (L.total && (!workspace || !aligned_to(workspace, 256))) return PDR_ERR_INVALID_ARG;
     if (workspace_bytes < L.total) return PDR_ERR_WORKSPACE_TOO_SMALL;
+    if (wait_error_pending()) return PDR_ERR_DEVICE_TIMEOUT;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     if (M == 0) {  // no rows: nothing to add up

@@ -447,7 +447,11 @@ def adapter(features: torch.Tensor, weights: AdapterWeights, base: torch.Tensor,
 
 
 def check_wait_error(device=None) -> None:
-    """Synchronise the current stream and raise if a product's kernel gave up a wait since the last call."""
+    """Synchronise the current stream and raise if a product's kernel gave up a wait since the last call.
+
+    A wait that gives up (after seconds) leaves wrong results.  linear, gated and adapter calls
+    made on that device after the kernel's end raise too, without synchronising, until
+    this call has reported it; this call waits for the work so far."""
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     if device.index is None:
         device = torch.device(device.type, torch.cuda.current_device())

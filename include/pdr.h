@@ -399,9 +399,12 @@ pdr_status pdr_rms_norm_bwd(const void *grad, const void *sum, int dtype, const 
                             size_t workspace_bytes, void *stream);
 
 /* The products' kernels bound every wait on the device; one that gives up ends
- * the kernel with wrong results and sets a word of the current device.
- * Synchronises `stream`, returns PDR_ERR_DEVICE_TIMEOUT if the word was set
- * since the last call, and clears it. */
+ * the kernel with wrong results and sets a word of its device, in host memory.
+ * The products' calls read it without waiting: while it is set, they launch
+ * nothing and return PDR_ERR_DEVICE_TIMEOUT, so that a caller learns of it at
+ * the first one made after that kernel's end.  This call synchronises `stream`, returns
+ * PDR_ERR_DEVICE_TIMEOUT if the current device's word is set, and clears it: the
+ * results since its last return are to be formed again. */
 pdr_status pdr_check_wait_error(void *stream);
 
 /* For tests of a caller's error handling: how often a wait of the products'

@@ -124,3 +124,42 @@ def test_arrays_around_the_results_stay_as_they_were(lib):
     assert (buf[:4096] == 7).all() and (buf[4096 + M * N:] == 7).all()
     assert torch.equal(x, xs) and torch.equal(w, ws)
     assert torch.equal(F.linear_fwd(x, w, out=out), want)
+
+
+def test_the_next_calls_refuse_until_the_error_was_reported(lib):
+    """Without check_wait_error too a wrong result does not stay unnoticed: the next product raises."""
+    rng = np.random.default_rng(4)
+    x, w, g = rand(rng, (300, 64), BF16), rand(rng, (64, 64), BF16), rand(rng, (300, 64), BF16)
+    want = F.linear_fwd(x, w)
+    lib.pdr_set_wait_limit(0)
+    F.linear_fwd(x, w)
+    lib.pdr_set_wait_limit(-1)
+    torch.cuda.synchronize()
+    y = torch.full_like(want, 7.0)
+    for call in (lambda: F.linear_fwd(x, w, out=y), lambda: F.linear_bwd(g, x, w), lambda: F.gated_fwd(x, w, w, out=y),
+                 lambda: F.gated_bwd(g, x, w, w), lambda: F.linear(x, w), lambda: F.gated(x, w, w)):
+        with pytest.raises(_lib.PdrError) as e:
+            call()
+        assert e.value.status == TIMEOUT
+    torch.cuda.synchronize()
+    assert (y == 7).all()  # nothing was launched
+    n = F.rms_norm_fwd(x, w[0].contiguous())[0]  # has no waits
+    assert torch.isfinite(n).all()
+    assert gave_up()
+    assert torch.equal(F.linear_fwd(x, w), want)
+
+
+def test_the_first_product_of_a_process_may_be_captured():
+    """The error word is made by the first launch, also inside a capture."""
+    import os
+    import subprocess
+    import sys
+    code = ("import torch; from differentiable_gaussian_splatting_pdr_b200 import features as F\n"
+            "x = torch.randn(100, 64, device='cuda', dtype=torch.bfloat16); w = x[:48].clone()\n"
+            "torch.cuda.synchronize(); g = torch.cuda.CUDAGraph()\n"
+            "with torch.cuda.graph(g):\n    y = F.linear_fwd(x, w)\n"
+            "g.replay(); torch.cuda.synchronize()\n"
+            "assert torch.equal(y, F.linear_fwd(x, w)); F.check_wait_error(); print('fine')\n")
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert out.returncode == 0 and "fine" in out.stdout, out.stderr[-2000:]
