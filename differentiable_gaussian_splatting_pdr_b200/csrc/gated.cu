@@ -270,7 +270,7 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
         e = launch_gemm(grad_x ? gx : gw, s);
     if (e == cudaSuccess && grad_x && L.pack_out) e = launch_unpack(ws + L.out, M, D, L.ldo, 2, grad_x, s);
     if (e == cudaSuccess && grad_gate && partial)
-        e = launch_join(part, L.splits, F, D, L.ldp, grad_gate, grad_up, dtype, {}, s);
+        e = launch_join(part, L.splits, F, D, L.ldp, n, grad_gate, grad_up, dtype, {}, s);
     return done(e);
 }
 

@@ -1110,7 +1110,7 @@ __global__ void __launch_bounds__(256) k_join_columns(const ColumnJob j) {
 // rows of threads.
 template <int Y>
 __global__ void __launch_bounds__(256) k_join(const float *__restrict__ part, int splits, int rows,
-                                              int cols, long long ld, void *to, void *to2,
+                                              int cols, long long ld, long long slice, void *to, void *to2,
                                               int dtype, unsigned blocks, const ColumnJob job) {
     constexpr int X = 256 / Y;
     __shared__ float4 sums[Y][X];
@@ -1119,8 +1119,8 @@ __global__ void __launch_bounds__(256) k_join(const float *__restrict__ part, in
         if (blockIdx.y == 0) join_columns<8>(job, blockIdx.x - blocks);
         return;
     }
-    const long long n = rows * ld, stride = n * (to2 ? 2 : 1);
-    part += blockIdx.y * n;
+    const long long n = rows * ld, stride = slice * (to2 ? 2 : 1);
+    part += blockIdx.y * slice;
     if (blockIdx.y) to = to2;
     const int x = threadIdx.x % X, y = threadIdx.x / X;
     const long long i = ((long long)blockIdx.x * X + x) * 4;
@@ -1259,14 +1259,17 @@ ColumnPlan column_plan(long long M, int N, int bytes) {
     return p;
 }
 
+// What rounding v to r leaves (an infinity stays one).
+__device__ __forceinline__ float rest(float v, float r) { return fabsf(r) <= 3.402823466e38f ? v - r : 0.0f; }
+
 // (Backward of 131072 x 256 to 256 columns, bf16 and a bias: 73 us, by single elements 162;
 // of 30000 x 256 to 777 columns, whose rows start anywhere, 63 and 101.)
 template <typename T>
 __global__ void __launch_bounds__(256) k_cast_columns(const T *__restrict__ dy, int dy_dtype,
                                                       long long M, int N, ColumnPlan p,
                                                       void *__restrict__ dz, int dz_dtype,
-                                                      long long ldz, float *__restrict__ colsum,
-                                                      const Bound bound) {
+                                                      long long ldz, int low,
+                                                      float *__restrict__ colsum, const Bound bound) {
     constexpr int E = 16 / sizeof(T);
     __shared__ float sums[256][E + 1];
     grid_dep_wait();
@@ -1310,12 +1313,19 @@ __global__ void __launch_bounds__(256) k_cast_columns(const T *__restrict__ dy, 
                 if (!dz || r + k * per >= r1) continue;
                 unsigned two[E / 2];
 #pragma unroll
-                for (int i = 0; i < E / 2; ++i) two[i] = pack2(v[2 * i] * factor, v[2 * i + 1] * factor, dz_dtype);
+                for (int i = 0; i < E; ++i) v[i] *= factor;
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) two[i] = pack2(v[2 * i], v[2 * i + 1], dz_dtype);
                 // (Padded rows hold whole vectors.)
                 unsigned short *to = static_cast<unsigned short *>(dz) + (r + k * per) * ldz + j * E;
-                if constexpr (E == 4)
+                if constexpr (E == 4) {
                     *reinterpret_cast<uint2 *>(to) = make_uint2(two[0], two[1]);
-                else
+                    if (low) {
+                        const float2 a = unpack2(two[0], dz_dtype), b = unpack2(two[1], dz_dtype);
+                        *reinterpret_cast<uint2 *>(to + low) = make_uint2(
+                            pack2(rest(v[0], a.x), rest(v[1], a.y), dz_dtype), pack2(rest(v[2], b.x), rest(v[3], b.y), dz_dtype));
+                    }
+                } else
                     *reinterpret_cast<uint4 *>(to) = make_uint4(two[0], two[1], two[2], two[3]);
             }
         }
@@ -1709,8 +1719,8 @@ cudaError_t launch_unpack(const void *from, long long rows, long long cols, long
                       : unpack_as<unsigned>(from, rows, cols, ld, to, s);
 }
 
-cudaError_t launch_join(const float *part, int splits, int rows, int cols, long long ld, void *to,
-                        void *to2, int dtype, const ColumnJob &columns, cudaStream_t s) {
+cudaError_t launch_join(const float *part, int splits, int rows, int cols, long long ld, long long slice,
+                        void *to, void *to2, int dtype, const ColumnJob &columns, cudaStream_t s) {
     const long long vectors = rows * ld / 4;
     // (Always Y = 8: gated backward with 1024 x 256 weights 75 against 68 us.  Always Y = 1:
     // backward of 131072 x 256 to 8 columns 60 against 57, to 256 columns 172 against 170.)
@@ -1718,7 +1728,7 @@ cudaError_t launch_join(const float *part, int splits, int rows, int cols, long 
     const unsigned blocks = (unsigned)((vectors + (few ? 31 : 255)) / (few ? 32 : 256));
     const dim3 grid(blocks + (unsigned)((columns.cols + 7) / 8), to2 ? 2 : 1);
     return launch_dependent(few ? k_join<8> : k_join<1>, grid, dim3(256), 0, s, part, splits, rows, cols, ld,
-                            to, to2, dtype, blocks, columns);
+                            slice, to, to2, dtype, blocks, columns);
 }
 
 cudaError_t launch_join_columns(const ColumnJob &columns, cudaStream_t s) {
@@ -1730,16 +1740,16 @@ long long column_groups(long long M, int N, int dy_dtype) {
 }
 
 cudaError_t launch_cast_columns(const void *dy, int dy_dtype, long long M, int N, void *dz,
-                                int dz_dtype, long long ldz, float *colsum, const Bound &bound,
-                                cudaStream_t s) {
+                                int dz_dtype, long long ldz, int low, float *colsum,
+                                const Bound &bound, cudaStream_t s) {
     const ColumnPlan p = column_plan(M, N, dtype_bytes(dy_dtype));
     const dim3 grid(p.blocks, p.across);
     if (dy_dtype == PDR_F32)
         return launch_dependent(k_cast_columns<float>, grid, dim3(256), 0, s, static_cast<const float *>(dy),
-                                dy_dtype, M, N, p, dz, dz_dtype, ldz, colsum, bound);
+                                dy_dtype, M, N, p, dz, dz_dtype, ldz, low, colsum, bound);
     return launch_dependent(k_cast_columns<unsigned short>, grid, dim3(256), 0, s,
                             static_cast<const unsigned short *>(dy), dy_dtype, M, N, p, dz, dz_dtype,
-                            ldz, colsum, bound);
+                            ldz, 0, colsum, bound);
 }
 
 cudaError_t launch_largest(const BoundJob *jobs, int n, float *part, cudaStream_t s) {

@@ -252,17 +252,17 @@ struct ColumnJob {
 };
 cudaError_t launch_join_columns(const ColumnJob &columns, cudaStream_t s);
 // to[r][c] = sum over the splits of part[split][r][c], rounded once to `dtype`;
-// partial rows are ld floats apart (a multiple of 4), results dense.  With a
-// second result the splits are part[split][2][rows][ld].  And column sums beside it.
-cudaError_t launch_join(const float *part, int splits, int rows, int cols, long long ld, void *to,
+// partial rows are ld floats apart (a multiple of 4), splits `slice` floats, results
+// dense.  With a second result the splits are part[split][2][slice].  And column sums beside it.
+cudaError_t launch_join(const float *part, int splits, int rows, int cols, long long ld, long long slice, void *to,
                         void *to2, int dtype, const ColumnJob &columns, cudaStream_t s);
-// dz = dy in `dz_dtype` times the bound's factor (rows of ldz; null: not wanted) and
-// partial column sums of dy, in column_groups(M, N, dy_dtype) rows of `colsum` (null: not
-// wanted).
+// dz = dy in `dz_dtype` times the bound's factor (rows of ldz; null: not wanted), what that
+// rounding leaves of an fp32 dy `low` elements behind it (0: not wanted), and partial column
+// sums of dy, in column_groups(M, N, dy_dtype) rows of `colsum` (null: not wanted).
 long long column_groups(long long M, int N, int dy_dtype);
 cudaError_t launch_cast_columns(const void *dy, int dy_dtype, long long M, int N, void *dz,
-                                int dz_dtype, long long ldz, float *colsum, const Bound &bound,
-                                cudaStream_t s);
+                                int dz_dtype, long long ldz, int low, float *colsum,
+                                const Bound &bound, cudaStream_t s);
 // kBoundParts partial maxima of |v| over the finite values of each job's arrays (16-byte
 // aligned; the second may be null).
 struct BoundJob {

@@ -22,6 +22,9 @@
 // taken times a power of two that brings the largest |dy| to 2^14 (one more pass over dy:
 // k_largest), and dx and dW are formed without it from the fp32 sums.  (16384 x 256 to 1024
 // with silu 78 us, without the factor 69; 65536 x 256 to 8 from fp32 dy 36 and 32.)
+// Of an fp32 dy with up to 32 columns (the head's, from the renderer) what the rounding leaves
+// is kept in 16 bits too, beside dz: the products' blocks of 64 k and tiles of 256 rows have
+// room for both, so that dx and dW are rounded once (16384 x 512 to 6: 22.5 us with and without).
 #include "gemm.cuh"
 
 namespace pdr {
@@ -34,7 +37,7 @@ struct LinearLayout {
     size_t x, w, in, out, dz, colsum, part, bound, total;
     long long ldk, ldi, ldo, ldz, ldp, sum_rows;
     bool pack_x, pack_in, pack_out, narrow, cast, scaled;
-    int splits;
+    int splits, low;  // low: where in a row of dz the rounding's rest is (0: nowhere)
     size_t take(size_t bytes) {
         const size_t at = total;
         total += align256(bytes);
@@ -82,6 +85,10 @@ LinearLayout bwd_layout(int M, int N, int K, int dtype, int grad_dtype, int act)
     if (L.pack_in) L.in = L.take((size_t)M * L.ldi * ge);
     L.cast = act != PDR_ACT_NONE || grad_dtype != dtype || N % 8 != 0;
     L.ldz = L.cast ? padded(N, 2, 32) : N;
+    if (act == PDR_ACT_NONE && grad_dtype == PDR_F32 && N <= 32) {
+        L.low = (int)padded(N, 2, 16);
+        L.ldz = 2 * L.low;
+    }
     if (L.cast) L.dz = L.take((size_t)M * L.ldz * 2);
     L.scaled = dtype == PDR_F16 && (act != PDR_ACT_NONE || grad_dtype != dtype);
     if (L.scaled) L.bound = L.take(kBoundParts * 4);
@@ -94,7 +101,7 @@ LinearLayout bwd_layout(int M, int N, int K, int dtype, int grad_dtype, int act)
     // dW through fp32 partial results, also where only its rows ask for it
     L.splits = gemm_splits(N, K, 1, M);
     L.ldp = padded(K, 4, 16);
-    if (L.splits > 1 || K % 8) L.part = L.take((size_t)L.splits * N * L.ldp * 4);
+    if (L.splits > 1 || K % 8 || L.low) L.part = L.take((size_t)L.splits * (L.low ? 2 * L.low : N) * L.ldp * 4);
     return L;
 }
 
@@ -255,7 +262,7 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
         e = launch_gemm(g, s);
     } else if ((L.cast && products) || colsum) {
         e = launch_cast_columns(grad, grad_dtype, M, N, L.cast && products ? ws + L.dz : nullptr,
-                                dtype, L.ldz, colsum, bound, s);
+                                dtype, L.ldz, L.low, colsum, bound, s);
     }
     GemmArgs gx, gw;  // dx = dz W, dW = dz^T x
     gx.dtype = gw.dtype = dtype;
@@ -264,8 +271,15 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
     gx.b[0] = ow;
     gw.b[0] = ox;
     gx.b_mn = gw.a_mn = gw.b_mn = true;
+    if (L.low) {  // dx: k over dz, then over the rest; dW: the rest's rows behind dz's
+        gx.mode = kTwoSources;
+        gx.a[1] = {ws + L.dz + L.low * 2, M, N, L.ldz};
+        gx.b[1] = ow;
+        gx.K[1] = N;
+        gw.a[0].cols = 2 * L.low;
+    }
     gx.M = M;
-    gw.M = N;
+    gw.M = L.low ? 2 * L.low : N;
     gx.N = gw.N = K;
     gx.K[0] = N;
     gw.K[0] = M;
@@ -273,12 +287,12 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
     gx.out = L.pack_out ? ws + L.out : grad_x;
     gx.out_dtype = dtype;
     gx.ldo = L.ldo;
-    const bool partial = L.splits > 1 || K % 8;
+    const bool partial = L.splits > 1 || K % 8 || L.low;
     gw.splits = L.splits;
     gw.out = partial ? ws + L.part : grad_weight;
     gw.out_dtype = partial ? (int)PDR_F32 : dtype;
     gw.ldo = partial ? L.ldp : K;
-    gw.out_split = L.splits > 1 ? N * L.ldp : 0;
+    gw.out_split = L.splits > 1 ? gw.M * L.ldp : 0;
     if (e == cudaSuccess && grad_x && grad_weight)
         e = launch_gemm2(gx, gw, s);
     else if (e == cudaSuccess && products)
@@ -287,8 +301,8 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
     ColumnJob db;
     if (colsum) db = {colsum, L.sum_rows, N, grad_bias, bias_dtype};
     if (e == cudaSuccess && grad_weight && partial)
-        e = launch_join(reinterpret_cast<float *>(ws + L.part), L.splits, N, K, L.ldp, grad_weight, nullptr,
-                        dtype, db, s);
+        e = launch_join(reinterpret_cast<float *>(ws + L.part), L.low ? 2 * L.splits : L.splits, N, K, L.ldp,
+                        (L.low ? L.low : N) * L.ldp, grad_weight, nullptr, dtype, db, s);
     else if (e == cudaSuccess && colsum)
         e = launch_join_columns(db, s);
     return done(e);

@@ -346,7 +346,9 @@ pdr_status pdr_linear_fwd(const void *x, const void *weight, int dtype, const fl
  * `dtype` as an operand of grad_x's and grad_weight's products; in PDR_F16 (of
  * another type's grad, or with an activation) it is taken times a power of two
  * that fits the largest finite |grad|, which those results are freed of in fp32:
- * gradients of any size keep fp16's 11 bits down to 2^-28 of the largest one. */
+ * gradients of any size keep fp16's 11 bits down to 2^-28 of the largest one.  A
+ * PDR_F32 grad of up to 32 columns without an activation (Gaussian parameters')
+ * is taken in two parts of 16 bits instead. */
 size_t pdr_linear_bwd_workspace_bytes(int M, int N, int K, int dtype, int grad_dtype,
                                       int activation);
 pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const void *weight,

@@ -240,6 +240,38 @@ def test_linear_fp16_gradients_of_zeros_and_infinities(kind):
     assert torch.isfinite(got[1][cols]).all() and not torch.isfinite(got[1][~cols]).any()
 
 
+@pytest.mark.parametrize("dtype,size", [(BF16, 1.0), (BF16, 1e-6), (F16, 1.0), (F16, 1e-6)])
+@pytest.mark.parametrize("M,K,N", [(1, 64, 8), (1000, 64, 8), (1000, 72, 6), (500, 77, 13), (300, 64, 32), (200, 520, 1), (40000, 40, 29),
+                                   (700, 9, 5)])
+def test_linear_gradients_of_few_columns_round_once(M, K, N, dtype, size):
+    """Up to 32 columns of fp32 gradients (the parameters'): dz in two parts of 16 bits leaves u(t)^2 of
+    it (and in fp16 a part's last bits, 2^-39 of the largest), and dx and dW have one rounding, their own."""
+    gen = generator(M + K + N)
+    x, w, g = rand(gen, (M, K), dtype, 50.0), rand(gen, (N, K), dtype, 50.0), rand(gen, (M, N), F32, size)
+    X, W, G = f64(x), f64(w), f64(g)
+    dx, dw, _ = F.linear_bwd(g, x, w)
+    er = U[dtype] ** 2 * G.abs() + (2.0 ** -39 * G.abs().max() if dtype == F16 else 0)
+    a = G.abs() + er
+    close(dx, G @ W, er @ W.abs() + (2 * N + 4) * STEP * (a @ W.abs()), dtype, "dx")
+    close(dw, G.t() @ X, er.t() @ X.abs() + (2 * M + 100) * STEP * (a.t() @ X.abs()), dtype, "dw")
+    assert torch.equal(F.linear_bwd(g, x, w, need=(True, False, False))[0], dx)
+    assert torch.equal(F.linear_bwd(g, x, w, need=(False, True, False))[1], dw)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_linear_gradients_of_few_columns_keep_infinities(dtype):
+    gen = generator(11)
+    x, w, g = rand(gen, (300, 64), dtype), rand(gen, (8, 64), dtype), rand(gen, (300, 8), F32)
+    clean = F.linear_bwd(g, x, w)
+    g[7, 3], g[150, 5] = float("inf"), float("nan")
+    dx, dw, _ = F.linear_bwd(g, x, w)
+    assert torch.equal(dx[7].float(), w[3].float().sign() * float("inf")) and torch.isnan(dx[150]).all()
+    rows = torch.ones(300, dtype=torch.bool, device="cuda")
+    rows[[7, 150]] = False
+    assert ((dx - clean[0]).abs()[rows].double() <= U[dtype] * clean[0][rows].abs().double() + 2 * TINY[dtype]).all()
+    assert torch.equal(dw[3].float(), x[7].float().sign() * float("inf")) and torch.isnan(dw[5]).all()
+
+
 def check_gated_bwd(M, D, Fw, dtype, kind, gs=1.0, xs=1.0, wgs=None, wus=None, seed=0):
     gen = generator(seed + M + D + Fw)
     x = rand(gen, (M, D), dtype, xs)
