@@ -329,11 +329,17 @@ __device__ __forceinline__ void norm_rows(const NormArgs &a, const Row<E, SHIFT>
             if (a.scale) {
                 const float scale = max_nan(both.y * k1 * (1.0f / kE4M3Max), kMinScale);
                 if (q.t == 0 && on) a.scale[row] = scale;
-                // One factor after the other: |v k1| <= 448 scale, while rstd / scale of a row of
-                // zeros (1000 x 2^126) is beyond fp32, and 0 times that no zero.
+                // rstd / scale of a row of zeros (1000 x 2^126) is beyond fp32, and 0 times that no
+                // zero: one factor after the other there, since |v rstd| <= 448 scale.  (For every
+                // row 73416 x 1152 to 8 bits took 81 us against 80.)
+                const float rstd = k1, inverse = rcp(scale);
+                k1 *= inverse;
+                if (__builtin_expect(!(k1 <= 3.402823466e38f), 0)) {
+                    asm volatile("");  // (a branch, not 16 conditional products)
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) v[j] *= k1;
-                k1 = rcp(scale);
+                    for (int j = 0; j < kPer; ++j) v[j] *= rstd;
+                    k1 = inverse;
+                }
             }
 #pragma unroll
             for (int j = 0; j < kPer; ++j) v[j] *= k1;
