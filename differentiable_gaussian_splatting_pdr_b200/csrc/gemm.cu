@@ -1268,7 +1268,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) k_cast_columns(const T *__restrict__ dy, int dy_dtype,
                                                       long long M, int N, ColumnPlan p,
                                                       void *__restrict__ dz, int dz_dtype,
-                                                      long long ldz, int low,
+                                                      long long ldz, int low, const TwiceJob two,
                                                       float *__restrict__ colsum, const Bound bound) {
     constexpr int E = 16 / sizeof(T);
     __shared__ float sums[256][E + 1];
@@ -1279,6 +1279,16 @@ __global__ void __launch_bounds__(256) k_cast_columns(const T *__restrict__ dy, 
     const int sub = threadIdx.x / width, j = base + threadIdx.x % width;
     const bool whole = N % E == 0;  // rows start at 16 bytes
     const float factor = bound.part ? bound_factor(bound, false) : 1.0f;
+    if (E == 4 && two.to) {
+        const int vectors = (int)(two.ld / 8), all = 2 * low * vectors;
+        for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x; i < all; i += gridDim.x * gridDim.y * 256) {
+            const int r = i / vectors, n = r < low ? r : r - low;
+            static_cast<uint4 *>(two.to)[i] =
+                n < N ? padded_vector(static_cast<const unsigned short *>(two.from) + (long long)n * two.cols,
+                                      i - r * vectors, two.cols)
+                      : make_uint4(0, 0, 0, 0);
+        }
+    }
     float s[E] = {};
     if (sub < per)
         for (long long r = r0 + sub; r < r1; r += 4 * per) {
@@ -1286,7 +1296,7 @@ __global__ void __launch_bounds__(256) k_cast_columns(const T *__restrict__ dy, 
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const T *row = dy + (r + k * per) * N;
-                if (r + k * per >= r1)
+                if (r + k * per >= r1 || j * E >= N)
                     raw[k] = make_uint4(0, 0, 0, 0);
                 else if (whole)
                     raw[k] = __ldg(reinterpret_cast<const uint4 *>(row) + j);
@@ -1311,25 +1321,25 @@ __global__ void __launch_bounds__(256) k_cast_columns(const T *__restrict__ dy, 
 #pragma unroll
                 for (int i = 0; i < E; ++i) s[i] += v[i];
                 if (!dz || r + k * per >= r1) continue;
-                unsigned two[E / 2];
+                unsigned h[E / 2];
 #pragma unroll
                 for (int i = 0; i < E; ++i) v[i] *= factor;
 #pragma unroll
-                for (int i = 0; i < E / 2; ++i) two[i] = pack2(v[2 * i], v[2 * i + 1], dz_dtype);
+                for (int i = 0; i < E / 2; ++i) h[i] = pack2(v[2 * i], v[2 * i + 1], dz_dtype);
                 // (Padded rows hold whole vectors.)
                 unsigned short *to = static_cast<unsigned short *>(dz) + (r + k * per) * ldz + j * E;
                 if constexpr (E == 4) {
-                    *reinterpret_cast<uint2 *>(to) = make_uint2(two[0], two[1]);
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(h[0], h[1]);
                     if (low) {
-                        const float2 a = unpack2(two[0], dz_dtype), b = unpack2(two[1], dz_dtype);
+                        const float2 a = unpack2(h[0], dz_dtype), b = unpack2(h[1], dz_dtype);
                         *reinterpret_cast<uint2 *>(to + low) = make_uint2(
                             pack2(rest(v[0], a.x), rest(v[1], a.y), dz_dtype), pack2(rest(v[2], b.x), rest(v[3], b.y), dz_dtype));
                     }
                 } else
-                    *reinterpret_cast<uint4 *>(to) = make_uint4(two[0], two[1], two[2], two[3]);
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(h[0], h[1], h[2], h[3]);
             }
         }
-    if (!colsum) return;
+    if (!colsum || blockIdx.x >= p.blocks) return;
     for (int half = 128; half >= 1; half /= 2) {  // the upper half of the rows to the lower, in turn
         if (half >= per) continue;
         if (sub >= half && sub < 2 * half && sub < per)
@@ -1735,21 +1745,23 @@ cudaError_t launch_join_columns(const ColumnJob &columns, cudaStream_t s) {
     return launch_dependent(k_join_columns, dim3((unsigned)((columns.cols + 7) / 8)), dim3(256), 0, s, columns);
 }
 
-long long column_groups(long long M, int N, int dy_dtype) {
-    return column_plan(M, N, dtype_bytes(dy_dtype)).blocks;
+long long column_groups(long long M, int N, int dy_dtype, int low) {
+    return column_plan(M, low ? low : N, dtype_bytes(dy_dtype)).blocks;
 }
 
 cudaError_t launch_cast_columns(const void *dy, int dy_dtype, long long M, int N, void *dz,
-                                int dz_dtype, long long ldz, int low, float *colsum,
-                                const Bound &bound, cudaStream_t s) {
-    const ColumnPlan p = column_plan(M, N, dtype_bytes(dy_dtype));
-    const dim3 grid(p.blocks, p.across);
+                                int dz_dtype, long long ldz, int low, const TwiceJob &two,
+                                float *colsum, const Bound &bound, cudaStream_t s) {
+    const ColumnPlan p = column_plan(M, low ? low : N, dtype_bytes(dy_dtype));
+    // (Few rows: more blocks for the weight alone.)
+    const long long copies = two.to ? (2 * low * two.ld / 8 + 255) / 256 : 0;
+    const dim3 grid((unsigned)(copies > p.blocks ? (copies < 4 * kSMs ? copies : 4 * kSMs) : p.blocks), p.across);
     if (dy_dtype == PDR_F32)
         return launch_dependent(k_cast_columns<float>, grid, dim3(256), 0, s, static_cast<const float *>(dy),
-                                dy_dtype, M, N, p, dz, dz_dtype, ldz, low, colsum, bound);
+                                dy_dtype, M, N, p, dz, dz_dtype, ldz, low, two, colsum, bound);
     return launch_dependent(k_cast_columns<unsigned short>, grid, dim3(256), 0, s,
                             static_cast<const unsigned short *>(dy), dy_dtype, M, N, p, dz, dz_dtype,
-                            ldz, 0, colsum, bound);
+                            ldz, 0, two, colsum, bound);
 }
 
 cudaError_t launch_largest(const BoundJob *jobs, int n, float *part, cudaStream_t s) {

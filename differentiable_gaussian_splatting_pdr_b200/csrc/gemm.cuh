@@ -256,13 +256,21 @@ cudaError_t launch_join_columns(const ColumnJob &columns, cudaStream_t s);
 // dense.  With a second result the splits are part[split][2][slice].  And column sums beside it.
 cudaError_t launch_join(const float *part, int splits, int rows, int cols, long long ld, long long slice, void *to,
                         void *to2, int dtype, const ColumnJob &columns, cudaStream_t s);
-// dz = dy in `dz_dtype` times the bound's factor (rows of ldz; null: not wanted), what that
-// rounding leaves of an fp32 dy `low` elements behind it (0: not wanted), and partial column
-// sums of dy, in column_groups(M, N, dy_dtype) rows of `colsum` (null: not wanted).
-long long column_groups(long long M, int N, int dy_dtype);
+// dz = dy in `dz_dtype` times the bound's factor (rows of ldz; null: not wanted), and partial
+// column sums of dy, in column_groups(M, N, dy_dtype, low) rows of `colsum` (null: not wanted).
+// With `low` (a multiple of 8, N at least) rows of dz are low elements of an fp32 dy, zeros
+// behind the N-th, then low of what that rounding leaves; and `two` takes the 16-bit weight
+// [N][cols] twice, one below the other, in rows of ld (zeros likewise; to null: not wanted).
+struct TwiceJob {
+    const void *from = nullptr;
+    void *to = nullptr;
+    int cols = 0;
+    long long ld = 0;
+};
+long long column_groups(long long M, int N, int dy_dtype, int low);
 cudaError_t launch_cast_columns(const void *dy, int dy_dtype, long long M, int N, void *dz,
-                                int dz_dtype, long long ldz, int low, float *colsum,
-                                const Bound &bound, cudaStream_t s);
+                                int dz_dtype, long long ldz, int low, const TwiceJob &two,
+                                float *colsum, const Bound &bound, cudaStream_t s);
 // kBoundParts partial maxima of |v| over the finite values of each job's arrays (16-byte
 // aligned; the second may be null).
 struct BoundJob {

@@ -23,8 +23,9 @@
 // k_largest), and dx and dW are formed without it from the fp32 sums.  (16384 x 256 to 1024
 // with silu 78 us, without the factor 69; 65536 x 256 to 8 from fp32 dy 36 and 32.)
 // Of an fp32 dy with up to 32 columns (the head's, from the renderer) what the rounding leaves
-// is kept in 16 bits too, beside dz: the products' blocks of 64 k and tiles of 256 rows have
-// room for both, so that dx and dW are rounded once (16384 x 512 to 6: 22.5 us with and without).
+// is kept in 16 bits too, beside dz: dx's block of 64 k (over W twice) and dW's tile of 256
+// rows have room for both, so that dx and dW are rounded once (65536 x 512 to 6:
+// 45 us with and without, with the rest as a second block of k 49).
 #include "gemm.cuh"
 
 namespace pdr {
@@ -34,7 +35,7 @@ namespace {
 // that are no multiple of 16 bytes; of the residual or of dy, of 32), padded
 // results that are copied out at the end, dz, and partial sums.
 struct LinearLayout {
-    size_t x, w, in, out, dz, colsum, part, bound, total;
+    size_t x, w, w2, in, out, dz, colsum, part, bound, total;
     long long ldk, ldi, ldo, ldz, ldp, sum_rows;
     bool pack_x, pack_in, pack_out, narrow, cast, scaled;
     int splits, low;  // low: where in a row of dz the rounding's rest is (0: nowhere)
@@ -88,6 +89,7 @@ LinearLayout bwd_layout(int M, int N, int K, int dtype, int grad_dtype, int act)
     if (act == PDR_ACT_NONE && grad_dtype == PDR_F32 && N <= 32) {
         L.low = (int)padded(N, 2, 16);
         L.ldz = 2 * L.low;
+        L.w2 = L.take((size_t)L.ldz * L.ldk * 2);
     }
     if (L.cast) L.dz = L.take((size_t)M * L.ldz * 2);
     L.scaled = dtype == PDR_F16 && (act != PDR_ACT_NONE || grad_dtype != dtype);
@@ -96,7 +98,7 @@ LinearLayout bwd_layout(int M, int N, int K, int dtype, int grad_dtype, int act)
     L.ldo = L.narrow ? K : padded(K, 2, 16);
     L.pack_out = L.ldo != K;
     if (L.pack_out) L.out = L.take((size_t)M * L.ldo * 2);
-    L.sum_rows = act != PDR_ACT_NONE ? 4 * (((long long)M + 127) / 128) : column_groups(M, N, grad_dtype);
+    L.sum_rows = act != PDR_ACT_NONE ? 4 * (((long long)M + 127) / 128) : column_groups(M, N, grad_dtype, L.low);
     L.colsum = L.take((size_t)L.sum_rows * N * 4);
     // dW through fp32 partial results, also where only its rows ask for it
     L.splits = gemm_splits(N, K, 1, M);
@@ -223,7 +225,7 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
         jobs[n++] = {x, ws + L.x, M, K, L.ldk, 2};
         x = ws + L.x;
     }
-    if (L.pack_x && (act || grad_x)) {
+    if (L.pack_x && (act || grad_x) && !L.low) {
         jobs[n++] = {weight, ws + L.w, N, K, L.ldk, 2};
         weight = ws + L.w;
     }
@@ -261,8 +263,10 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
         g.bound = bound;
         e = launch_gemm(g, s);
     } else if ((L.cast && products) || colsum) {
+        TwiceJob two;
+        if (L.low && grad_x) two = {weight, ws + L.w2, K, L.ldk};
         e = launch_cast_columns(grad, grad_dtype, M, N, L.cast && products ? ws + L.dz : nullptr,
-                                dtype, L.ldz, L.low, colsum, bound, s);
+                                dtype, L.ldz, L.low, two, colsum, bound, s);
     }
     GemmArgs gx, gw;  // dx = dz W, dW = dz^T x
     gx.dtype = gw.dtype = dtype;
@@ -271,18 +275,15 @@ pdr_status pdr_linear_bwd(const void *grad, int grad_dtype, const void *x, const
     gx.b[0] = ow;
     gw.b[0] = ox;
     gx.b_mn = gw.a_mn = gw.b_mn = true;
-    if (L.low) {  // dx: k over dz, then over the rest; dW: the rest's rows behind dz's
-        gx.mode = kTwoSources;
-        gx.a[1] = {ws + L.dz + L.low * 2, M, N, L.ldz};
-        gx.b[1] = ow;
-        gx.K[1] = N;
-        gw.a[0].cols = 2 * L.low;
-    }
     gx.M = M;
-    gw.M = L.low ? 2 * L.low : N;
+    gw.M = N;
     gx.N = gw.N = K;
     gx.K[0] = N;
     gw.K[0] = M;
+    if (L.low) {  // dx: k over dz and the rest; dW: the rest's rows behind dz's
+        gx.a[0].cols = gw.a[0].cols = gx.K[0] = gw.M = 2 * L.low;
+        gx.b[0] = {ws + L.w2, 2 * L.low, K, L.ldk};
+    }
     gx.narrow = L.narrow;
     gx.out = L.pack_out ? ws + L.out : grad_x;
     gx.out_dtype = dtype;

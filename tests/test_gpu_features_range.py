@@ -242,7 +242,7 @@ def test_linear_fp16_gradients_of_zeros_and_infinities(kind):
 
 @pytest.mark.parametrize("dtype,size", [(BF16, 1.0), (BF16, 1e-6), (F16, 1.0), (F16, 1e-6)])
 @pytest.mark.parametrize("M,K,N", [(1, 64, 8), (1000, 64, 8), (1000, 72, 6), (500, 77, 13), (300, 64, 32), (200, 520, 1), (40000, 40, 29),
-                                   (700, 9, 5)])
+                                   (700, 9, 5), (2, 20000, 30), (130, 1001, 9)])
 def test_linear_gradients_of_few_columns_round_once(M, K, N, dtype, size):
     """Up to 32 columns of fp32 gradients (the parameters'): dz in two parts of 16 bits leaves u(t)^2 of
     it (and in fp16 a part's last bits, 2^-39 of the largest), and dx and dW have one rounding, their own."""
