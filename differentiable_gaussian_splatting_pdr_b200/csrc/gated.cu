@@ -15,9 +15,9 @@
 // In fp16 dg and du are taken times a power of two that fits their bound, as dz in
 // linear.cu: |dg| and |du| are at most 1.13 max |dh| D max |x| max |w| (k_largest over the
 // four).  The bound is loose by some 2^7, and 2^-28 of it still a normal number.
-// (16384 x 256 to 1024: 85 us, without the factor 76.)
-// 65536 x 256 to 1024 in bf16: 61 us (74 under the power cap that a long run meets; 1120 and
-// 929 TFLOP/s); the backward of 16384 rows 69 us.
+// (16384 x 256 to 1024 with a cold L2: 85 us, without the factor 76.)
+// 65536 x 256 to 1024 in bf16: 61 to 64 us (71 to 74 under the power cap that a long run meets;
+// 1100 and 950 TFLOP/s); the backward of 16384 rows 69 us.
 #include "gemm.cuh"
 
 namespace pdr {

@@ -15,8 +15,8 @@
 //            into one of the accumulators there (2 of 256 columns, 4 of fewer);
 //   warps 4..19 take finished accumulators to registers and run the
 //            epilogue, while the next tile's products run.
-// What the four epilogues compute is in gemm.cuh (GemmEpi).  524288 x 256 to 8 columns: 50 us,
-// 6.1 TB/s; 4096 x 4096 x 4096 in bf16: 106 us, 1300 TFLOP/s, bound by the operands' way
+// What the four epilogues compute is in gemm.cuh (GemmEpi).  524288 x 256 to 8 columns: 49 us,
+// 6.2 TB/s; 4096 x 4096 x 4096 in bf16: 109 us, 1260 TFLOP/s, bound by the operands' way
 // from L2.
 #include <stdint.h>
 #include <string.h>
@@ -1262,8 +1262,8 @@ ColumnPlan column_plan(long long M, int N, int bytes) {
 // What rounding v to r leaves (an infinity stays one).
 __device__ __forceinline__ float rest(float v, float r) { return fabsf(r) <= 3.402823466e38f ? v - r : 0.0f; }
 
-// (Backward of 131072 x 256 to 256 columns, bf16 and a bias: 73 us, by single elements 162;
-// of 30000 x 256 to 777 columns, whose rows start anywhere, 63 and 101.)
+// (Backward of 131072 x 256 to 256 columns, bf16 and a bias: 83 us with a cold L2, by single elements
+// 180; of 30000 x 256 to 777 columns, whose rows start anywhere, 69 and 110.)
 template <typename T>
 __global__ void __launch_bounds__(256) k_cast_columns(const T *__restrict__ dy, int dy_dtype,
                                                       long long M, int N, ColumnPlan p,

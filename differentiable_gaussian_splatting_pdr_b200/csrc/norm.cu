@@ -459,8 +459,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // Threads per row, block size and blocks for M rows of D elements.  Rows of more than
 // 1024 elements have a block each, as many blocks as `per_sm` threads an SM make
-// (with powers of two for T and blocks of 256, 512 or 1024 threads 73416 x 1152 to 8 bits took
-// 104 us against 73, 17708 x 4170 189 against 89, the backward of 30114 x 2304 144 against 109).
+// (with powers of two for T and blocks of 256, 512 or 1024 threads 73416 x 1152 bf16 to 8 bits
+// took 109 us against 80 with a cold L2, 17708 x 4170 195 against 94, the backward of 30114 x 2304 132 against
+// 95; that of 60000 x 777, with 64 threads a row either way, 108 against 112).
 struct NormShape {
     bool shift;
     int T, threads, blocks;

@@ -380,7 +380,8 @@ pdr_status pdr_gated_bwd(const void *grad, const void *x, const void *w_gate, co
  * wanted; it must be NULL without a residual) and y, of `dtype` or PDR_E4M3.
  * The norm is taken of the fp32 sum before it is rounded to `sum`.  PDR_E4M3:
  * y stands for y * y_scale[m], y_scale[m] = max(max |row| / 448, 2^-126); a
- * row with a NaN or an infinity has a NaN or infinite scale. */
+ * row with a NaN or an infinity has a NaN or infinite scale.  eps = 0 is taken:
+ * a row of zeros is 0 / 0 then, here and in the gradients. */
 pdr_status pdr_rms_norm_fwd(const void *x, const void *residual, int dtype, const void *weight,
                             int weight_dtype, float eps, int M, int D, void *sum, void *y,
                             int y_dtype, float *y_scale, void *stream);
