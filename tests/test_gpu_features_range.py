@@ -389,3 +389,67 @@ def test_8_bits_over_many_tiles(M, K, N):
     a = act(g, "silu")[0]
     h = F.gated_fwd(x, wg, wu, x_scale=xs, gate_scale=gs, up_scale=us)
     close(h, a * u, value_error(g, eg, "silu") * (u.abs() + eu) + a.abs() * eu + STEP * (a * u).abs(), BF16, "h")
+
+
+# ---- replayed, and with given workspaces --------------------------------------------
+
+
+def backward_calls(gen):
+    x, w, wu, b = rand(gen, (333, 77), F16), rand(gen, (45, 77), F16, 0.1), rand(gen, (45, 77), F16, 0.1), rand(gen, (45,), F32)
+    g32, g6, g16 = rand(gen, (333, 45), F32), rand(gen, (333, 6), F32), rand(gen, (333, 45), F16)
+    head = w[:6].contiguous()
+    calls = [lambda: F.linear_bwd(g32, x, w, b), lambda: F.linear_bwd(g6, x, head, b[:6].contiguous()), lambda: F.linear_bwd(g16, x, w, b, "silu"),
+             lambda: F.linear_bwd(g32, x, w, b, "gelu"), lambda: F.gated_bwd(g16, x, w, wu)]
+    return (g32, g6, g16), calls
+
+
+def test_captured_gradients_fit_their_factor_to_each_replay():
+    """The power of two comes from the gradients of the replay, not of the capture; two graphs share a pool."""
+    grads, calls = backward_calls(generator(12))
+    clean = [g.clone() for g in grads]
+    for c in calls:
+        c()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, pool=graphs[0].pool() if graphs else None):
+            outs.append([t for c in calls for t in c()])
+        graphs.append(graph)
+    for size in (1.0, 2.0 ** -12, 2.0 ** 8):
+        for g, c in zip(grads, clean):
+            g.copy_(c * size)
+        want = [t for c in calls for t in c()]
+        for graph, out in zip(graphs, outs):
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, e in zip(out, want):
+                assert torch.equal(a, e)
+
+
+def test_workspaces_full_of_nan_change_nothing():
+    from differentiable_gaussian_splatting_pdr_b200 import _lib
+    lib, stream = _lib.load(), torch.cuda.current_stream().cuda_stream
+    gen = generator(13)
+    ws = torch.empty(64 << 20, device="cuda", dtype=torch.uint8)
+    acts = ["none", "relu", "silu", "gelu", "gelu_tanh"]
+    code = {F32: 0, F16: 1, BF16: 2}
+    for M, K, N, dt, gdt, act_ in [(333, 77, 6, F16, F32, 0), (129, 64, 29, BF16, F32, 0), (70, 9, 1, F16, F32, 0), (200, 72, 40, F16, F16, 3),
+                                   (200, 72, 45, F16, F32, 0), (100, 64, 33, F16, BF16, 2)]:
+        x, w, b, g = rand(gen, (M, K), dt), rand(gen, (N, K), dt), rand(gen, (N,), F32), rand(gen, (M, N), gdt)
+        want = F.linear_bwd(g, x, w, b, acts[act_])
+        got = [torch.full_like(t, 7) for t in want]
+        ws.fill_(255)
+        assert lib.pdr_linear_bwd(g.data_ptr(), code[gdt], x.data_ptr(), w.data_ptr(), code[dt], b.data_ptr(), 0, act_, M, N, K,
+                                  *(t.data_ptr() for t in got), ws.data_ptr(), ws.numel(), stream) == 0
+        for a, e in zip(got, want):
+            assert torch.equal(a, e)
+        if gdt == dt:
+            wu = rand(gen, (N, K), dt)
+            want = F.gated_bwd(g, x, w, wu)
+            got = [torch.full_like(t, 7) for t in want]
+            ws.fill_(255)
+            assert lib.pdr_gated_bwd(g.data_ptr(), x.data_ptr(), w.data_ptr(), wu.data_ptr(), code[dt], 2, M, K, N,
+                                     *(t.data_ptr() for t in got), ws.data_ptr(), ws.numel(), stream) == 0
+            for a, e in zip(got, want):
+                assert torch.equal(a, e)
